@@ -25,6 +25,10 @@ __all__ = [
     "moonep_prefetch", "moonep_dispatch",
     "moonep_combine", "moonep_dispatch_staged", "moonep_combine_staged", "moonep_grouped_ffn",
     "moonep_grouped_ffn_backward", "moonep_reduce_grad", "moonep_strerror", "moonep_version", "EXPORTED",
+    "moonep_layer_norm", "moonep_layer_norm_workspace_bytes", "moonep_layer_norm_backward",
+    "GradList", "moonep_grad_norm_workspace_bytes", "moonep_grad_norm", "moonep_grad_clip",
+    "W4_MAX_PAIRS", "moonep_w4_code_bytes", "moonep_w4_scale_bytes", "moonep_quantize_w4",
+    "moonep_w4_ffn_workspace_bytes", "moonep_w4_ffn",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoonep.so")
@@ -45,10 +49,15 @@ STAT_NAMES = (
     "reserved14", "reserved15",
 )
 NOALLOC_WS_BYTES = 8 << 20     # static plan workspace of moonep_plan_noalloc, per GPU
+W4_MAX_PAIRS = 8192            # (token, k) pairs of one moonep_w4_ffn call, at most
 EXPORTED = (
     "moonep_plan_workspace_bytes", "moonep_plan", "moonep_plan_noalloc", "moonep_prefetch", "moonep_dispatch",
     "moonep_combine", "moonep_dispatch_staged", "moonep_combine_staged", "moonep_grouped_ffn",
     "moonep_grouped_ffn_backward", "moonep_reduce_grad", "moonep_strerror", "moonep_version",
+    "moonep_layer_norm", "moonep_layer_norm_workspace_bytes", "moonep_layer_norm_backward",
+    "moonep_grad_norm_workspace_bytes", "moonep_grad_norm", "moonep_grad_clip",
+    "moonep_w4_code_bytes", "moonep_w4_scale_bytes", "moonep_quantize_w4",
+    "moonep_w4_ffn_workspace_bytes", "moonep_w4_ffn",
 )
 
 
@@ -102,6 +111,23 @@ def _load():
     for n in ("moonep_plan", "moonep_plan_noalloc", "moonep_prefetch", "moonep_dispatch", "moonep_combine",
               "moonep_dispatch_staged", "moonep_combine_staged", "moonep_grouped_ffn",
               "moonep_grouped_ffn_backward", "moonep_reduce_grad"):
+        getattr(L, n).restype = I32
+    F32, N32 = ctypes.c_float, ctypes.c_int32
+    L.moonep_layer_norm.argtypes = [P, VP, VP, VP, F32, VP, VP, VP, VP]
+    L.moonep_layer_norm_workspace_bytes.argtypes = [P]
+    L.moonep_layer_norm_backward.argtypes = [P] + [VP] * 10
+    L.moonep_grad_norm_workspace_bytes.argtypes = [N32]
+    L.moonep_grad_norm.argtypes = [N32] + [VP] * 6
+    L.moonep_grad_clip.argtypes = [N32] + [VP] * 4 + [F32, VP]
+    L.moonep_w4_code_bytes.argtypes = L.moonep_w4_scale_bytes.argtypes = [N32, N32]
+    L.moonep_quantize_w4.argtypes = [N32, N32, N32] + [VP] * 4
+    L.moonep_w4_ffn_workspace_bytes.argtypes = [P]
+    L.moonep_w4_ffn.argtypes = [P] + [VP] * 10
+    for n in ("moonep_layer_norm_workspace_bytes", "moonep_grad_norm_workspace_bytes", "moonep_w4_code_bytes",
+              "moonep_w4_scale_bytes", "moonep_w4_ffn_workspace_bytes"):
+        getattr(L, n).restype = SZ
+    for n in ("moonep_layer_norm", "moonep_layer_norm_backward", "moonep_grad_norm", "moonep_grad_clip",
+              "moonep_quantize_w4", "moonep_w4_ffn"):
         getattr(L, n).restype = I32
     L.moonep_strerror.argtypes = [I32]
     L.moonep_strerror.restype = ctypes.c_char_p
@@ -354,3 +380,149 @@ def moonep_reduce_grad(d: Dims, plan_ws, dw13_home, dw2_home, dw13_red, dw2_red,
         _ptr(dw2_red, "dw2_red", f32, (d.R, d.B, d.I, d.H), optional=nb),
     )
     _check(_lib().moonep_reduce_grad(ctypes.byref(d), *args, _stream(stream)), "moonep_reduce_grad")
+
+
+# ----------------------------------------------------------------------------
+# round the layer: norm, gradient clipping, decoding with 4-bit experts
+# ----------------------------------------------------------------------------
+
+def moonep_layer_norm(d: Dims, x, weight, bias, eps, y, mean=None, rstd=None, stream=None) -> None:
+    """y = layer norm of the [R, S, H] rows x.  weight, bias [H] float32 or None; mean, rstd [R*S]
+    float32, for the backward, or both None."""
+    f32, rt = _torch().float32, _rows_dtype(d)
+    args = (
+        _ptr(x, "x", rt, (d.R, d.S, d.H)),
+        _ptr(weight, "weight", f32, (d.H,), optional=True),
+        _ptr(bias, "bias", f32, (d.H,), optional=True),
+        float(eps),
+        _ptr(y, "y", rt, (d.R, d.S, d.H)),
+        _ptr(mean, "mean", f32, (d.R * d.S,), optional=True),
+        _ptr(rstd, "rstd", f32, (d.R * d.S,), optional=True),
+    )
+    _check(_lib().moonep_layer_norm(ctypes.byref(d), *args, _stream(stream)), "moonep_layer_norm")
+
+
+def moonep_layer_norm_workspace_bytes(d: Dims) -> int:
+    return _bytes(_lib().moonep_layer_norm_workspace_bytes(ctypes.byref(d)), "moonep_layer_norm_workspace_bytes")
+
+
+def moonep_layer_norm_backward(d: Dims, dy, x, weight, mean, rstd, dx, dweight, dbias, ws=None, stream=None) -> None:
+    """dx, and the sums dweight and dbias [H] float32 over all rows (either may be None; ws too if both
+    are).  With GRAD_ACCUM the sums are added to what dweight and dbias hold."""
+    torch = _torch()
+    f32, rt = torch.float32, _rows_dtype(d)
+    sums = dweight is not None or dbias is not None
+    args = (
+        _ptr(dy, "dy", rt, (d.R, d.S, d.H)),
+        _ptr(x, "x", rt, (d.R, d.S, d.H)),
+        _ptr(weight, "weight", f32, (d.H,), optional=True),
+        _ptr(mean, "mean", f32, (d.R * d.S,)),
+        _ptr(rstd, "rstd", f32, (d.R * d.S,)),
+        _ptr(dx, "dx", rt, (d.R, d.S, d.H)),
+        _ptr(dweight, "dweight", f32, (d.H,), optional=True),
+        _ptr(dbias, "dbias", f32, (d.H,), optional=True),
+        _ptr(ws, "ws", torch.uint8, numel=moonep_layer_norm_workspace_bytes(d), optional=not sums),
+    )
+    _check(_lib().moonep_layer_norm_backward(ctypes.byref(d), *args, _stream(stream)), "moonep_layer_norm_backward")
+
+
+class GradList:
+    """The gradients that moonep_grad_norm and moonep_grad_clip work on: contiguous float32 or bf16
+    GPU tensors of any shape, made once and used step after step.  It keeps the tensors; every call
+    takes their addresses of that moment."""
+
+    def __init__(self, tensors):
+        torch = _torch()
+        types = {torch.float32: 0, torch.bfloat16: 1}
+        self.tensors = tuple(tensors)
+        for i, t in enumerate(self.tensors):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"gradient {i} must be a torch.Tensor")
+            if t.dtype not in types:
+                raise ValueError(f"gradient {i} must be float32 or bfloat16, got {t.dtype}")
+            _ptr(t, f"gradient {i}")
+        n = len(self.tensors)
+        self.n = n
+        self.device = self.tensors[0].device if n else None
+        self._numel = [t.numel() for t in self.tensors]
+        self._c_numel = (ctypes.c_int64 * n)(*self._numel)
+        self._c_dtype = (ctypes.c_int32 * n)(*(types[t.dtype] for t in self.tensors))
+
+    def _arrays(self):
+        torch = _torch()
+        if self.n and self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the gradients are on {self.device}; the library runs on the current device "
+                             f"cuda:{torch.cuda.current_device()}")
+        if [t.numel() if t.is_contiguous() else -1 for t in self.tensors] != self._numel:
+            raise ValueError("a gradient changed its size or layout since the list was made")
+        at = (ctypes.c_void_p * self.n)(*[t.data_ptr() for t in self.tensors])
+        return self.n, at, self._c_numel, self._c_dtype
+
+
+def moonep_grad_norm_workspace_bytes(grads: GradList) -> int:
+    return _bytes(_lib().moonep_grad_norm_workspace_bytes(grads.n), "moonep_grad_norm_workspace_bytes")
+
+
+def moonep_grad_norm(grads: GradList, ws, norm, stream=None) -> None:
+    """norm[0] (float32) = the 2-norm of all gradients together."""
+    torch = _torch()
+    ws = _ptr(ws, "ws", torch.uint8, numel=moonep_grad_norm_workspace_bytes(grads))
+    norm = _ptr(norm, "norm", torch.float32, (1,))
+    _check(_lib().moonep_grad_norm(*grads._arrays(), ws, norm, _stream(stream)), "moonep_grad_norm")
+
+
+def moonep_grad_clip(grads: GradList, norm, max_norm, stream=None) -> None:
+    """Scales the gradients in place by max_norm / norm[0] where norm[0] is larger than max_norm."""
+    norm = _ptr(norm, "norm", _torch().float32, (1,))
+    _check(_lib().moonep_grad_clip(*grads._arrays(), norm, float(max_norm), _stream(stream)), "moonep_grad_clip")
+
+
+def _bytes(n: int, where: str) -> int:
+    if n == 0:
+        raise MoonEPError(-1, where)
+    return int(n)
+
+
+def moonep_w4_code_bytes(Kin: int, N: int) -> int:
+    return _bytes(_lib().moonep_w4_code_bytes(Kin, N), "moonep_w4_code_bytes")
+
+
+def moonep_w4_scale_bytes(Kin: int, N: int) -> int:
+    return _bytes(_lib().moonep_w4_scale_bytes(Kin, N), "moonep_w4_scale_bytes")
+
+
+def moonep_quantize_w4(w, codes, scales, stream=None) -> None:
+    """Quantises w [E, Kin, N] bf16 to 4 bits: codes [E, moonep_w4_code_bytes(Kin, N)] and scales
+    [E, moonep_w4_scale_bytes(Kin, N)], both uint8."""
+    torch = _torch()
+    pw = _ptr(w, "w", torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError(f"w must have shape (E, Kin, N), got {tuple(w.shape)}")
+    E, Kin, N = w.shape
+    args = (pw, _ptr(codes, "codes", torch.uint8, (E, moonep_w4_code_bytes(Kin, N))),
+            _ptr(scales, "scales", torch.uint8, (E, moonep_w4_scale_bytes(Kin, N))))
+    _check(_lib().moonep_quantize_w4(E, Kin, N, *args, _stream(stream)), "moonep_quantize_w4")
+
+
+def moonep_w4_ffn_workspace_bytes(d: Dims) -> int:
+    return _bytes(_lib().moonep_w4_ffn_workspace_bytes(ctypes.byref(d)), "moonep_w4_ffn_workspace_bytes")
+
+
+def moonep_w4_ffn(d: Dims, topk, gates, x, w13_codes, w13_scales, w2_codes, w2_scales, ws, out, stream=None) -> None:
+    """out [R, S, H] = the gated sum of each token's experts' FFN, weights in 4 bits (moonep_quantize_w4
+    of w13 [E, H, 2I] and w2 [E, I, H]).  Ids outside [0, E) add nothing."""
+    torch = _torch()
+    u8, bf = torch.uint8, torch.bfloat16
+    wsb = moonep_w4_ffn_workspace_bytes(d)
+    args = (
+        _ptr(topk, "topk", torch.int32, (d.R, d.S, d.K)),
+        _ptr(gates, "gates", torch.float32, (d.R, d.S, d.K)),
+        _ptr(x, "x", bf, (d.R, d.S, d.H)),
+        _ptr(w13_codes, "w13_codes", u8, (d.E, moonep_w4_code_bytes(d.H, 2 * d.I))),
+        _ptr(w13_scales, "w13_scales", u8, (d.E, moonep_w4_scale_bytes(d.H, 2 * d.I))),
+        _ptr(w2_codes, "w2_codes", u8, (d.E, moonep_w4_code_bytes(d.I, d.H))),
+        _ptr(w2_scales, "w2_scales", u8, (d.E, moonep_w4_scale_bytes(d.I, d.H))),
+        _ptr(ws, "ws", u8, numel=wsb),
+        _ptr(out, "out", bf, (d.R, d.S, d.H)),
+    )
+    _check(_lib().moonep_w4_ffn(ctypes.byref(d), *args, _stream(stream)), "moonep_w4_ffn")

@@ -1,0 +1,190 @@
+// The global norm of many gradients, and clipping by it.
+//
+// Both are streams over memory: the norm reads every gradient once, clipping reads and writes it
+// once (or leaves it alone where the norm is small enough).  The gradients' addresses travel in the
+// kernel arguments, kTable of them a launch, so a call needs no device table and can be captured.
+#include "common.h"
+
+#include <cmath>
+#include <new>
+#include <vector>
+
+namespace moonep {
+
+constexpr int kTable = 160;          // gradients a launch: 20 bytes each, within 4 KiB of arguments
+constexpr int kSpan = 16384;         // elements a workgroup takes at a time
+constexpr int kNormBlocks = 1024;    // workgroups (and partial sums) a launch, at most
+
+struct GradTable {
+    uint64_t at[kTable];             // address; bit 0: the type
+    int64_t numel[kTable];
+    int32_t first[kTable + 1];       // spans before gradient i
+    int32_t n;
+};
+static_assert(sizeof(GradTable) <= 3584, "kernel arguments");
+
+// The gradient that span c is of.
+__device__ __forceinline__ int find_grad(const GradTable& t, int c) {
+    int lo = 0, hi = t.n;            // first[lo] <= c < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.first[mid] <= c) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double sq(float f) { return (double)f * (double)f; }
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double lds[4];
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// part[block] = sum of squares of the block's spans, in float64.
+__global__ __launch_bounds__(256) void grad_squares_kernel(GradTable t, double* __restrict__ part) {
+    double s = 0.0;
+    const int spans = t.first[t.n];
+    for (int c = blockIdx.x; c < spans; c += gridDim.x) {
+        const int i = find_grad(t, c);
+        const int64_t lo = (int64_t)(c - t.first[i]) * kSpan;
+        const int n = (int)std::min<int64_t>(kSpan, t.numel[i] - lo);
+        const uint64_t at = t.at[i];
+        if (at & MOONEP_GRAD_BF16) {
+            const uint16_t* g = reinterpret_cast<const uint16_t*>(at & ~1ull) + lo;
+            for (int j = threadIdx.x; j < n; j += 256) s += sq(__uint_as_float((uint32_t)g[j] << 16));
+        } else {
+            const float* g = reinterpret_cast<const float*>(at) + lo;
+            for (int j = threadIdx.x; j < n; j += 256) s += sq(g[j]);
+        }
+    }
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(256) void grad_join_kernel(const double* __restrict__ part, int n,
+                                                        float* __restrict__ norm) {
+    double s = 0.0;
+    for (int j = threadIdx.x; j < n; j += 256) s += part[j];
+    s = block_sum(s);
+    if (threadIdx.x == 0) norm[0] = (float)sqrt(s);
+}
+
+__global__ __launch_bounds__(256) void grad_clip_kernel(GradTable t, const float* __restrict__ norm, float most) {
+    const float s = norm[0];
+    if (s <= most) return;
+    const float f = most / s;        // NaN for a NaN norm, 0 for an infinite one
+    const int spans = t.first[t.n];
+    for (int c = blockIdx.x; c < spans; c += gridDim.x) {
+        const int i = find_grad(t, c);
+        const int64_t lo = (int64_t)(c - t.first[i]) * kSpan;
+        const int n = (int)std::min<int64_t>(kSpan, t.numel[i] - lo);
+        const uint64_t at = t.at[i];
+        if (at & MOONEP_GRAD_BF16) {
+            uint16_t* g = reinterpret_cast<uint16_t*>(at & ~1ull) + lo;
+            for (int j = threadIdx.x; j < n; j += 256)
+                g[j] = (uint16_t)pack_bf16(__uint_as_float((uint32_t)g[j] << 16) * f, 0.0f);
+        } else {
+            float* g = reinterpret_cast<float*>(at) + lo;
+            for (int j = threadIdx.x; j < n; j += 256) g[j] *= f;
+        }
+    }
+}
+
+static int check_grads(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dtype) {
+    if (n < 0 || (n > 0 && (!grads || !numel || !dtype))) return MOONEP_EINVAL;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        if (numel[i] < 0 || numel[i] > (int64_t)1 << 40) return MOONEP_EINVAL;
+        if (dtype[i] != MOONEP_GRAD_F32 && dtype[i] != MOONEP_GRAD_BF16) return MOONEP_EINVAL;
+        if (numel[i] == 0) continue;
+        MOONEP_CHECK_PTR(grads[i]);
+        total += (numel[i] + kSpan - 1) / kSpan;
+    }
+    return total > 0x7fffffff ? MOONEP_EINVAL : MOONEP_OK;
+}
+
+// Calls launch(table, workgroups) for every kTable gradients that hold something.
+template <class F>
+static int for_tables(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dtype, F launch) {
+    for (int i = 0; i < n;) {
+        GradTable t{};
+        for (; i < n && t.n < kTable; ++i) {
+            if (numel[i] == 0) continue;
+            t.at[t.n] = reinterpret_cast<uint64_t>(grads[i]) | (uint64_t)dtype[i];
+            t.numel[t.n] = numel[i];
+            t.first[t.n + 1] = t.first[t.n] + (int32_t)((numel[i] + kSpan - 1) / kSpan);
+            ++t.n;
+        }
+        if (t.n == 0) break;
+        launch(t, std::min(t.first[t.n], kNormBlocks));
+        if (hipGetLastError() != hipSuccess) return MOONEP_EHIP;
+    }
+    return MOONEP_OK;
+}
+
+// Whether two of the gradients share memory.
+static bool overlap(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dtype) {
+    auto begin = [&](int i) { return reinterpret_cast<uintptr_t>(grads[i]); };
+    auto end = [&](int i) { return begin(i) + (uintptr_t)numel[i] * (dtype[i] == MOONEP_GRAD_BF16 ? 2 : 4); };
+    std::vector<int32_t> order;
+    order.reserve(n);
+    bool sorted = true;
+    for (int i = 0; i < n; ++i) {
+        if (numel[i] == 0) continue;
+        sorted = sorted && (order.empty() || begin(order.back()) <= begin(i));
+        order.push_back(i);
+    }
+    if (!sorted) std::sort(order.begin(), order.end(), [&](int a, int b) { return begin(a) < begin(b); });
+    for (size_t j = 1; j < order.size(); ++j)
+        if (end(order[j - 1]) > begin(order[j])) return true;
+    return false;
+}
+
+}  // namespace moonep
+
+using namespace moonep;
+
+extern "C" size_t moonep_grad_norm_workspace_bytes(int32_t n) {
+    if (n < 0) return 0;
+    return (size_t)((n + (int64_t)kTable - 1) / kTable + (n == 0)) * kNormBlocks * sizeof(double);
+}
+
+extern "C" int moonep_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                                void* ws, float* norm, void* stream) {
+    int rc = check_grads(n, grads, numel, dtype);
+    if (rc != MOONEP_OK) return rc;
+    MOONEP_CHECK_PTR(ws);
+    MOONEP_CHECK_PTR(norm);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    double* part = static_cast<double*>(ws);
+    int parts = 0;
+    rc = for_tables(n, grads, numel, dtype, [&](const GradTable& t, int blocks) {
+        hipLaunchKernelGGL(grad_squares_kernel, dim3(blocks), dim3(256), 0, s, t, part + parts);
+        parts += blocks;
+    });
+    if (rc != MOONEP_OK) return rc;
+    hipLaunchKernelGGL(grad_join_kernel, dim3(1), dim3(256), 0, s, part, parts, norm);
+    MOONEP_LAUNCH_CHECK();
+    return MOONEP_OK;
+}
+
+extern "C" int moonep_grad_clip(int32_t n, void* const* grads, const int64_t* numel, const int32_t* dtype,
+                                const float* norm, float max_norm, void* stream) {
+    const int rc = check_grads(n, grads, numel, dtype);
+    if (rc != MOONEP_OK) return rc;
+    if (!(max_norm >= 0.0f)) return MOONEP_EINVAL;
+    MOONEP_CHECK_PTR(norm);
+    try {
+        if (overlap(n, grads, numel, dtype)) return MOONEP_EINVAL;
+    } catch (const std::bad_alloc&) {
+        return MOONEP_EINVAL;
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return for_tables(n, grads, numel, dtype, [&](const GradTable& t, int blocks) {
+        hipLaunchKernelGGL(grad_clip_kernel, dim3(blocks), dim3(256), 0, s, t, norm, max_norm);
+    });
+}

@@ -14,9 +14,12 @@ from __future__ import annotations
 
 import torch
 
-from . import (Dims, moonep_combine, moonep_dispatch, moonep_grouped_ffn,
-               moonep_grouped_ffn_backward, moonep_plan, moonep_plan_workspace_bytes,
-               moonep_prefetch, moonep_reduce_grad, NSTATS)
+from . import (Dims, GradList, moonep_combine, moonep_dispatch, moonep_grad_clip, moonep_grad_norm,
+               moonep_grad_norm_workspace_bytes, moonep_grouped_ffn, moonep_grouped_ffn_backward,
+               moonep_layer_norm, moonep_layer_norm_backward, moonep_layer_norm_workspace_bytes,
+               moonep_plan, moonep_plan_workspace_bytes, moonep_prefetch, moonep_quantize_w4,
+               moonep_reduce_grad, moonep_w4_code_bytes, moonep_w4_ffn, moonep_w4_ffn_workspace_bytes,
+               moonep_w4_scale_bytes, NSTATS)
 
 
 def _slot_shapes(R, B, H, I):
@@ -69,9 +72,17 @@ class MoonEPLayer:
     ``w13`` [E, H, 2I] and ``w2`` [E, I, H] are the home expert weights (bf16, on the
     device).  With ``I == 0`` the layer has no expert FFN (identity experts): only
     planning, dispatch and combine run.
+
+    With ``norm_weight`` [H] (float32; ``norm_bias`` [H] or None) the rows are layer-normed before
+    they are dispatched, and ``backward`` returns the gradient of the rows before the norm; it also
+    writes ``dnorm_weight`` and ``dnorm_bias``.  A router that reads the normed rows calls ``norm(x)``
+    itself; ``forward`` given what that returned does not norm again.
     """
 
-    def __init__(self, dims: Dims, w13=None, w2=None, training: bool = False, device="cuda", pool=None):
+    def __init__(self, dims: Dims, w13=None, w2=None, training: bool = False, device="cuda", pool=None,
+                 norm_weight=None, norm_bias=None, norm_eps: float = 1e-5):
+        if norm_bias is not None and norm_weight is None:
+            raise ValueError("norm_bias needs norm_weight")
         self.d = dims
         self.training = training
         self.pool = pool
@@ -88,6 +99,18 @@ class MoonEPLayer:
         self.recv = torch.empty((M, H), dtype=rt, device=dev)
         self.out = torch.empty((R, S, H), dtype=rt, device=dev)
         self.w13, self.w2 = w13, w2
+        self.norm_weight, self.norm_bias, self.norm_eps = norm_weight, norm_bias, norm_eps
+        if norm_weight is not None:
+            f32 = torch.float32
+            self.normed = torch.empty((R, S, H), dtype=rt, device=dev)
+            self.mean = torch.empty((R * S,), dtype=f32, device=dev) if training else None
+            self.rstd = torch.empty((R * S,), dtype=f32, device=dev) if training else None
+            self.x = None         # the rows of the last norm(), which its backward reads
+            if training:
+                self.dnorm_weight = torch.zeros((H,), dtype=f32, device=dev)
+                self.dnorm_bias = torch.zeros((H,), dtype=f32, device=dev) if norm_bias is not None else None
+                self.norm_ws = torch.empty(moonep_layer_norm_workspace_bytes(dims), dtype=torch.uint8, device=dev)
+                self.dx_in = torch.empty((R, S, H), dtype=rt, device=dev)
         if I > 0:
             bf = torch.bfloat16
             if pool is not None:
@@ -116,6 +139,13 @@ class MoonEPLayer:
             self.y = self.recv          # identity experts
 
     # -- steps ---------------------------------------------------------------
+    def norm(self, x):
+        """Layer norm of the rows [R, S, H]; x must stay as it is until the backward."""
+        moonep_layer_norm(self.d, x, self.norm_weight, self.norm_bias, self.norm_eps, self.normed, self.mean,
+                          self.rstd)
+        self.x = x
+        return self.normed
+
     def plan(self, topk):
         moonep_plan(self.d, topk, self.ws, self.cu, self.dest, self.stats)
 
@@ -138,6 +168,8 @@ class MoonEPLayer:
 
     def forward(self, x, topk, gates):
         """Returns the [R, S, H] output (a view of a static buffer, replaced by the next call)."""
+        if self.norm_weight is not None and x.data_ptr() != self.normed.data_ptr():
+            x = self.norm(x)
         self.plan(topk)
         self.prefetch()
         self.dispatch(x)
@@ -159,4 +191,83 @@ class MoonEPLayer:
                                     self.dw13, self.dw2, self.dw13_red, self.dw2_red)
         moonep_combine(self.d, self.dest, self.drecv, None, self.dx)
         moonep_reduce_grad(self.d, self.ws, self.dw13, self.dw2, self.dw13_red, self.dw2_red)
-        return self.dx
+        if self.norm_weight is None:
+            return self.dx
+        moonep_layer_norm_backward(self.d, self.dx, self.x, self.norm_weight, self.mean, self.rstd, self.dx_in,
+                                   self.dnorm_weight, self.dnorm_bias, self.norm_ws)
+        return self.dx_in
+
+    # -- round the step --------------------------------------------------------
+    def grads(self) -> list:
+        """The weights' gradients that backward() leaves behind."""
+        norm = [self.dnorm_weight, self.dnorm_bias] if self.norm_weight is not None else []
+        return [g for g in [self.dw13, self.dw2, *norm] if g is not None]
+
+    def decoder(self, max_tokens: int) -> "W4Experts":
+        """The same norm and experts for decoding, with 4-bit weights made from the present ones."""
+        return W4Experts(self.w13, self.w2, self.d.K, max_tokens, self.norm_weight, self.norm_bias, self.norm_eps)
+
+
+class GradClipper:
+    """Clips the gradients of one or more layers by their global norm."""
+
+    def __init__(self, layers):
+        self.list = GradList(g for layer in layers for g in layer.grads())
+        dev = self.list.device
+        self.ws = torch.empty(moonep_grad_norm_workspace_bytes(self.list), dtype=torch.uint8, device=dev)
+        self.norm = torch.empty((1,), dtype=torch.float32, device=dev)
+
+    def clip(self, max_norm):
+        """Scales the gradients so that their norm is at most max_norm; returns the norm they had, a
+        [1] float32 tensor on the GPU (a static buffer, replaced by the next call)."""
+        moonep_grad_norm(self.list, self.ws, self.norm)
+        moonep_grad_clip(self.list, self.norm, max_norm)
+        return self.norm
+
+
+class W4Experts:
+    """A layer's experts for decoding: up to max_tokens tokens a call, weights in 4 bits.
+
+    ``w13`` [E, H, 2I] and ``w2`` [E, I, H] bf16 are quantised here, once, and not kept.  All buffers
+    are static, so a call can be captured; a call replaces the output of the one before.
+    """
+
+    def __init__(self, w13, w2, K: int, max_tokens: int, norm_weight=None, norm_bias=None, norm_eps: float = 1e-5):
+        E, H, I = w13.shape[0], w13.shape[1], w2.shape[1]
+        dev, u8 = w13.device, torch.uint8
+        self.E, self.H, self.I, self.K, self.max_tokens = E, H, I, K, max_tokens
+        self.norm_weight, self.norm_bias, self.norm_eps = norm_weight, norm_bias, norm_eps
+        self.packed = []
+        for w, kin, n in ((w13, H, 2 * I), (w2, I, H)):
+            codes = torch.empty((E, moonep_w4_code_bytes(kin, n)), dtype=u8, device=dev)
+            scales = torch.empty((E, moonep_w4_scale_bytes(kin, n)), dtype=u8, device=dev)
+            moonep_quantize_w4(w, codes, scales)
+            self.packed += [codes, scales]
+        self.ws = torch.empty(moonep_w4_ffn_workspace_bytes(self._dims(max_tokens)), dtype=u8, device=dev)
+        self.normed = torch.empty((max_tokens, H), dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty((max_tokens, H), dtype=torch.bfloat16, device=dev)
+
+    def _dims(self, T):
+        return Dims.make(1, self.E, 0, T, self.K, self.H, self.I)
+
+    def norm(self, x):
+        """Layer norm of the tokens x [T, H] (a view of a static buffer)."""
+        T = x.shape[0]
+        d = Dims.make(1, 1, 0, T, 1, self.H)
+        moonep_layer_norm(d, x.unsqueeze(0), self.norm_weight, self.norm_bias, self.norm_eps,
+                          self.normed[:T].unsqueeze(0))
+        return self.normed[:T]
+
+    def forward(self, x, topk, gates):
+        """x [T, H] bf16 (before the norm, or what norm(x) returned), topk [T, K] int32 (-1: nothing),
+        gates [T, K] float32 -> [T, H] bf16 (a view of a static buffer)."""
+        T = x.shape[0]
+        if not 1 <= T <= self.max_tokens:
+            raise ValueError(f"{T} tokens: this decoder takes 1 to {self.max_tokens}")
+        if self.norm_weight is not None and x.data_ptr() != self.normed.data_ptr():
+            x = self.norm(x)
+        d = self._dims(T)
+        ws = self.ws[:moonep_w4_ffn_workspace_bytes(d)]
+        out = self.out[:T]
+        moonep_w4_ffn(d, topk.unsqueeze(0), gates.unsqueeze(0), x.unsqueeze(0), *self.packed, ws, out.unsqueeze(0))
+        return out

@@ -236,6 +236,107 @@ int moonep_reduce_grad(const moonep_dims_t* dims, const void* plan_ws,
                        float* dw13_home, float* dw2_home, float* dw13_red, float* dw2_red,
                        void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Round the layer: the norm in front of it, gradient clipping behind it, and the experts in 4 bits
+ * for decoding.  The pages cover none of these; the formulas below are their definition.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Layer norm of the R*S rows of H elements: with m the mean and v the variance (divided by H) of a
+ * row, y = (x - m) * rstd * weight + bias, rstd = 1 / sqrt(v + eps).  Only R, S, H and the row type
+ * (MOONEP_F32_ROWS) of dims matter to it.  Statistics in float32, two passes (the variance is that
+ * of the centred row); y is rounded to nearest even once.
+ *   x      [R, S, H] bf16 (float32 with MOONEP_F32_ROWS)
+ *   weight [H] float32 or NULL (ones), bias [H] float32 or NULL (zeros)
+ *   eps    finite, >= 0.  With 0 a constant row gives NaN, as the formula does.
+ *   y      [R, S, H] out, same type as x
+ *   mean, rstd [R*S] float32 out, for the backward; both NULL if it is not needed
+ * A row that holds an infinity or a NaN gives NaN in its own row only.  y must not overlap x. */
+int moonep_layer_norm(const moonep_dims_t* dims, const void* x, const float* weight, const float* bias,
+                      float eps, void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of the scratch of moonep_layer_norm_backward (its contents need not be kept between calls;
+ * calls that may overlap need one each).  Pure host function.  Returns 0 for invalid dims. */
+size_t moonep_layer_norm_workspace_bytes(const moonep_dims_t* dims);
+
+/* Backward of moonep_layer_norm.  With n = (x - mean) * rstd and g = dy * weight, per row:
+ *   dx = rstd * (g - avg(g) - n * avg(g * n));   over all rows: dweight = sum dy * n, dbias = sum dy.
+ * Sums in float32, in an order that dims alone fix: the same bits every time.
+ *   dy     [R, S, H] type of the rows; x, weight, mean, rstd as in and from the forward
+ *   dx     [R, S, H] out, type of the rows
+ *   dweight, dbias [H] float32 out, or NULL where not needed.  Written, or with MOONEP_GRAD_ACCUM
+ *             added to what they hold.
+ *   ws     moonep_layer_norm_workspace_bytes() bytes; NULL if dweight and dbias are
+ * Outputs must not overlap inputs or each other. */
+int moonep_layer_norm_backward(const moonep_dims_t* dims, const void* dy, const void* x, const float* weight,
+                               const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                               void* ws, void* stream);
+
+/* Element types of the gradients of moonep_grad_norm and moonep_grad_clip. */
+#define MOONEP_GRAD_F32 0
+#define MOONEP_GRAD_BF16 1
+
+/* Bytes of the scratch of moonep_grad_norm for n gradients (same rules as above).  Pure host
+ * function.  Returns 0 for n < 0. */
+size_t moonep_grad_norm_workspace_bytes(int32_t n);
+
+/* Global norm of n gradients: norm[0] = sqrt(sum over all elements of g^2), squares and sums in
+ * float64 (no finite gradient overflows, none is lost to underflow), rounded once to float32; in an
+ * order that n and numel alone fix.  An infinity or a NaN in a gradient is one in the norm.
+ *   grads  host array [n] of device pointers; numel host array [n], each >= 0 (a pointer may be
+ *          NULL where it is 0); dtype host array [n] of MOONEP_GRAD_*.  The arrays are read before
+ *          the call returns.  n may be 0.
+ *   norm   [1] float32 out, on the device */
+int moonep_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dtype,
+                     void* ws, float* norm, void* stream);
+
+/* Clips n gradients in place by the norm on the device (of moonep_grad_norm, or one joined from
+ * several devices): g *= max_norm / norm where norm > max_norm, product in float32, rounded to
+ * nearest even; nothing is read or written where norm <= max_norm.  A NaN norm makes every gradient
+ * NaN, an infinite one makes finite elements 0.
+ *   max_norm  >= 0 (may be infinite)
+ *   other arguments as for moonep_grad_norm.  MOONEP_EINVAL if two gradients overlap: a shared
+ *   gradient would be scaled more than once. */
+int moonep_grad_clip(int32_t n, void* const* grads, const int64_t* numel, const int32_t* dtype,
+                     const float* norm, float max_norm, void* stream);
+
+/* 4-bit weights.  A matrix [Kin, N] (multiples of 32 both) is held as OCP Microscaling FP4: codes
+ * e2m1 (values 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives; sign in bit 3) and one scale byte s,
+ * worth 2^(s - 127), for each group of 32 values along Kin.  A scale byte of 255 makes its group NaN;
+ * 0 is not used.  Layout, chosen so that a wave's 16-byte loads are one KiB in a row, each lane's one
+ * group, and one 4-byte load brings a lane the scales of four of them:
+ *   codes  [N/16][ceil(Kin/128)][4 groups][16 columns][16 bytes]; byte b holds the group's values 2b
+ *          (low half) and 2b + 1; codes past Kin are 0
+ *   scales [N/16][ceil(Kin/512)][4 groups][16 columns][4 blocks of 128]; scales past Kin are 127
+ * These give one matrix's bytes; 0 for invalid sizes. */
+size_t moonep_w4_code_bytes(int32_t Kin, int32_t N);
+size_t moonep_w4_scale_bytes(int32_t Kin, int32_t N);
+
+/* Quantises E matrices: the scale of a group is 2^(floor(log2(largest magnitude)) - 2), at least 2^-126 (all
+ * that is zero or too small for it rounds from there); each value is divided by it and rounded to
+ * the nearest code, halfway to the even one, magnitudes over 6 to 6.  A group with an infinity or a
+ * NaN gets the scale byte 255.
+ *   w [E, Kin, N] bf16;  codes [E, moonep_w4_code_bytes()], scales [E, moonep_w4_scale_bytes()] out */
+int moonep_quantize_w4(int32_t E, int32_t Kin, int32_t N, const void* w, void* codes, void* scales, void* stream);
+
+/* The experts' SwiGLU FFN for decoded tokens, with 4-bit weights:
+ *   out[r,s] = sum over k (in k order) of gates[r,s,k] * ((silu(x G) * (x U)) D)  of expert topk[r,s,k],
+ * G | U the columns of its w13, D its w2.  Products in matrix instructions on exact bf16 weights
+ * (code times scale) with float32 accumulation; the activation is kept as two bf16 terms (16 bits or
+ * more); the result is rounded to nearest even once.  Needs no plan: dims' R, S, K, E, H and I count,
+ * the planner's limits on E/R and B do not apply.
+ *   topk  [R, S, K] int32: an id outside [0, E) adds nothing, whatever its gate (rows of ended
+ *         sequences: all ids -1, their output is zero); an id named twice counts twice
+ *   gates [R, S, K] float32;  x [R, S, H] bf16;  out [R, S, H] bf16 out
+ *   w13_codes, w13_scales: E matrices [H, 2I];  w2_codes, w2_scales: E matrices [I, H]
+ *   ws    moonep_w4_ffn_workspace_bytes() bytes, scratch (same rules as above)
+ * MOONEP_ENOTSUP if H or I is not a multiple of 32, with MOONEP_F32_ROWS, or if R*S*K is more than
+ * MOONEP_W4_MAX_PAIRS (such a batch is no longer bound by its weights: use moonep_grouped_ffn). */
+#define MOONEP_W4_MAX_PAIRS 8192
+size_t moonep_w4_ffn_workspace_bytes(const moonep_dims_t* dims);
+int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* gates, const void* x,
+                  const void* w13_codes, const void* w13_scales, const void* w2_codes, const void* w2_scales,
+                  void* ws, void* out, void* stream);
+
 /* Static description of an error code. */
 const char* moonep_strerror(int code);
 

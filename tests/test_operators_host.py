@@ -1,0 +1,165 @@
+"""The operators round the layer without a GPU: sizes, and everything that is refused on the host
+before a launch."""
+import ctypes
+
+import pytest
+
+import balanced_token_dispatch_moonep_amd as M
+
+EINVAL, EALIGN, ENOTSUP = -1, -2, -4
+VP = ctypes.c_void_p
+G, MIS = VP(0x10000), VP(0x10004)
+
+
+def _dims(**kw):
+    base = dict(R=1, E=32, B=0, S=8, K=8, H=7168, I=2048)
+    base.update(kw)
+    return M.Dims.make(**base)
+
+
+def _norm(d, x=G, w=G, b=G, eps=1e-5, y=G, mean=G, rstd=G):
+    return M.lib.moonep_layer_norm(ctypes.byref(d) if d else None, x, w, b, eps, y, mean, rstd, None)
+
+
+def test_norm_refuses():
+    d = _dims()
+    assert _norm(None) == EINVAL
+    assert _norm(_dims(H=1004)) == EINVAL
+    assert _norm(_dims(S=0)) == EINVAL
+    assert _norm(d, x=None) == EINVAL and _norm(d, y=None) == EINVAL
+    for eps in (-1e-5, float("nan"), float("inf")):
+        assert _norm(d, eps=eps) == EINVAL
+    assert _norm(d, mean=None) == EINVAL and _norm(d, rstd=None) == EINVAL
+    for name in ("x", "w", "b", "y", "mean", "rstd"):
+        assert _norm(d, **{name: MIS}) == EALIGN
+
+
+def test_norm_backward_refuses():
+    d = _dims()
+    names = ("dy", "x", "weight", "mean", "rstd", "dx", "dweight", "dbias", "ws")
+
+    def call(d=d, **kw):
+        a = [kw.get(n, G) for n in names]
+        return M.lib.moonep_layer_norm_backward(ctypes.byref(d), *a, None)
+
+    assert call(_dims(H=12)) == EINVAL
+    for n in ("dy", "x", "mean", "rstd", "dx", "ws"):
+        assert call(**{n: None}) == EINVAL
+    assert call(ws=None, dweight=None) == EINVAL
+    for n in names:
+        assert call(**{n: MIS}) == EALIGN
+
+
+def test_norm_workspace():
+    one, many = (M.moonep_layer_norm_workspace_bytes(_dims(S=s)) for s in (1, 1 << 15))
+    assert 2 * 7168 * 4 <= one < many < 64 << 20
+    assert M.lib.moonep_layer_norm_workspace_bytes(ctypes.byref(_dims(H=4))) == 0
+    assert M.lib.moonep_layer_norm_workspace_bytes(None) == 0
+
+
+def _grads(at, numel, dtype):
+    n = len(at)
+    return n, (VP * n)(*at), (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*dtype)
+
+
+def test_grad_norm_refuses():
+    f = M.lib.moonep_grad_norm
+    assert f(-1, None, None, None, G, G, None) == EINVAL
+    assert f(1, None, None, None, G, G, None) == EINVAL
+    ok = ([0x10000, 0x20000], [100, 100], [0, 1])
+    assert f(*_grads(*ok), None, G, None) == EINVAL
+    assert f(*_grads(*ok), G, None, None) == EINVAL
+    assert f(*_grads(*ok), MIS, G, None) == EALIGN
+    assert f(*_grads(*ok), G, MIS, None) == EALIGN
+    assert f(*_grads([0x10000, None], [100, 100], [0, 1]), G, G, None) == EINVAL
+    assert f(*_grads([0x10000, 0x20002], [100, 100], [0, 1]), G, G, None) == EALIGN
+    assert f(*_grads([0x10000, 0x20000], [100, -1], [0, 1]), G, G, None) == EINVAL
+    assert f(*_grads([0x10000, 0x20000], [100, 1 << 41], [0, 1]), G, G, None) == EINVAL
+    assert f(*_grads([0x10000, 0x20000], [100, 100], [0, 2]), G, G, None) == EINVAL
+    assert M.lib.moonep_grad_norm_workspace_bytes(-1) == 0
+    assert 0 < M.lib.moonep_grad_norm_workspace_bytes(0) <= M.lib.moonep_grad_norm_workspace_bytes(1000)
+
+
+def test_grad_clip_refuses():
+    f = M.lib.moonep_grad_clip
+    ok = ([0x10000, 0x20000], [100, 100], [0, 1])
+    for most in (-1.0, float("nan")):
+        assert f(*_grads(*ok), G, most, None) == EINVAL
+    assert f(*_grads(*ok), None, 1.0, None) == EINVAL
+    assert f(*_grads(*ok), MIS, 1.0, None) == EALIGN
+    # shared memory: the same gradient twice, one that reaches into another (in either order)
+    assert f(*_grads([0x10000, 0x10000], [100, 100], [0, 0]), G, 1.0, None) == EINVAL
+    assert f(*_grads([0x10000, 0x10190 - 16], [100, 4], [0, 0]), G, 1.0, None) == EINVAL
+    assert f(*_grads([0x20000, 0x10000], [4, 0x4001], [1, 0]), G, 1.0, None) == EINVAL
+    assert f(*_grads([0x30000, 0x20000, 0x10000], [4, 0x8001, 4], [1, 1, 0]), G, 1.0, None) == EINVAL
+
+
+def test_w4_sizes():
+    assert M.moonep_w4_code_bytes(7168, 4096) == 7168 * 4096 // 2
+    assert M.moonep_w4_scale_bytes(7168, 4096) == 7168 * 4096 // 32
+    assert M.moonep_w4_code_bytes(160, 96) == 96 * 2 * 64
+    assert M.moonep_w4_scale_bytes(160, 96) == 96 * 16
+    for kin, n in ((0, 32), (33, 32), (32, 16), (-32, 32), (32, 0), (16, 32)):
+        assert M.lib.moonep_w4_code_bytes(kin, n) == 0 and M.lib.moonep_w4_scale_bytes(kin, n) == 0
+        with pytest.raises(M.MoonEPError):
+            M.moonep_w4_code_bytes(kin, n)
+
+
+def test_quantize_refuses():
+    f = M.lib.moonep_quantize_w4
+    for e, kin, n in ((0, 64, 64), (1025, 64, 64), (1, 0, 64), (1, 64, -1)):
+        assert f(e, kin, n, G, G, G, None) == EINVAL
+    assert f(1, 72, 64, G, G, G, None) == ENOTSUP
+    for i in range(3):
+        a = [G, G, G]
+        a[i] = None
+        assert f(1, 64, 64, *a, None) == EINVAL
+        a[i] = MIS
+        assert f(1, 64, 64, *a, None) == EALIGN
+
+
+def test_ffn_refuses():
+    def call(d, **kw):
+        a = [kw.get(str(i), G) for i in range(9)]
+        return M.lib.moonep_w4_ffn(ctypes.byref(d) if d else None, *a, None)
+
+    assert call(None) == EINVAL
+    for bad in (dict(R=0), dict(S=0), dict(E=0), dict(E=1025), dict(K=0), dict(K=17), dict(E=4, K=5), dict(I=0)):
+        assert call(_dims(**bad)) == EINVAL
+        assert M.lib.moonep_w4_ffn_workspace_bytes(ctypes.byref(_dims(**bad))) == 0
+    bad = _dims()
+    bad.flags = 1024
+    assert call(bad) == EINVAL
+    for bad in (dict(H=7176), dict(I=2056), dict(f32_rows=True), dict(S=1025)):
+        assert call(_dims(**bad)) == ENOTSUP
+    for i in range(9):
+        assert call(_dims(), **{str(i): None}) == EINVAL
+        assert call(_dims(), **{str(i): MIS}) == EALIGN
+    # the planner's limit of 64 home experts a rank is not this call's
+    assert M.moonep_w4_ffn_workspace_bytes(_dims(E=256, S=1)) > 0
+    assert M.W4_MAX_PAIRS == 8192
+
+
+def test_binding_refuses_cpu_tensors():
+    torch = pytest.importorskip("torch")
+    d = M.Dims.make(1, 1, 0, 4, 1, 64)
+    x, w, u = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(64), torch.zeros(8, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        M.moonep_layer_norm(d, x, w, w, 1e-5, x, stream=0)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        M.GradList([w])
+    with pytest.raises(TypeError):
+        M.GradList([1.0])
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        M.GradList([u])
+    with pytest.raises(ValueError, match="GPU tensor"):
+        M.moonep_quantize_w4(torch.zeros(1, 32, 32, dtype=torch.bfloat16), u, u, stream=0)
+
+
+def test_new_constants_match_header():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "moonep.h")).read()
+    found = dict(re.findall(r"#define MOONEP_([A-Z0-9_]+) (\d+)\n", text))
+    assert int(found["W4_MAX_PAIRS"]) == M.W4_MAX_PAIRS
+    assert (int(found["GRAD_F32"]), int(found["GRAD_BF16"])) == (0, 1)
