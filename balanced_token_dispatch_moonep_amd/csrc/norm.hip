@@ -6,6 +6,7 @@
 #include "common.h"
 
 #include <cmath>
+#include <type_traits>
 
 namespace moonep {
 
@@ -67,6 +68,243 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
     __syncthreads();
     return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
+
+// ---------------------------------------------------------------------------
+// rows that fit a wave's or a workgroup's registers
+// ---------------------------------------------------------------------------
+
+// LPR lanes hold a row (a wave 64 / LPR rows), or with LPR = 0 a whole workgroup does.  Lane l of a
+// row holds its vectors l, l + lanes, ...: NV of them, so its columns are the same for every row, and
+// the parameters and the sums over rows stay in registers while the workgroup walks over its rows.
+
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// Sum over the row.  For workgroups, `lds` is 16 words that no wave still reads: one barrier a sum.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+    if constexpr (LPR > 0) {
+        return lanes_sum<LPR>(v);
+    } else {
+        v = lanes_sum<64>(v);
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        float s = 0.0f;
+        for (int i = 0; i < (int)(blockDim.x >> 6); ++i) s += lds[i];
+        return s;
+    }
+}
+
+template <bool F32, int LPR, int NV>
+__global__ __launch_bounds__(LPR > 0 ? 256 : 1024) void norm_kernel(const uint4* __restrict__ x,
+                                                                    const float* __restrict__ w,
+                                                                    const float* __restrict__ b,
+                                                                    uint4* __restrict__ y, float* __restrict__ mean,
+                                                                    float* __restrict__ rstd, int rows, int nv,
+                                                                    float eps) {
+    constexpr int N = RowVec<F32>::N;
+    __shared__ float lds[2][16];
+    const int lanes = LPR > 0 ? LPR : blockDim.x;
+    const int lane = LPR > 0 ? threadIdx.x & (LPR - 1) : threadIdx.x;
+    const int at_once = LPR > 0 ? 256 / LPR : 1;
+    const int stride = gridDim.x * at_once;
+    const float n = (float)nv * N;     // divided by, so that a constant row has its value as the mean
+    int row = blockIdx.x * at_once + (LPR > 0 ? threadIdx.x / LPR : 0);
+    if (row >= rows) return;           // whole rows only: a row's lanes leave together
+    float wf[NV][N], bf[NV][N];
+    uint4 next[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int v = lane + u * lanes;
+        if (v >= nv) continue;
+        load_param<N>(w, v, 1.0f, wf[u]);
+        load_param<N>(b, v, 0.0f, bf[u]);
+        next[u] = x[(size_t)row * nv + v];
+    }
+    for (; row < rows; row += stride) {
+        float f[NV][N], s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int v = lane + u * lanes;
+            if (v < nv) unpack_row<F32>(next[u], f[u]);
+            else
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[u][i] = 0.0f;
+        }
+        if (row + stride < rows) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                const int v = lane + u * lanes;
+                if (v < nv) next[u] = x[(size_t)(row + stride) * nv + v];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s += f[u][i];
+        const float m = row_sum<LPR>(s, lds[0]) / n;
+        s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (lane + u * lanes >= nv) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                f[u][i] -= m;
+                s += f[u][i] * f[u][i];
+            }
+        }
+        const float r = 1.0f / sqrtf(row_sum<LPR>(s, lds[1]) / n + eps);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int v = lane + u * lanes;
+            if (v >= nv) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[u][i] = f[u][i] * r * wf[u][i] + bf[u][i];
+            st_nt(pack_row<F32>(f[u]), y + (size_t)row * nv + v);
+        }
+        if (mean && lane == 0) {
+            mean[row] = m;
+            rstd[row] = r;
+        }
+    }
+}
+
+// One pass over dy and x: dx, and the workgroup's share of the sums over rows in
+// ws[workgroup][0] = sum dy n, ws[workgroup][1] = sum dy (ws NULL: not wanted).
+template <bool F32, int LPR, int NV>
+__global__ __launch_bounds__(LPR > 0 ? 256 : 512) void norm_backward_kernel(
+    const uint4* __restrict__ dy, const uint4* __restrict__ x, const float* __restrict__ w,
+    const float* __restrict__ mean, const float* __restrict__ rstd, uint4* __restrict__ dx, float* __restrict__ ws,
+    int rows, int nv) {
+    constexpr int N = RowVec<F32>::N;
+    __shared__ float lds[4][16];
+    const int lanes = LPR > 0 ? LPR : blockDim.x;
+    const int lane = LPR > 0 ? threadIdx.x & (LPR - 1) : threadIdx.x;
+    const int at_once = LPR > 0 ? 256 / LPR : 1;
+    const int stride = gridDim.x * at_once;
+    const float n = (float)nv * N;
+    int row = blockIdx.x * at_once + (LPR > 0 ? threadIdx.x / LPR : 0);
+    float wf[NV][N], aw[NV][N], ab[NV][N];
+    uint4 nx[NV], nd[NV];
+    float nm = 0.0f, nr = 0.0f;
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int v = lane + u * lanes;
+            if (v >= nv) continue;
+            nx[u] = x[(size_t)t * nv + v];
+            nd[u] = dy[(size_t)t * nv + v];
+        }
+        nm = mean[t];
+        nr = rstd[t];
+    };
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int v = lane + u * lanes;
+        if (v < nv) load_param<N>(w, v, 1.0f, wf[u]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) aw[u][i] = ab[u][i] = 0.0f;
+    }
+    if (row < rows) fetch(row);
+    for (int turn = 0; row < rows; row += stride, turn ^= 2) {
+        float f[NV][N], d[NV][N], sg = 0.0f, sn = 0.0f;
+        const float m = nm, r = nr;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (lane + u * lanes < nv) {
+                unpack_row<F32>(nx[u], f[u]);
+                unpack_row<F32>(nd[u], d[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[u][i] = d[u][i] = wf[u][i] = 0.0f;
+            }
+        }
+        if (row + stride < rows) fetch(row + stride);
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                f[u][i] = (f[u][i] - m) * r;
+                aw[u][i] += d[u][i] * f[u][i];
+                ab[u][i] += d[u][i];
+                d[u][i] *= wf[u][i];
+                sg += d[u][i];
+                sn += d[u][i] * f[u][i];
+            }
+        float c1, c2;
+        if constexpr (LPR > 0) {
+            c1 = lanes_sum<LPR>(sg) / n;
+            c2 = lanes_sum<LPR>(sn) / n;
+        } else {
+            // the sums of two rows in a row use different words: one barrier a row
+            sg = lanes_sum<64>(sg);
+            sn = lanes_sum<64>(sn);
+            if ((threadIdx.x & 63) == 0) {
+                lds[turn][threadIdx.x >> 6] = sg;
+                lds[turn + 1][threadIdx.x >> 6] = sn;
+            }
+            __syncthreads();
+            sg = sn = 0.0f;
+            for (int i = 0; i < (int)(blockDim.x >> 6); ++i) {
+                sg += lds[turn][i];
+                sn += lds[turn + 1][i];
+            }
+            c1 = sg / n;
+            c2 = sn / n;
+        }
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int v = lane + u * lanes;
+            if (v >= nv) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[u][i] = r * (d[u][i] - c1 - f[u][i] * c2);
+            st_nt(pack_row<F32>(f[u]), dx + (size_t)row * nv + v);
+        }
+    }
+    if (!ws) return;
+    const size_t H = (size_t)nv * N;
+    float* o = ws + (size_t)blockIdx.x * 2 * H;
+    if constexpr (LPR > 0) {
+        // the rows of a wave, then those of the four waves
+        __shared__ float part[4][LPR * N];
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    float s = k == 0 ? aw[u][i] : ab[u][i];
+#pragma unroll
+                    for (int off = LPR; off < 64; off <<= 1) s += __shfl_xor(s, off, 64);
+                    if ((threadIdx.x & 63) < LPR) part[threadIdx.x >> 6][lane * N + i] = s;
+                }
+                __syncthreads();
+                const int c0 = u * LPR * N;
+                for (int c = threadIdx.x; c < LPR * N && c0 + c < (int)H; c += 256)
+                    o[k * H + c0 + c] = (part[0][c] + part[1][c]) + (part[2][c] + part[3][c]);
+            }
+    } else {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int v = lane + u * lanes;
+            if (v >= nv) continue;
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                *reinterpret_cast<float4*>(o + (size_t)v * N + i) = make_float4(aw[u][i], aw[u][i + 1], aw[u][i + 2], aw[u][i + 3]);
+                *reinterpret_cast<float4*>(o + H + (size_t)v * N + i) = make_float4(ab[u][i], ab[u][i + 1], ab[u][i + 2], ab[u][i + 3]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// longer rows
+// ---------------------------------------------------------------------------
 
 // One workgroup per row; the row is read three times (from L2 after the first).
 template <bool F32>
@@ -171,20 +409,123 @@ __global__ __launch_bounds__(256) void norm_dw_cols_kernel(const uint4* __restri
     }
 }
 
-// Joins the partial sums of `splits` shares, one column per thread.
-__global__ __launch_bounds__(256) void norm_dw_join_kernel(const float* __restrict__ ws, float* __restrict__ dw,
-                                                           float* __restrict__ db, int splits, int H, int accum) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
+// Joins the partial sums of `splits` shares: 64 columns a workgroup, the shares dealt to its 16 waves.
+__global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict__ ws, float* __restrict__ dw,
+                                                         float* __restrict__ db, int splits, int H, int accum) {
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
     float* out = blockIdx.y == 0 ? dw : db;
-    if (c >= H || !out) return;
+    if (!out) return;
     const float* p = ws + (size_t)blockIdx.y * H + c;
     float s = 0.0f;
-    for (int i = 0; i < splits; ++i) s += p[(size_t)i * 2 * H];
+    if (c < H) {
+#pragma unroll 8
+        for (int i = wave; i < splits; i += 16) s += p[(size_t)i * 2 * H];
+    }
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave > 0 || c >= H) return;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += part[i][lane];
     out[c] = accum ? out[c] + s : s;
 }
 
-// Shares of the rows whose sums the backward joins.
-static int norm_splits(const moonep_dims_t* d) { return std::min(d->R * d->S, 512); }
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+constexpr int kCUs = 256;
+
+// How a row of nv vectors is spread: over `lpr` lanes of a wave, or (0) over `waves` waves, `per`
+// vectors a lane; per == 0: it does not fit, the kernels for longer rows take it.
+struct RowShape {
+    int lpr, waves, per;
+};
+
+static RowShape row_shape(int nv, int max_waves) {
+    if (nv <= 8) return {8, 4, 1};
+    if (nv <= 16) return {16, 4, 1};
+    if (nv <= 32) return {32, 4, 1};
+    if (nv <= 64) return {64, 4, 1};
+    if (nv <= 128) return {64, 4, 2};
+    for (int per = 2; per <= 4; per *= 2) {
+        const int waves = (nv + 64 * per - 1) / (64 * per);
+        if (waves <= max_waves) return {0, waves, per};
+    }
+    return {0, 4, 0};
+}
+
+static RowShape forward_shape(const moonep_dims_t* d) {
+    return row_shape(d->H / (d->flags & MOONEP_F32_ROWS ? 4 : 8), 16);
+}
+
+// The backward holds two rows and its sums: workgroups of more than 8 waves would spill registers
+// (measured 336 us instead of 262 at 32768 rows of 7168 bf16).
+static RowShape backward_shape(const moonep_dims_t* d) {
+    return row_shape(d->H / (d->flags & MOONEP_F32_ROWS ? 4 : 8), 8);
+}
+
+// Workgroups of the backward, each with its share of the rows.
+static int norm_splits(const moonep_dims_t* d) {
+    const int rows = d->R * d->S;
+    const RowShape s = backward_shape(d);
+    if (s.per == 0) return std::min(rows, 2 * kCUs);
+    const int at_once = s.lpr > 0 ? 256 / s.lpr : 1;
+    const int most = kCUs * (s.lpr > 0 ? 2 : std::max(1, 8 / s.waves));
+    return std::min((rows + at_once - 1) / at_once, most);
+}
+
+template <bool F32, class F>
+static void with_shape(const RowShape& s, F f) {
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I4 = std::integral_constant<int, 4>;
+    if (s.lpr == 8) f(std::integral_constant<int, 8>{}, I1{});
+    else if (s.lpr == 16) f(std::integral_constant<int, 16>{}, I1{});
+    else if (s.lpr == 32) f(std::integral_constant<int, 32>{}, I1{});
+    else if (s.lpr == 64 && s.per == 1) f(std::integral_constant<int, 64>{}, I1{});
+    else if (s.lpr == 64) f(std::integral_constant<int, 64>{}, I2{});
+    else if (s.per == 2) f(I0{}, I2{});
+    else f(I0{}, I4{});
+}
+
+template <bool F32>
+static void launch_norm(const moonep_dims_t* d, hipStream_t s, const uint4* x, const float* w, const float* b,
+                        uint4* y, float* mean, float* rstd, float eps) {
+    const int rows = d->R * d->S, nv = d->H / RowVec<F32>::N;
+    const RowShape sh = forward_shape(d);
+    if (sh.per == 0) {
+        hipLaunchKernelGGL(norm_rows_kernel<F32>, dim3(rows), dim3(256), 0, s, x, w, b, y, mean, rstd, nv, eps);
+        return;
+    }
+    const int at_once = sh.lpr > 0 ? 256 / sh.lpr : 1;
+    const int most = kCUs * (sh.lpr > 0 ? 5 : std::max(1, 24 / sh.waves));
+    const dim3 grid(std::min((rows + at_once - 1) / at_once, most));
+    with_shape<F32>(sh, [&](auto lpr, auto per) {
+        hipLaunchKernelGGL((norm_kernel<F32, lpr.value, per.value>), grid, dim3(64 * sh.waves), 0, s, x, w, b, y,
+                           mean, rstd, rows, nv, eps);
+    });
+}
+
+template <bool F32>
+static void launch_norm_backward(const moonep_dims_t* d, hipStream_t s, const uint4* dy, const uint4* x,
+                                 const float* w, const float* mean, const float* rstd, uint4* dx, float* ws) {
+    const int rows = d->R * d->S, nv = d->H / RowVec<F32>::N, splits = norm_splits(d);
+    const RowShape sh = backward_shape(d);
+    if (sh.per == 0) {
+        hipLaunchKernelGGL(norm_dx_rows_kernel<F32>, dim3(rows), dim3(256), 0, s, dy, x, w, mean, rstd, dx, nv);
+        if (ws)
+            hipLaunchKernelGGL(norm_dw_cols_kernel<F32>, dim3((nv + 255) / 256, splits), dim3(256), 0, s, dy, x, mean,
+                               rstd, ws, rows, nv);
+        return;
+    }
+    with_shape<F32>(sh, [&](auto lpr, auto per) {
+        hipLaunchKernelGGL((norm_backward_kernel<F32, lpr.value, per.value>), dim3(splits), dim3(64 * sh.waves), 0, s,
+                           dy, x, w, mean, rstd, dx, ws, rows, nv);
+    });
+}
 
 }  // namespace moonep
 
@@ -199,13 +540,11 @@ extern "C" int moonep_layer_norm(const moonep_dims_t* dims, const void* x, const
     MOONEP_CHECK_PTR(y);
     if (!aligned16(weight) || !aligned16(bias) || !aligned16(mean) || !aligned16(rstd)) return MOONEP_EALIGN;
     const bool f32 = (dims->flags & MOONEP_F32_ROWS) != 0;
-    const int nv = dims->H / (f32 ? 4 : 8);
-    const dim3 grid(dims->R * dims->S);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const uint4* xv = static_cast<const uint4*>(x);
     uint4* yv = static_cast<uint4*>(y);
-    if (f32) hipLaunchKernelGGL(norm_rows_kernel<true>, grid, dim3(256), 0, s, xv, weight, bias, yv, mean, rstd, nv, eps);
-    else hipLaunchKernelGGL(norm_rows_kernel<false>, grid, dim3(256), 0, s, xv, weight, bias, yv, mean, rstd, nv, eps);
+    if (f32) launch_norm<true>(dims, s, xv, weight, bias, yv, mean, rstd, eps);
+    else launch_norm<false>(dims, s, xv, weight, bias, yv, mean, rstd, eps);
     MOONEP_LAUNCH_CHECK();
     return MOONEP_OK;
 }
@@ -229,22 +568,16 @@ extern "C" int moonep_layer_norm_backward(const moonep_dims_t* dims, const void*
     const bool sums = dweight || dbias;
     if (sums) MOONEP_CHECK_PTR(ws);
     const bool f32 = (dims->flags & MOONEP_F32_ROWS) != 0;
-    const int rows = dims->R * dims->S, nv = dims->H / (f32 ? 4 : 8);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const uint4 *dv = static_cast<const uint4*>(dy), *xv = static_cast<const uint4*>(x);
     uint4* ov = static_cast<uint4*>(dx);
-    if (f32) hipLaunchKernelGGL(norm_dx_rows_kernel<true>, dim3(rows), dim3(256), 0, s, dv, xv, weight, mean, rstd, ov, nv);
-    else hipLaunchKernelGGL(norm_dx_rows_kernel<false>, dim3(rows), dim3(256), 0, s, dv, xv, weight, mean, rstd, ov, nv);
+    float* wsf = sums ? static_cast<float*>(ws) : nullptr;
+    if (f32) launch_norm_backward<true>(dims, s, dv, xv, weight, mean, rstd, ov, wsf);
+    else launch_norm_backward<false>(dims, s, dv, xv, weight, mean, rstd, ov, wsf);
     MOONEP_LAUNCH_CHECK();
     if (!sums) return MOONEP_OK;
-    const int splits = norm_splits(dims);
-    const dim3 grid((nv + 255) / 256, splits);
-    float* wsf = static_cast<float*>(ws);
-    if (f32) hipLaunchKernelGGL(norm_dw_cols_kernel<true>, grid, dim3(256), 0, s, dv, xv, mean, rstd, wsf, rows, nv);
-    else hipLaunchKernelGGL(norm_dw_cols_kernel<false>, grid, dim3(256), 0, s, dv, xv, mean, rstd, wsf, rows, nv);
-    MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(norm_dw_join_kernel, dim3((dims->H + 255) / 256, 2), dim3(256), 0, s, wsf, dweight, dbias,
-                       splits, dims->H, (dims->flags & MOONEP_GRAD_ACCUM) != 0);
+    hipLaunchKernelGGL(norm_join_kernel, dim3((dims->H + 63) / 64, 2), dim3(1024), 0, s, wsf, dweight, dbias,
+                       norm_splits(dims), dims->H, (dims->flags & MOONEP_GRAD_ACCUM) != 0);
     MOONEP_LAUNCH_CHECK();
     return MOONEP_OK;
 }
