@@ -307,7 +307,7 @@ def test_grad_list_empty_and_refusals():
     with pytest.raises(M.MoonEPError):
         M.moonep_grad_clip(M.GradList([g, g[16:32]]), norm, 1.0)
     with pytest.raises(M.MoonEPError):
-        M.moonep_grad_norm(M.GradList([g[1:]]), torch.empty(8192, dtype=torch.uint8, device=DEV), norm)
+        _norm_of(M.GradList([g[1:]]))
     with pytest.raises(ValueError, match="contiguous"):
         M.GradList([g.view(8, 8).t()])
     h = torch.zeros(64, device=DEV)
