@@ -13,6 +13,7 @@ PyTorch is used only to own device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -165,16 +166,23 @@ def moonep_version() -> str:
 # marshalling helpers
 # ----------------------------------------------------------------------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported with the first call that needs it."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else int(stream.cuda_stream)
     torch = _torch()
-    return int(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t, name, dtype=None, shape=None, numel=None, optional=False):
@@ -187,14 +195,14 @@ def _ptr(t, name, dtype=None, shape=None, numel=None, optional=False):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}; the library runs on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
@@ -386,6 +394,18 @@ def moonep_reduce_grad(d: Dims, plan_ws, dw13_home, dw2_home, dw13_red, dw2_red,
 # round the layer: norm, gradient clipping, decoding with 4-bit experts
 # ----------------------------------------------------------------------------
 
+def _bytes(n: int, where: str) -> int:
+    if n == 0:
+        raise MoonEPError(-1, where)
+    return int(n)
+
+
+@functools.lru_cache(maxsize=1024)
+def _dims_bytes(name: str, dims: bytes) -> int:
+    """What the size function `name` says for these dims (a pure function of them)."""
+    return _bytes(getattr(_lib(), name)(ctypes.byref(Dims.from_buffer_copy(dims))), name)
+
+
 def moonep_layer_norm(d: Dims, x, weight, bias, eps, y, mean=None, rstd=None, stream=None) -> None:
     """y = layer norm of the [R, S, H] rows x.  weight, bias [H] float32 or None; mean, rstd [R*S]
     float32, for the backward, or both None."""
@@ -403,7 +423,7 @@ def moonep_layer_norm(d: Dims, x, weight, bias, eps, y, mean=None, rstd=None, st
 
 
 def moonep_layer_norm_workspace_bytes(d: Dims) -> int:
-    return _bytes(_lib().moonep_layer_norm_workspace_bytes(ctypes.byref(d)), "moonep_layer_norm_workspace_bytes")
+    return _dims_bytes("moonep_layer_norm_workspace_bytes", bytes(d))
 
 
 def moonep_layer_norm_backward(d: Dims, dy, x, weight, mean, rstd, dx, dweight, dbias, ws=None, stream=None) -> None:
@@ -477,16 +497,12 @@ def moonep_grad_clip(grads: GradList, norm, max_norm, stream=None) -> None:
     _check(_lib().moonep_grad_clip(*grads._arrays(), norm, float(max_norm), _stream(stream)), "moonep_grad_clip")
 
 
-def _bytes(n: int, where: str) -> int:
-    if n == 0:
-        raise MoonEPError(-1, where)
-    return int(n)
-
-
+@functools.lru_cache(maxsize=1024)
 def moonep_w4_code_bytes(Kin: int, N: int) -> int:
     return _bytes(_lib().moonep_w4_code_bytes(Kin, N), "moonep_w4_code_bytes")
 
 
+@functools.lru_cache(maxsize=1024)
 def moonep_w4_scale_bytes(Kin: int, N: int) -> int:
     return _bytes(_lib().moonep_w4_scale_bytes(Kin, N), "moonep_w4_scale_bytes")
 
@@ -505,7 +521,7 @@ def moonep_quantize_w4(w, codes, scales, stream=None) -> None:
 
 
 def moonep_w4_ffn_workspace_bytes(d: Dims) -> int:
-    return _bytes(_lib().moonep_w4_ffn_workspace_bytes(ctypes.byref(d)), "moonep_w4_ffn_workspace_bytes")
+    return _dims_bytes("moonep_w4_ffn_workspace_bytes", bytes(d))
 
 
 def moonep_w4_ffn(d: Dims, topk, gates, x, w13_codes, w13_scales, w2_codes, w2_scales, ws, out, stream=None) -> None:
