@@ -6,11 +6,15 @@
 // OCP Microscaling FP4 format).  v_cvt_scalef32_pk_bf16_fp4 turns two codes and their scale into two
 // bf16 values, exactly, in one instruction; matrix instructions multiply them by the tokens' rows.
 //
-// Pairs (token, k) are grouped by expert first, so that an expert's weights are read once for all
-// its tokens.  A lane (column c = lane % 16, group q = lane / 16) of a wave loads 16 bytes: the 32
-// codes of group q of column c in a block of 128 input values.  The matrix instruction of step m
+// Pairs (token, k) are grouped by expert, so that an expert's weights are read once for all its
+// tokens.  A lane (column c = lane % 16, group q = lane / 16) of a wave loads 16 bytes: the 32 codes
+// of group q of column c in a block of 128 input values.  The matrix instruction of step m
 // multiplies values q * 32 + m * 8 .. + 8 of each group, which is an order of the input direction
 // that both operands share.
+//
+// Up to 64 pairs, one wave can look at all ids at once: each workgroup finds its own group, and rows
+// are read where they lie.  Beyond, a first kernel groups the pairs and lays their rows out in the
+// order in which the matrix instruction's operand reads them.
 #include "common.h"
 
 namespace moonep {
@@ -20,7 +24,10 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kGroup = 32;           // values a scale
 constexpr int kBlock = 128;          // input values of one wave's load
-constexpr int kRowsUp = 16;          // rows a matrix instruction takes
+constexpr int kTile = 16;            // rows a matrix instruction takes, columns of a tile
+constexpr int kRowTiles = 4;         // row tiles of a chunk
+constexpr int kChunk4 = kTile * kRowTiles;
+constexpr int kFewPairs = 64;
 
 struct W4Dims {
     int T, K, E, H, I;
@@ -33,24 +40,33 @@ struct W4Mat {
     int kin, kb, sb, nb;
 };
 
-// A run of an expert's pairs: at most kRowsUp of them.
+// A run of an expert's pairs, at most kChunk4 of them, in row tiles of their own.
 struct Chunk {
-    int32_t expert, first, rows, pad;
+    int32_t expert, tile, rows, pad;
 };
 
+// Scratch.  Few pairs use act alone, as [T*K][2][I]; otherwise
 struct W4Ws {
     int32_t* nchunk;                 // [1]
-    Chunk* chunks;                   // [max chunks]
-    int32_t* pair;                   // [T*K] pairs t * K + k by expert
-    uint16_t* act;                   // [T*K][2][I] bf16: leading and trailing term, by place in `pair`
+    Chunk* chunks;                   // [max_chunks]
+    int32_t* pair;                   // [max_tiles][16] the pair of each row
+    uint4* rows;                     // [max_tiles][H/128][4 steps][64 lanes] x, as operands
+    uint16_t* act;                   // [max_tiles * 2][I/128][4 steps][64 lanes][8]: a row tile's 16
+                                     // activations in two bf16 terms, a pair's terms next to each other
     float* y;                        // [T*K][H] by pair
     int max_chunks;
 };
 
+static int blocks_of(int kin) { return (kin + kBlock - 1) / kBlock; }
+static int fours_of(int kin) { return (blocks_of(kin) + 3) / 4; }
+
 static size_t w4_ws_layout(const W4Dims& d, void* base, W4Ws* ws) {
-    const size_t pairs = (size_t)d.T * d.K;
+    const size_t pairs = (size_t)d.T * d.K, experts = std::min<size_t>(pairs, d.E);
+    const bool few = pairs <= kFewPairs;
+    // an expert leaves less than one tile, and less than one chunk, partly empty
+    const size_t tiles = few ? 0 : experts + pairs / kTile;
     W4Ws w{};
-    w.max_chunks = (int)(std::min<size_t>(pairs, d.E) + pairs / kRowsUp);
+    w.max_chunks = (int)(experts + pairs / kChunk4);
     size_t off = 0;
     auto take = [&](size_t bytes) -> void* {
         void* p = base ? static_cast<char*>(base) + off : nullptr;
@@ -59,59 +75,14 @@ static size_t w4_ws_layout(const W4Dims& d, void* base, W4Ws* ws) {
     };
     w.nchunk = (int32_t*)take(4);
     w.chunks = (Chunk*)take(w.max_chunks * sizeof(Chunk));
-    w.pair = (int32_t*)take(pairs * 4);
-    w.act = (uint16_t*)take(pairs * 2 * d.I * 2);
-    w.y = (float*)take(pairs * d.H * 4);
+    w.pair = (int32_t*)take(tiles * kTile * 4);
+    w.rows = (uint4*)take(tiles * blocks_of(d.H) * 4096);
+    // one tile more: the second product takes an expert's last tiles by two, and reads (without using
+    // it) the tile after an odd one
+    w.act = (uint16_t*)take(few ? pairs * 2 * d.I * 2 : (tiles + 1) * 2 * blocks_of(d.I) * 4096);
+    w.y = (float*)take(few ? 0 : pairs * d.H * 4);
     if (ws) *ws = w;
     return off;
-}
-
-// ---------------------------------------------------------------------------
-// Groups the pairs by expert: one workgroup, a thread an expert.  The order of an expert's pairs
-// depends on which thread's atomic comes first; a row's result does not depend on its place.
-// ---------------------------------------------------------------------------
-
-__device__ __forceinline__ int wave_scan(int v) {    // inclusive prefix sum over the wave
-    const int lane = threadIdx.x & 63;
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(v, o, 64);
-        if (lane >= o) v += u;
-    }
-    return v;
-}
-
-__global__ __launch_bounds__(1024) void w4_group_kernel(const int32_t* __restrict__ topk, W4Ws w, int pairs, int E) {
-    __shared__ int count[1024], place[1024];
-    __shared__ int wave_rows[16], wave_chunks[16];
-    const int e = threadIdx.x, lane = e & 63, wv = e >> 6;
-    count[e] = 0;
-    __syncthreads();
-    for (int p = e; p < pairs; p += 1024) {
-        const int id = topk[p];
-        if ((unsigned)id < (unsigned)E) atomicAdd(&count[id], 1);
-    }
-    __syncthreads();
-    const int rows = count[e], chunks = (rows + kRowsUp - 1) / kRowsUp;
-    const int rs = wave_scan(rows), cs = wave_scan(chunks);
-    if (lane == 63) {
-        wave_rows[wv] = rs;
-        wave_chunks[wv] = cs;
-    }
-    __syncthreads();
-    int row0 = rs - rows, chunk0 = cs - chunks;
-    for (int i = 0; i < wv; ++i) {
-        row0 += wave_rows[i];
-        chunk0 += wave_chunks[i];
-    }
-    place[e] = row0;
-    for (int i = 0; i < chunks; ++i)
-        w.chunks[chunk0 + i] = Chunk{e, row0 + i * kRowsUp, min(kRowsUp, rows - i * kRowsUp), 0};
-    if (e == 1023) w.nchunk[0] = chunk0 + chunks;
-    __syncthreads();
-    for (int p = e; p < pairs; p += 1024) {
-        const int id = topk[p];
-        if ((unsigned)id < (unsigned)E) w.pair[atomicAdd(&place[id], 1)] = p;
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -137,80 +108,363 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t codes, float scale) {
     return r.all;
 }
 
-// acc += rows (each lane's own, bf16, its group's first value in the first block) times one column tile.
-__device__ __forceinline__ f32x4_t w4_tile(const uint16_t* __restrict__ row, const W4Mat& m, size_t tile) {
-    const int lane = threadIdx.x & 63, q = lane >> 4;
-    const uint4* codes = m.codes + tile * m.kb * 64 + lane;
-    const uint32_t* scales = m.scales + tile * m.sb * 64 + lane;
-    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb = 0; kb < m.kb; ++kb) {
-        const uint4 c = codes[(size_t)kb * 64];
-        const float s = scale_of(scales[(size_t)(kb >> 2) * 64], kb & 3);
-        const bool in = kb * kBlock + q * kGroup < m.kin;
-        const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+__device__ __forceinline__ uint32_t dword(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// A lane's codes and scales of four blocks of NT column tiles.
+template <int NT>
+struct Four {
+    uint4 codes[NT][4];
+    uint32_t scales[NT];
+};
+
+template <int NT>
+__device__ __forceinline__ void load_four(Four<NT>& f, const W4Mat& m, const size_t* tile, int four) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const uint4* c = m.codes + (tile[t] * m.kb + four * 4) * 64 + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (four * 4 + j < m.kb) f.codes[t][j] = ld_nt(c + j * 64);
+        f.scales[t] = m.scales[(tile[t] * m.sb + four) * 64 + lane];
+    }
+}
+
+// acc[r][t] += rows * weights of four blocks; a(r, kb, i, in) is the row operand of row tile r, block
+// kb and step i, of which lanes with `in` false are past the end of the input direction.
+template <int RT, int NT, class A>
+__device__ __forceinline__ void multiply_four(f32x4_t (&acc)[RT][NT], const Four<NT>& f, const W4Mat& m, int four, A a) {
+    auto block = [&](int j, bool in) {
+        const int kb = four * 4 + j;
+        float s[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t] = scale_of(f.scales[t], j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint4 a = make_uint4(0, 0, 0, 0);
-            if (in) a = *reinterpret_cast<const uint4*>(row + kb * kBlock + i * 8);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), widen(cs[i], s), acc, 0, 0, 0);
+            bf16x8_t b[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) b[t] = widen(dword(f.codes[t][j], i), s[t]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const bf16x8_t v = __builtin_bit_cast(bf16x8_t, a(r, kb, i, in));
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[t], acc[r][t], 0, 0, 0);
+            }
+        }
+    };
+    if ((four + 1) * 4 * kBlock <= m.kin) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) block(j, true);
+    } else {
+        const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (four * 4 + j < m.kb) block(j, (four * 4 + j) * kBlock + q * kGroup < m.kin);
+    }
+}
+
+// acc = rows times NT column tiles over fours first, first + step, ...; the next four's loads are in
+// flight while one is multiplied.
+template <int RT, int NT, class A>
+__device__ __forceinline__ void multiply(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, int first,
+                                         int step, A a) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (first >= m.sb) return;
+    Four<NT> next;
+    load_four(next, m, tile, first);
+    for (int four = first; four < m.sb; four += step) {
+        const Four<NT> now = next;
+        if (four + step < m.sb) load_four(next, m, tile, four + step);
+        multiply_four<RT, NT>(acc, now, m, four, a);
+    }
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// a as two bf16 terms, at least 16 bits together.  The leading one is cut, not rounded, so that it
+// cannot overflow; the rest is exact before its own rounding.
+__device__ __forceinline__ void two_terms(float a, uint16_t& lead, uint16_t& rest) {
+    const uint32_t hi = __float_as_uint(a) & 0xffff0000u;
+    const float lo = (hi & 0x7f800000u) == 0x7f800000u ? 0.0f : a - __uint_as_float(hi);
+    lead = (uint16_t)(hi >> 16);
+    rest = (uint16_t)pack_bf16(lo, 0.0f);
+}
+
+// ---------------------------------------------------------------------------
+// few pairs
+// ---------------------------------------------------------------------------
+
+// A wave's view of all pairs: the expert of pair `lane`, -1 for none.
+__device__ __forceinline__ int pair_expert(const int32_t* topk, int pairs, int E) {
+    const int lane = threadIdx.x & 63;
+    const int id = lane < pairs ? topk[lane] : -1;
+    return (unsigned)id < (unsigned)E ? id : -1;
+}
+
+// Lane r's pair of the r-th member of `members`, r < popcount.
+__device__ __forceinline__ int member_pair(unsigned long long members) {
+    const int lane = threadIdx.x & 63;
+    const unsigned long long below = (1ull << lane) - 1;
+    const int n = __popcll(members);
+    const int to = (members >> lane) & 1 ? __popcll(members & below) : n + __popcll(~members & below);
+    return __builtin_amdgcn_ds_permute(to * 4, lane);
+}
+
+// act = silu(x G) * (x U) for one expert and 16 columns.  The waves deal out the input direction and
+// join their sums in order.  blockIdx.y: a pair, that leads its expert's group if it is the first of
+// it, or an expert where there are fewer experts than pairs.
+constexpr int kUpWaves = 7;
+
+__global__ __launch_bounds__(64 * kUpWaves) void w4_few_up_kernel(const int32_t* __restrict__ topk,
+                                                                  const uint16_t* __restrict__ x, W4Mat m,
+                                                                  uint16_t* __restrict__ act, W4Dims d) {
+    __shared__ float4 part[kUpWaves][2][64];
+    const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+    const int id = pair_expert(topk, pairs, d.E);
+    const int e = pairs <= d.E ? __builtin_amdgcn_readlane(id, blockIdx.y) : blockIdx.y;
+    const unsigned long long members = __ballot(id == e);
+    if (e < 0 || members == 0) return;
+    if (pairs <= d.E && __ffsll(members) - 1 != (int)blockIdx.y) return;
+    const int n = __popcll(members), pair = member_pair(members);
+    const size_t g = (size_t)e * m.nb + blockIdx.x, tile[2] = {g, g + m.nb / 2};
+    for (int r0 = 0; r0 < n; r0 += kTile) {
+        // rows past the group's compute with its last one; nothing of them is stored
+        const int token = __shfl(pair, min(r0 + c, n - 1), 64) / d.K;
+        const uint16_t* row = x + (size_t)token * d.H + q * kGroup;
+        f32x4_t acc[1][2];
+        multiply<1, 2>(acc, m, tile, wave, kUpWaves, [&](int, int kb, int i, bool in) {
+            return in ? *reinterpret_cast<const uint4*>(row + kb * kBlock + i * 8) : make_uint4(0, 0, 0, 0);
+        });
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            part[wave][t][lane] = make_float4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]);
+        __syncthreads();
+        const int r = threadIdx.x >> 4, to = __shfl(pair, min(r0 + r, n - 1), 64);
+        if (r < min(kTile, n - r0)) {
+            const int at = (r / 4 * 16 + c) * 4 + r % 4;
+            float gate = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kUpWaves; ++w) {
+                gate += reinterpret_cast<const float*>(part[w][0])[at];
+                up += reinterpret_cast<const float*>(part[w][1])[at];
+            }
+            uint16_t lead, rest;
+            two_terms(swiglu(gate, up), lead, rest);
+            uint16_t* o = act + (size_t)to * 2 * d.I + blockIdx.x * kTile + c;
+            o[0] = lead;
+            o[d.I] = rest;
         }
     }
-    return acc;
 }
 
-// act = silu(x G) * (x U) for one chunk and 16 columns, as two bf16 terms.
-__global__ __launch_bounds__(64) void w4_up_kernel(const uint16_t* __restrict__ x, W4Mat m, W4Ws w, W4Dims d) {
-    if ((int)blockIdx.y >= w.nchunk[0]) return;
-    const Chunk ch = w.chunks[blockIdx.y];
-    const int lane = threadIdx.x, c = lane & 15, q = lane >> 4;
-    // rows past the chunk's compute with its last one; nothing of them is stored
-    const int token = w.pair[ch.first + min(c, ch.rows - 1)] / d.K;
-    const uint16_t* row = x + (size_t)token * d.H + q * kGroup;
-    const size_t tile = (size_t)ch.expert * m.nb + blockIdx.x;
-    const f32x4_t g = w4_tile(row, m, tile);
-    const f32x4_t u = w4_tile(row, m, tile + m.nb / 2);
+// out for 16 columns and all tokens: the waves take the experts in turn, each group's rows go to LDS,
+// and a token's are joined in k order.  The rows of a matrix instruction are the two terms of 8 pairs.
+constexpr int kDownWaves = 8;
+
+__global__ __launch_bounds__(64 * kDownWaves) void w4_few_down_kernel(const int32_t* __restrict__ topk,
+                                                                      const float* __restrict__ gates,
+                                                                      const uint16_t* __restrict__ act, W4Mat m,
+                                                                      uint16_t* __restrict__ out, W4Dims d) {
+    __shared__ float y[kFewPairs][kTile];
+    const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+    const int id = pair_expert(topk, pairs, d.E);
+    unsigned long long left = __ballot(id >= 0);
+    for (int turn = 0; left; ++turn) {
+        const int e = __builtin_amdgcn_readlane(id, __ffsll(left) - 1);
+        const unsigned long long members = __ballot(id == e);
+        left &= ~members;
+        if (turn % kDownWaves != wave) continue;
+        const int n = __popcll(members), pair = member_pair(members);
+        const size_t tile[1] = {(size_t)e * m.nb + blockIdx.x};
+        for (int r0 = 0; r0 < n; r0 += kTile / 2) {
+            const int term = min(r0 * 2 + c, n * 2 - 1);
+            const uint16_t* row = act + ((size_t)__shfl(pair, term / 2, 64) * 2 + term % 2) * d.I + q * kGroup;
+            f32x4_t acc[1][1];
+            multiply<1, 1>(acc, m, tile, 0, 1, [&](int, int kb, int i, bool in) {
+                return in ? *reinterpret_cast<const uint4*>(row + kb * kBlock + i * 8) : make_uint4(0, 0, 0, 0);
+            });
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = q * 4 + i;
-        if (r >= ch.rows) continue;
-        const float a = g[i] / (1.0f + expf(-g[i])) * u[i];
-        // leading term cut, not rounded, so that it cannot overflow; the rest is exact before its rounding
-        const uint32_t hi = __float_as_uint(a) & 0xffff0000u;
-        const float lo = (hi & 0x7f800000u) == 0x7f800000u ? 0.0f : a - __uint_as_float(hi);
-        uint16_t* o = w.act + (size_t)(ch.first + r) * 2 * d.I + blockIdx.x * 16 + c;
-        o[0] = (uint16_t)(hi >> 16);
-        o[d.I] = (uint16_t)pack_bf16(lo, 0.0f);
+            for (int i = 0; i < 2; ++i) {
+                const int r = r0 + q * 2 + i, p = __shfl(pair, min(r, n - 1), 64);
+                if (r < n) y[p][c] = acc[0][0][2 * i] + acc[0][0][2 * i + 1];
+            }
+        }
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < d.T * kTile; v += 64 * kDownWaves) {
+        const int t = v / kTile, col = v % kTile;
+        float s = 0.0f;
+        for (int p = t * d.K; p < (t + 1) * d.K; ++p)
+            if ((unsigned)topk[p] < (unsigned)d.E) s += gates[p] * y[p][col];
+        out[(size_t)t * d.H + blockIdx.x * kTile + col] = (uint16_t)pack_bf16(s, 0.0f);
     }
 }
 
-// y = act D for one chunk and 16 columns: the rows of the matrix instruction are the two terms of 8 pairs.
-__global__ __launch_bounds__(64) void w4_down_kernel(W4Mat m, W4Ws w, W4Dims d) {
+// ---------------------------------------------------------------------------
+// many pairs
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ int block_sum(int v, int* lds) {   // workgroup of 256
+    v = wave_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// Expert blockIdx.y's pairs in order, and four blocks of their rows as operands.  Every workgroup
+// counts all pairs itself, so that one launch does.
+__global__ __launch_bounds__(256) void w4_gather_kernel(const int32_t* __restrict__ topk,
+                                                        const uint16_t* __restrict__ x, W4Ws w, W4Dims d) {
+    __shared__ int count[kMaxE];
+    __shared__ uint16_t member[MOONEP_W4_MAX_PAIRS];
+    __shared__ int lds[4];
+    const int pairs = d.T * d.K, e = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = tid; i < d.E; i += 256) count[i] = 0;
+    __syncthreads();
+    for (int p = tid; p < pairs; p += 256) {
+        const int id = topk[p];
+        if ((unsigned)id < (unsigned)d.E) atomicAdd(&count[id], 1);
+    }
+    __syncthreads();
+    const int n = count[e];
+    int tiles = 0, chunks = 0;
+    for (int i = tid; i < e; i += 256) {
+        tiles += (count[i] + kTile - 1) / kTile;
+        chunks += (count[i] + kChunk4 - 1) / kChunk4;
+    }
+    tiles = block_sum(tiles, lds);
+    chunks = block_sum(chunks, lds);
+    if (e == d.E - 1 && blockIdx.x == 0 && tid == 0) w.nchunk[0] = chunks + (n + kChunk4 - 1) / kChunk4;
+    if (n == 0) return;
+    for (int p0 = 0, got = 0; p0 < pairs && got < n; p0 += 256) {
+        const int p = p0 + tid;
+        const bool hit = p < pairs && topk[p] == e;
+        const unsigned long long hits = __ballot(hit);
+        __syncthreads();
+        if (lane == 0) lds[wave] = __popcll(hits);
+        __syncthreads();
+        int at = got + __popcll(hits & ((1ull << lane) - 1));
+        for (int i = 0; i < wave; ++i) at += lds[i];
+        if (hit) member[at] = (uint16_t)p;
+        got += (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int r = tid; r < n; r += 256) w.pair[tiles * kTile + r] = member[r];
+        for (int i = tid; i * kChunk4 < n; i += 256)
+            w.chunks[chunks + i] = Chunk{e, tiles + i * kRowTiles, min(kChunk4, n - i * kChunk4), 0};
+    }
+    const int kb_all = (d.H + kBlock - 1) / kBlock, kb0 = blockIdx.x * 4;
+    const int per_tile = min(4, kb_all - kb0) * 256, tiles_here = (n + kTile - 1) / kTile;
+    for (int v = tid; v < tiles_here * per_tile; v += 256) {
+        const int rt = v / per_tile, s = v % per_tile, l = s & 63, i = (s >> 6) & 3, kb = kb0 + (s >> 8);
+        const int r = rt * kTile + (l & 15), k = kb * kBlock + (l >> 4) * kGroup + i * 8;
+        if (r >= n || k >= d.H) continue;
+        const int token = member[r] / d.K;
+        w.rows[((size_t)(tiles + rt) * kb_all + kb) * 256 + (s & 255)] =
+            *reinterpret_cast<const uint4*>(x + (size_t)token * d.H + k);
+    }
+}
+
+// acc over the whole input direction for RT row tiles whose operands start at `rows`.
+template <int RT, int NT>
+__device__ __forceinline__ void multiply_rows(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, const uint4* rows) {
+    const uint4* mine = rows + (threadIdx.x & 63);
+    multiply<RT, NT>(acc, m, tile, 0, 1, [&](int r, int kb, int i, bool in) {
+        const uint4 v = mine[((size_t)r * m.kb + kb) * 256 + i * 64];
+        return in ? v : make_uint4(0, 0, 0, 0);
+    });
+}
+
+// act for one chunk; a wave takes 16 columns.
+template <int RT>
+__device__ __forceinline__ void up_tiles(const W4Mat& m, const W4Ws& w, const W4Dims& d, const Chunk& ch, int col) {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    const size_t g = (size_t)ch.expert * m.nb + col, tile[2] = {g, g + m.nb / 2};
+    f32x4_t acc[RT][2];
+    multiply_rows<RT, 2>(acc, m, tile, w.rows + (size_t)ch.tile * m.kb * 256);
+    const int kb_all = (d.I + kBlock - 1) / kBlock, k = col * kTile + c;
+    const int kb = k / kBlock, lane0 = k % kBlock / kGroup * 16, step = k % kGroup / 8, j = k % 8;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = r * kTile + q * 4 + i;
+            if (row >= ch.rows) continue;
+            uint16_t lead, rest;
+            two_terms(swiglu(acc[r][0][i], acc[r][1][i]), lead, rest);
+            const size_t half = (size_t)ch.tile * 2 + row / 8;
+            uint16_t* o = w.act + (((half * kb_all + kb) * 4 + step) * 64 + lane0 + row % 8 * 2) * 8 + j;
+            o[0] = lead;
+            o[8] = rest;
+        }
+}
+
+__global__ __launch_bounds__(256) void w4_up_kernel(W4Mat m, W4Ws w, W4Dims d) {
     if ((int)blockIdx.y >= w.nchunk[0]) return;
     const Chunk ch = w.chunks[blockIdx.y];
-    const int lane = threadIdx.x, c = lane & 15, q = lane >> 4;
-    const size_t tile = (size_t)ch.expert * m.nb + blockIdx.x;
-    for (int r0 = 0; r0 < ch.rows; r0 += 8) {
-        const int term = min(r0 * 2 + c, ch.rows * 2 - 1);
-        const f32x4_t v = w4_tile(w.act + ((size_t)ch.first * 2 + term) * d.I + q * kGroup, m, tile);
+    const int col = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (col >= d.I / kTile) return;
+    const int rt = (ch.rows + kTile - 1) / kTile;
+    if (rt == 1) up_tiles<1>(m, w, d, ch, col);
+    else if (rt == 2) up_tiles<2>(m, w, d, ch, col);
+    else if (rt == 3) up_tiles<3>(m, w, d, ch, col);
+    else up_tiles<4>(m, w, d, ch, col);
+}
+
+// y for one chunk; a wave takes 32 columns.
+template <int RT>
+__device__ __forceinline__ void down_tiles(const W4Mat& m, const W4Ws& w, const W4Dims& d, const Chunk& ch, int col) {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    const size_t g = (size_t)ch.expert * m.nb + col, tile[2] = {g, g + 1};
+    f32x4_t acc[RT][2];
+    multiply_rows<RT, 2>(acc, m, tile, reinterpret_cast<const uint4*>(w.act) + (size_t)ch.tile * 2 * m.kb * 256);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = r0 + q * 2 + i;
-            if (r < ch.rows) w.y[(size_t)w.pair[ch.first + r] * d.H + blockIdx.x * 16 + c] = v[2 * i] + v[2 * i + 1];
+            const int row = r * 8 + q * 2 + i;
+            if (row >= ch.rows) continue;
+            float* o = w.y + (size_t)w.pair[ch.tile * kTile + row] * d.H + col * kTile + c;
+            o[0] = acc[r][0][2 * i] + acc[r][0][2 * i + 1];
+            o[kTile] = acc[r][1][2 * i] + acc[r][1][2 * i + 1];
         }
-    }
+}
+
+__global__ __launch_bounds__(256) void w4_down_kernel(W4Mat m, W4Ws w, W4Dims d) {
+    if ((int)blockIdx.y >= w.nchunk[0]) return;
+    const Chunk ch = w.chunks[blockIdx.y];
+    const int col = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 2;
+    if (col >= d.H / kTile) return;
+    const int rt = (ch.rows + kTile / 2 - 1) / (kTile / 2);
+    if (rt == 1) down_tiles<1>(m, w, d, ch, col);
+    else if (rt == 2) down_tiles<2>(m, w, d, ch, col);
+    else if (rt <= 4) down_tiles<4>(m, w, d, ch, col);
+    else down_tiles<8>(m, w, d, ch, col);
 }
 
 // out = sum over k of gate * y, in k order, skipping ids that name no expert.
 __global__ __launch_bounds__(256) void w4_join_kernel(const int32_t* __restrict__ topk, const float* __restrict__ gates,
-                                                      W4Ws w, uint16_t* __restrict__ out, W4Dims d) {
+                                                      const float4* __restrict__ y, uint2* __restrict__ out, W4Dims d) {
     const int h = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
-    if (h >= d.H) return;
-    float s = 0.0f;
-    for (int k = 0; k < d.K; ++k) {
-        const int p = t * d.K + k;
-        if ((unsigned)topk[p] < (unsigned)d.E) s += gates[p] * w.y[(size_t)p * d.H + h];
+    if (h >= d.H / 4) return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p = t * d.K; p < (t + 1) * d.K; ++p) {
+        if ((unsigned)topk[p] >= (unsigned)d.E) continue;
+        const float4 v = y[(size_t)p * (d.H / 4) + h];
+        const float g = gates[p];
+        s.x += g * v.x;
+        s.y += g * v.y;
+        s.z += g * v.z;
+        s.w += g * v.w;
     }
-    out[(size_t)t * d.H + h] = (uint16_t)pack_bf16(s, 0.0f);
+    out[(size_t)t * (d.H / 4) + h] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
 // ---------------------------------------------------------------------------
@@ -264,9 +518,6 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __rest
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-
-static int blocks_of(int kin) { return (kin + kBlock - 1) / kBlock; }
-static int fours_of(int kin) { return (blocks_of(kin) + 3) / 4; }
 
 static W4Mat w4_mat(const void* codes, const void* scales, int kin, int n) {
     return W4Mat{static_cast<const uint4*>(codes), static_cast<const uint32_t*>(scales), kin, blocks_of(kin),
@@ -340,15 +591,24 @@ extern "C" int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, con
     w4_ws_layout(d, ws, &w);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const W4Mat up = w4_mat(w13_codes, w13_scales, d.H, 2 * d.I), down = w4_mat(w2_codes, w2_scales, d.I, d.H);
-    hipLaunchKernelGGL(w4_group_kernel, dim3(1), dim3(1024), 0, s, topk, w, d.T * d.K, d.E);
+    const uint16_t* xr = static_cast<const uint16_t*>(x);
+    if (d.T * d.K <= kFewPairs) {
+        hipLaunchKernelGGL(w4_few_up_kernel, dim3(d.I / kTile, std::min(d.T * d.K, d.E)), dim3(64 * kUpWaves), 0, s,
+                           topk, xr, up, w.act, d);
+        MOONEP_LAUNCH_CHECK();
+        hipLaunchKernelGGL(w4_few_down_kernel, dim3(d.H / kTile), dim3(64 * kDownWaves), 0, s, topk, gates, w.act,
+                           down, static_cast<uint16_t*>(out), d);
+        MOONEP_LAUNCH_CHECK();
+        return MOONEP_OK;
+    }
+    hipLaunchKernelGGL(w4_gather_kernel, dim3(fours_of(d.H), d.E), dim3(256), 0, s, topk, xr, w, d);
     MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(w4_up_kernel, dim3(d.I / 16, w.max_chunks), dim3(64), 0, s, static_cast<const uint16_t*>(x), up,
-                       w, d);
+    hipLaunchKernelGGL(w4_up_kernel, dim3((d.I / kTile + 3) / 4, w.max_chunks), dim3(256), 0, s, up, w, d);
     MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(w4_down_kernel, dim3(d.H / 16, w.max_chunks), dim3(64), 0, s, down, w, d);
+    hipLaunchKernelGGL(w4_down_kernel, dim3((d.H / kTile + 7) / 8, w.max_chunks), dim3(256), 0, s, down, w, d);
     MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(w4_join_kernel, dim3((d.H + 255) / 256, d.T), dim3(256), 0, s, topk, gates, w,
-                       static_cast<uint16_t*>(out), d);
+    hipLaunchKernelGGL(w4_join_kernel, dim3((d.H / 4 + 255) / 256, d.T), dim3(256), 0, s, topk, gates,
+                       reinterpret_cast<const float4*>(w.y), static_cast<uint2*>(out), d);
     MOONEP_LAUNCH_CHECK();
     return MOONEP_OK;
 }
