@@ -7,15 +7,16 @@
 // bf16 values, exactly, in one instruction; matrix instructions multiply them by the tokens' rows.
 //
 // Pairs (token, k) are grouped by expert, so that an expert's weights are read once for all its
-// tokens.  A lane (column c = lane % 16, group q = lane / 16) of a wave loads 16 bytes: the 32 codes
-// of group q of column c in a block of 128 input values.  The matrix instruction of step m
-// multiplies values q * 32 + m * 8 .. + 8 of each group, which is an order of the input direction
-// that both operands share.
+// tokens; each workgroup finds its expert's pairs among the ids itself.  A lane (column c = lane % 16,
+// group q = lane / 16) of a wave loads 16 bytes: the 32 codes of group q of column c in a block of
+// 128 input values.  The matrix instruction of step i multiplies values q * 32 + i * 8 .. + 8 of each
+// group, which is an order of the input direction that both operands share.
 //
-// Up to 64 pairs, one wave can look at all ids at once: each workgroup finds its own group, and rows
-// are read where they lie.  Beyond, a first kernel groups the pairs and lays their rows out in the
-// order in which the matrix instruction's operand reads them.
+// Rows go through LDS, and not from global memory to the operand: loads return in order, so a wait
+// for rows would be a wait for the weights that were asked for before them.
 #include "common.h"
+
+#include <type_traits>
 
 namespace moonep {
 
@@ -24,10 +25,9 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kGroup = 32;           // values a scale
 constexpr int kBlock = 128;          // input values of one wave's load
+constexpr int kFour = 4 * kBlock;    // input values of four blocks, whose scales come in one load
 constexpr int kTile = 16;            // rows a matrix instruction takes, columns of a tile
-constexpr int kRowTiles = 4;         // row tiles of a chunk
-constexpr int kChunk4 = kTile * kRowTiles;
-constexpr int kFewPairs = 64;
+constexpr int kFewPairs = 32;
 
 struct W4Dims {
     int T, K, E, H, I;
@@ -40,50 +40,27 @@ struct W4Mat {
     int kin, kb, sb, nb;
 };
 
-// A run of an expert's pairs, at most kChunk4 of them, in row tiles of their own.
-struct Chunk {
-    int32_t expert, tile, rows, pad;
-};
-
-// Scratch.  Few pairs use act alone, as [T*K][2][I]; otherwise
+// Scratch.
 struct W4Ws {
-    int32_t* nchunk;                 // [1]
-    Chunk* chunks;                   // [max_chunks]
-    int32_t* pair;                   // [max_tiles][16] the pair of each row
-    uint4* rows;                     // [max_tiles][H/128][4 steps][64 lanes] x, as operands
-    uint16_t* act;                   // [max_tiles * 2][I/128][4 steps][64 lanes][8]: a row tile's 16
-                                     // activations in two bf16 terms, a pair's terms next to each other
-    float* y;                        // [T*K][H] by pair
-    int max_chunks;
+    uint16_t* act;                   // [T*K][2][I] bf16: leading and trailing term
+    float* y;                        // [T*K][H]; none for few pairs
 };
 
 static int blocks_of(int kin) { return (kin + kBlock - 1) / kBlock; }
 static int fours_of(int kin) { return (blocks_of(kin) + 3) / 4; }
 
 static size_t w4_ws_layout(const W4Dims& d, void* base, W4Ws* ws) {
-    const size_t pairs = (size_t)d.T * d.K, experts = std::min<size_t>(pairs, d.E);
-    const bool few = pairs <= kFewPairs;
-    // an expert leaves less than one tile, and less than one chunk, partly empty
-    const size_t tiles = few ? 0 : experts + pairs / kTile;
-    W4Ws w{};
-    w.max_chunks = (int)(experts + pairs / kChunk4);
-    size_t off = 0;
-    auto take = [&](size_t bytes) -> void* {
-        void* p = base ? static_cast<char*>(base) + off : nullptr;
-        off = align_up(off + bytes, 256);
-        return p;
-    };
-    w.nchunk = (int32_t*)take(4);
-    w.chunks = (Chunk*)take(w.max_chunks * sizeof(Chunk));
-    w.pair = (int32_t*)take(tiles * kTile * 4);
-    w.rows = (uint4*)take(tiles * blocks_of(d.H) * 4096);
-    // one tile more: the second product takes an expert's last tiles by two, and reads (without using
-    // it) the tile after an odd one
-    w.act = (uint16_t*)take(few ? pairs * 2 * d.I * 2 : (tiles + 1) * 2 * blocks_of(d.I) * 4096);
-    w.y = (float*)take(few ? 0 : pairs * d.H * 4);
-    if (ws) *ws = w;
-    return off;
+    const size_t pairs = (size_t)d.T * d.K;
+    const size_t act = align_up(pairs * 2 * d.I * 2, 256);
+    if (ws) {
+        ws->act = static_cast<uint16_t*>(base);
+        ws->y = reinterpret_cast<float*>(static_cast<char*>(base) + act);
+    }
+    return act + (pairs <= kFewPairs ? 0 : pairs * d.H * 4);
 }
+
+// The wave's number, known to be the same for all its lanes: what follows from it stays in scalar registers.
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // ---------------------------------------------------------------------------
 // products
@@ -117,28 +94,55 @@ struct Four {
     uint32_t scales[NT];
 };
 
+// Where a lane's codes and scales of a column tile lie.
 template <int NT>
-__device__ __forceinline__ void load_four(Four<NT>& f, const W4Mat& m, const size_t* tile, int four) {
-    const int lane = threadIdx.x & 63;
+struct Weights {
+    const uint4* codes[NT];          // of the tile; the lane is added at each load, to keep these scalar
+    const uint32_t* scales[NT];
+    int kb, sb;
+
+    __device__ __forceinline__ Weights(const W4Mat& m, const size_t* tile) : kb(m.kb), sb(m.sb) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const uint4* c = m.codes + (tile[t] * m.kb + four * 4) * 64 + lane;
+        for (int t = 0; t < NT; ++t) {
+            codes[t] = m.codes + tile[t] * m.kb * 64;
+            scales[t] = m.scales + tile[t] * m.sb * 64;
+        }
+    }
+
+    __device__ __forceinline__ void load_scales(Four<NT>& f, int four) const {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) f.scales[t] = (scales[t] + four * 64)[threadIdx.x & 63];
+    }
+
+    __device__ __forceinline__ void load_codes(Four<NT>& f, int four, int j) const {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) f.codes[t][j] = ld_nt(codes[t] + (four * 4 + j) * 64 + (threadIdx.x & 63));
+    }
+
+    __device__ __forceinline__ void load(Four<NT>& f, int four, int blocks) const {
+        load_scales(f, four);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (four * 4 + j < m.kb) f.codes[t][j] = ld_nt(c + j * 64);
-        f.scales[t] = m.scales[(tile[t] * m.sb + four) * 64 + lane];
+            if (j < blocks) load_codes(f, four, j);
     }
-}
+};
 
-// acc[r][t] += rows * weights of four blocks; a(r, kb, i, in) is the row operand of row tile r, block
-// kb and step i, of which lanes with `in` false are past the end of the input direction.
-template <int RT, int NT, class A>
-__device__ __forceinline__ void multiply_four(f32x4_t (&acc)[RT][NT], const Four<NT>& f, const W4Mat& m, int four, A a) {
-    auto block = [&](int j, bool in) {
-        const int kb = four * 4 + j;
+// acc[r][t] += rows * weights of four blocks, or of the first `blocks` of them (a constant 4 but at the
+// end); a(r, j, i) is the operand of row tile r, block j and step i.  With THEN, each block's codes make
+// room for the same block's of four `then`.
+template <bool THEN, int RT, int NT, class A>
+__device__ __forceinline__ void multiply_four(f32x4_t (&acc)[RT][NT], Four<NT>& f, const Weights<NT>& w, int blocks,
+                                              int then, A a) {
+    uint32_t scales[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) scales[t] = f.scales[t];
+    if constexpr (THEN) w.load_scales(f, then);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j >= blocks) break;
         float s[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = scale_of(f.scales[t], j);
+        for (int t = 0; t < NT; ++t) s[t] = scale_of(scales[t], j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             bf16x8_t b[NT];
@@ -146,41 +150,56 @@ __device__ __forceinline__ void multiply_four(f32x4_t (&acc)[RT][NT], const Four
             for (int t = 0; t < NT; ++t) b[t] = widen(dword(f.codes[t][j], i), s[t]);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const bf16x8_t v = __builtin_bit_cast(bf16x8_t, a(r, kb, i, in));
+                const bf16x8_t v = __builtin_bit_cast(bf16x8_t, a(r, j, i));
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[t], acc[r][t], 0, 0, 0);
             }
         }
-    };
-    if ((four + 1) * 4 * kBlock <= m.kin) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) block(j, true);
-    } else {
-        const int q = (threadIdx.x & 63) >> 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (four * 4 + j < m.kb) block(j, (four * 4 + j) * kBlock + q * kGroup < m.kin);
+        if constexpr (THEN) w.load_codes(f, then, j);
+        // without it all blocks' operands are read ahead, into registers that spill
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-// acc = rows times NT column tiles over fours first, first + step, ...; the next four's loads are in
-// flight while one is multiplied.
-template <int RT, int NT, class A>
+// The order of a product over fours first, first + step, ...: fetch(four, whole) asks for the rows of
+// four blocks, place() puts them into LDS.  Rows, then weights, of the next four are on their way while
+// one is multiplied.  The loop has no branches: a load whose register meets another value at a join of
+// two paths would be waited for there.
+template <int RT, int NT, class Fetch, class Place, class A>
 __device__ __forceinline__ void multiply(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, int first,
-                                         int step, A a) {
+                                         int step, Fetch fetch, Place place, A a) {
+    const Weights<NT> w(m, tile);
+    const int whole = m.kin / kFour;
+    Four<NT> f;
+    int four = first;
+    if (four < whole) {
+        fetch(four, true);
+        w.load(f, four, 4);
+        for (; four + step < whole; four += step) {
+            place();
+            fetch(four + step, true);
+            multiply_four<true>(acc, f, w, 4, four + step, a);
+        }
+        place();
+        multiply_four<false>(acc, f, w, 4, 0, a);
+        four += step;
+    }
+    if (four < m.sb) {               // the end of the input direction, in part
+        const int blocks = m.kb - four * 4;
+        fetch(four, false);
+        w.load(f, four, blocks);
+        place();
+        multiply_four<false>(acc, f, w, blocks, 0, a);
+    }
+}
+
+template <int RT, int NT>
+__device__ __forceinline__ void clear(f32x4_t (&acc)[RT][NT]) {
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[r][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (first >= m.sb) return;
-    Four<NT> next;
-    load_four(next, m, tile, first);
-    for (int four = first; four < m.sb; four += step) {
-        const Four<NT> now = next;
-        if (four + step < m.sb) load_four(next, m, tile, four + step);
-        multiply_four<RT, NT>(acc, now, m, four, a);
-    }
 }
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
@@ -214,16 +233,52 @@ __device__ __forceinline__ int member_pair(unsigned long long members) {
     return __builtin_amdgcn_ds_permute(to * 4, lane);
 }
 
+// acc = up to eight rows times NT column tiles, over fours first, first + step, ...  The wave keeps
+// RN rows of four blocks in `lds` (RN KiB of its own), 16-byte pieces swapped by row so that equal
+// pieces of different rows lie in different banks.  Rows past RN repeat the last.
+template <int RN, int NT, class Row>
+__device__ __forceinline__ void multiply_few(f32x4_t (&acc)[1][NT], const W4Mat& m, const size_t* tile, int first,
+                                             int step, uint4* lds, Row row) {
+    const int lane = threadIdx.x & 63, q = lane >> 4, mine = min(lane & 15, RN - 1);
+    uint4 a[RN];
+    clear(acc);
+    multiply<1, NT>(
+        acc, m, tile, first, step,
+        [&](int four, bool whole) {
+            const int k = four * kFour + lane * 8;
+#pragma unroll
+            for (int r = 0; r < RN; ++r)
+                a[r] = whole || k < m.kin ? *reinterpret_cast<const uint4*>(row(r) + k) : make_uint4(0, 0, 0, 0);
+        },
+        [&] {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int r = 0; r < RN; ++r) lds[r * 64 + (lane ^ r)] = a[r];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        },
+        [&](int, int j, int i) { return lds[mine * 64 + ((j * 16 + q * 4 + i) ^ mine)]; });
+}
+
+// Calls f with the number of rows, 1, 2, 4 or 8, that n rows at most eight are computed as.
+template <class F>
+__device__ __forceinline__ void with_rows(int n, F f) {
+    if (n <= 1) f(std::integral_constant<int, 1>{});
+    else if (n <= 2) f(std::integral_constant<int, 2>{});
+    else if (n <= 4) f(std::integral_constant<int, 4>{});
+    else f(std::integral_constant<int, 8>{});
+}
+
 // act = silu(x G) * (x U) for one expert and 16 columns.  The waves deal out the input direction and
 // join their sums in order.  blockIdx.y: a pair, that leads its expert's group if it is the first of
 // it, or an expert where there are fewer experts than pairs.
-constexpr int kUpWaves = 7;
+constexpr int kUpWaves = 4;
 
-__global__ __launch_bounds__(64 * kUpWaves) void w4_few_up_kernel(const int32_t* __restrict__ topk,
+__global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32_t* __restrict__ topk,
                                                                   const uint16_t* __restrict__ x, W4Mat m,
                                                                   uint16_t* __restrict__ act, W4Dims d) {
-    __shared__ float4 part[kUpWaves][2][64];
-    const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+    __shared__ uint4 lds[kUpWaves][8 * 64];
+    const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), c = lane & 15;
     const int id = pair_expert(topk, pairs, d.E);
     const int e = pairs <= d.E ? __builtin_amdgcn_readlane(id, blockIdx.y) : blockIdx.y;
     const unsigned long long members = __ballot(id == e);
@@ -231,27 +286,29 @@ __global__ __launch_bounds__(64 * kUpWaves) void w4_few_up_kernel(const int32_t*
     if (pairs <= d.E && __ffsll(members) - 1 != (int)blockIdx.y) return;
     const int n = __popcll(members), pair = member_pair(members);
     const size_t g = (size_t)e * m.nb + blockIdx.x, tile[2] = {g, g + m.nb / 2};
-    for (int r0 = 0; r0 < n; r0 += kTile) {
-        // rows past the group's compute with its last one; nothing of them is stored
-        const int token = __shfl(pair, min(r0 + c, n - 1), 64) / d.K;
-        const uint16_t* row = x + (size_t)token * d.H + q * kGroup;
+    for (int r0 = 0; r0 < n; r0 += 8) {
+        const int rows = min(8, n - r0);
         f32x4_t acc[1][2];
-        multiply<1, 2>(acc, m, tile, wave, kUpWaves, [&](int, int kb, int i, bool in) {
-            return in ? *reinterpret_cast<const uint4*>(row + kb * kBlock + i * 8) : make_uint4(0, 0, 0, 0);
-        });
         __syncthreads();
+        with_rows(rows, [&](auto rn) {
+            multiply_few<rn.value, 2>(acc, m, tile, wave, kUpWaves, lds[wave], [&](int r) {
+                return x + (size_t)(__builtin_amdgcn_readlane(pair, min(r0 + r, n - 1)) / d.K) * d.H;
+            });
+        });
+        // the sums take the place of the wave's rows
+        float4* part = reinterpret_cast<float4*>(lds[wave]);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            part[wave][t][lane] = make_float4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]);
+            part[t * 64 + lane] = make_float4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]);
         __syncthreads();
         const int r = threadIdx.x >> 4, to = __shfl(pair, min(r0 + r, n - 1), 64);
-        if (r < min(kTile, n - r0)) {
+        if (r < rows) {
             const int at = (r / 4 * 16 + c) * 4 + r % 4;
             float gate = 0.0f, up = 0.0f;
 #pragma unroll
             for (int w = 0; w < kUpWaves; ++w) {
-                gate += reinterpret_cast<const float*>(part[w][0])[at];
-                up += reinterpret_cast<const float*>(part[w][1])[at];
+                gate += reinterpret_cast<const float*>(lds[w])[at];
+                up += reinterpret_cast<const float*>(lds[w])[256 + at];
             }
             uint16_t lead, rest;
             two_terms(swiglu(gate, up), lead, rest);
@@ -263,15 +320,16 @@ __global__ __launch_bounds__(64 * kUpWaves) void w4_few_up_kernel(const int32_t*
 }
 
 // out for 16 columns and all tokens: the waves take the experts in turn, each group's rows go to LDS,
-// and a token's are joined in k order.  The rows of a matrix instruction are the two terms of 8 pairs.
+// and a token's are joined in k order.  The rows of a matrix instruction are the two terms of 4 pairs.
 constexpr int kDownWaves = 8;
 
-__global__ __launch_bounds__(64 * kDownWaves) void w4_few_down_kernel(const int32_t* __restrict__ topk,
+__global__ __launch_bounds__(64 * kDownWaves, 3) void w4_few_down_kernel(const int32_t* __restrict__ topk,
                                                                       const float* __restrict__ gates,
                                                                       const uint16_t* __restrict__ act, W4Mat m,
                                                                       uint16_t* __restrict__ out, W4Dims d) {
+    __shared__ uint4 lds[kDownWaves][8 * 64];
     __shared__ float y[kFewPairs][kTile];
-    const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+    const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), c = lane & 15, q = lane >> 4;
     const int id = pair_expert(topk, pairs, d.E);
     unsigned long long left = __ballot(id >= 0);
     for (int turn = 0; left; ++turn) {
@@ -281,17 +339,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void w4_few_down_kernel(const int3
         if (turn % kDownWaves != wave) continue;
         const int n = __popcll(members), pair = member_pair(members);
         const size_t tile[1] = {(size_t)e * m.nb + blockIdx.x};
-        for (int r0 = 0; r0 < n; r0 += kTile / 2) {
-            const int term = min(r0 * 2 + c, n * 2 - 1);
-            const uint16_t* row = act + ((size_t)__shfl(pair, term / 2, 64) * 2 + term % 2) * d.I + q * kGroup;
+        for (int r0 = 0; r0 < n; r0 += 4) {
             f32x4_t acc[1][1];
-            multiply<1, 1>(acc, m, tile, 0, 1, [&](int, int kb, int i, bool in) {
-                return in ? *reinterpret_cast<const uint4*>(row + kb * kBlock + i * 8) : make_uint4(0, 0, 0, 0);
+            with_rows(min(8, (n - r0) * 2), [&](auto rn) {
+                multiply_few<rn.value, 1>(acc, m, tile, 0, 1, lds[wave], [&](int r) {
+                    const int p = __builtin_amdgcn_readlane(pair, min(r0 + r / 2, n - 1));
+                    return act + ((size_t)p * 2 + r % 2) * d.I;
+                });
             });
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = r0 + q * 2 + i, p = __shfl(pair, min(r, n - 1), 64);
-                if (r < n) y[p][c] = acc[0][0][2 * i] + acc[0][0][2 * i + 1];
+                if (q < 2 && r < n) y[p][c] = acc[0][0][2 * i] + acc[0][0][2 * i + 1];
             }
         }
     }
@@ -309,144 +368,182 @@ __global__ __launch_bounds__(64 * kDownWaves) void w4_few_down_kernel(const int3
 // many pairs
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ int block_sum(int v, int* lds) {   // workgroup of 256
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
-}
-
-// Expert blockIdx.y's pairs in order, and four blocks of their rows as operands.  Every workgroup
-// counts all pairs itself, so that one launch does.
-__global__ __launch_bounds__(256) void w4_gather_kernel(const int32_t* __restrict__ topk,
-                                                        const uint16_t* __restrict__ x, W4Ws w, W4Dims d) {
-    __shared__ int count[kMaxE];
-    __shared__ uint16_t member[MOONEP_W4_MAX_PAIRS];
-    __shared__ int lds[4];
-    const int pairs = d.T * d.K, e = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < d.E; i += 256) count[i] = 0;
-    __syncthreads();
-    for (int p = tid; p < pairs; p += 256) {
-        const int id = topk[p];
-        if ((unsigned)id < (unsigned)d.E) atomicAdd(&count[id], 1);
+// Pairs first .. first + most of expert e, in order, into member[]; returns how many.  Workgroup of 256.
+__device__ __forceinline__ int find_members(const int32_t* __restrict__ topk, int pairs, int e, int first, int most,
+                                            int* member) {
+    __shared__ int before[MOONEP_W4_MAX_PAIRS / 64 + 1];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int waves = (pairs + 63) / 64;
+    for (int i = tid >> 6; i < waves; i += 4) {
+        const int p = i * 64 + lane;
+        const unsigned long long hits = __ballot(p < pairs && topk[p] == e);
+        if (lane == 0) before[i + 1] = __popcll(hits);
     }
     __syncthreads();
-    const int n = count[e];
-    int tiles = 0, chunks = 0;
-    for (int i = tid; i < e; i += 256) {
-        tiles += (count[i] + kTile - 1) / kTile;
-        chunks += (count[i] + kChunk4 - 1) / kChunk4;
+    if (tid < 64) {                  // prefix sums, 64 counts at a time
+        int sum = 0;
+        for (int i0 = 0; i0 < waves; i0 += 64) {
+            int v = i0 + lane < waves ? before[i0 + lane + 1] : 0;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int u = __shfl_up(v, o, 64);
+                if (lane >= o) v += u;
+            }
+            if (i0 + lane < waves) before[i0 + lane + 1] = sum + v;
+            sum += __shfl(v, 63, 64);
+        }
+        if (lane == 0) before[0] = 0;
     }
-    tiles = block_sum(tiles, lds);
-    chunks = block_sum(chunks, lds);
-    if (e == d.E - 1 && blockIdx.x == 0 && tid == 0) w.nchunk[0] = chunks + (n + kChunk4 - 1) / kChunk4;
-    if (n == 0) return;
-    for (int p0 = 0, got = 0; p0 < pairs && got < n; p0 += 256) {
-        const int p = p0 + tid;
+    __syncthreads();
+    const int n = min(most, before[waves] - first);
+    if (n <= 0) return 0;
+    for (int i = tid >> 6; i < waves; i += 4) {
+        if (before[i + 1] <= first || before[i] >= first + n) continue;
+        const int p = i * 64 + lane;
         const bool hit = p < pairs && topk[p] == e;
         const unsigned long long hits = __ballot(hit);
-        __syncthreads();
-        if (lane == 0) lds[wave] = __popcll(hits);
-        __syncthreads();
-        int at = got + __popcll(hits & ((1ull << lane) - 1));
-        for (int i = 0; i < wave; ++i) at += lds[i];
-        if (hit) member[at] = (uint16_t)p;
-        got += (lds[0] + lds[1]) + (lds[2] + lds[3]);
+        const int at = before[i] + __popcll(hits & ((1ull << lane) - 1)) - first;
+        if (hit && at >= 0 && at < n) member[at] = p;
     }
     __syncthreads();
-    if (blockIdx.x == 0) {
-        for (int r = tid; r < n; r += 256) w.pair[tiles * kTile + r] = member[r];
-        for (int i = tid; i * kChunk4 < n; i += 256)
-            w.chunks[chunks + i] = Chunk{e, tiles + i * kRowTiles, min(kChunk4, n - i * kChunk4), 0};
-    }
-    const int kb_all = (d.H + kBlock - 1) / kBlock, kb0 = blockIdx.x * 4;
-    const int per_tile = min(4, kb_all - kb0) * 256, tiles_here = (n + kTile - 1) / kTile;
-    for (int v = tid; v < tiles_here * per_tile; v += 256) {
-        const int rt = v / per_tile, s = v % per_tile, l = s & 63, i = (s >> 6) & 3, kb = kb0 + (s >> 8);
-        const int r = rt * kTile + (l & 15), k = kb * kBlock + (l >> 4) * kGroup + i * 8;
-        if (r >= n || k >= d.H) continue;
-        const int token = member[r] / d.K;
-        w.rows[((size_t)(tiles + rt) * kb_all + kb) * 256 + (s & 255)] =
-            *reinterpret_cast<const uint4*>(x + (size_t)token * d.H + k);
-    }
+    return n;
 }
 
-// acc over the whole input direction for RT row tiles whose operands start at `rows`.
+// acc = RT row tiles times two column tiles, a wave's own; the workgroup's 256 threads bring the rows
+// of four blocks to LDS, each 16 bytes of a row at a time: row[t] is the thread's row of tile t at its
+// piece.  Where a piece lies in LDS is swapped by row, so that neither side meets a bank twice.
 template <int RT, int NT>
-__device__ __forceinline__ void multiply_rows(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, const uint4* rows) {
-    const uint4* mine = rows + (threadIdx.x & 63);
-    multiply<RT, NT>(acc, m, tile, 0, 1, [&](int r, int kb, int i, bool in) {
-        const uint4 v = mine[((size_t)r * m.kb + kb) * 256 + i * 64];
-        return in ? v : make_uint4(0, 0, 0, 0);
-    });
+__device__ __forceinline__ void multiply_many(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, uint4* lds,
+                                              const uint16_t* const* row) {
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+    const int piece = tid & 15, swapped = piece % 4 * 64 + piece / 4 * 16 + ((tid >> 4) ^ (piece % 4 * 4 + piece / 4));
+    uint4 a[RT][4];
+    clear(acc);
+    multiply<RT, NT>(
+        acc, m, tile, 0, 1,
+        [&](int four, bool whole) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = four * kFour + j * kBlock;
+                    a[t][j] = whole || k + piece * 8 < m.kin ? *reinterpret_cast<const uint4*>(row[t] + k)
+                                                             : make_uint4(0, 0, 0, 0);
+                }
+        },
+        [&] {
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) lds[(t * 4 + j) * 256 + swapped] = a[t][j];
+            __syncthreads();
+        },
+        [&](int t, int j, int i) { return lds[(t * 4 + j) * 256 + i * 64 + q * 16 + (c ^ (i * 4 + q))]; });
 }
 
-// act for one chunk; a wave takes 16 columns.
+// act for one expert; a wave takes kUpCols column tiles of 16.
+constexpr int kUpCols = 1, kDownCols = 2;
+
 template <int RT>
-__device__ __forceinline__ void up_tiles(const W4Mat& m, const W4Ws& w, const W4Dims& d, const Chunk& ch, int col) {
-    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-    const size_t g = (size_t)ch.expert * m.nb + col, tile[2] = {g, g + m.nb / 2};
-    f32x4_t acc[RT][2];
-    multiply_rows<RT, 2>(acc, m, tile, w.rows + (size_t)ch.tile * m.kb * 256);
-    const int kb_all = (d.I + kBlock - 1) / kBlock, k = col * kTile + c;
-    const int kb = k / kBlock, lane0 = k % kBlock / kGroup * 16, step = k % kGroup / 8, j = k % 8;
+__device__ __forceinline__ void up_tiles(const uint16_t* x, const W4Mat& m, uint16_t* act, const W4Dims& d, int e,
+                                         const int* member, int n, uint4* lds) {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, last = d.I / kTile - 1;
+    const int col = (blockIdx.x * 4 + wave_of()) * kUpCols;
+    const uint16_t* row[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int t = 0; t < RT; ++t) {
+        const int r = min(t * kTile + (int)(threadIdx.x >> 4), n - 1);
+        row[t] = x + (size_t)(member[r] / d.K) * d.H + (threadIdx.x & 15) * 8;
+    }
+    size_t tile[2 * kUpCols];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = r * kTile + q * 4 + i;
-            if (row >= ch.rows) continue;
-            uint16_t lead, rest;
-            two_terms(swiglu(acc[r][0][i], acc[r][1][i]), lead, rest);
-            const size_t half = (size_t)ch.tile * 2 + row / 8;
-            uint16_t* o = w.act + (((half * kb_all + kb) * 4 + step) * 64 + lane0 + row % 8 * 2) * 8 + j;
-            o[0] = lead;
-            o[8] = rest;
-        }
+    for (int u = 0; u < kUpCols; ++u) {
+        tile[2 * u] = (size_t)e * m.nb + min(col + u, last);
+        tile[2 * u + 1] = tile[2 * u] + m.nb / 2;
+    }
+    f32x4_t acc[RT][2 * kUpCols];
+    multiply_many(acc, m, tile, lds, row);
+#pragma unroll
+    for (int u = 0; u < kUpCols; ++u) {
+        if (col + u > last) return;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = t * kTile + q * 4 + i;
+                if (r >= n) continue;
+                uint16_t lead, rest;
+                two_terms(swiglu(acc[t][2 * u][i], acc[t][2 * u + 1][i]), lead, rest);
+                uint16_t* o = act + (size_t)member[r] * 2 * d.I + (col + u) * kTile + c;
+                o[0] = lead;
+                o[d.I] = rest;
+            }
+    }
 }
 
-__global__ __launch_bounds__(256) void w4_up_kernel(W4Mat m, W4Ws w, W4Dims d) {
-    if ((int)blockIdx.y >= w.nchunk[0]) return;
-    const Chunk ch = w.chunks[blockIdx.y];
-    const int col = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (col >= d.I / kTile) return;
-    const int rt = (ch.rows + kTile - 1) / kTile;
-    if (rt == 1) up_tiles<1>(m, w, d, ch, col);
-    else if (rt == 2) up_tiles<2>(m, w, d, ch, col);
-    else if (rt == 3) up_tiles<3>(m, w, d, ch, col);
-    else up_tiles<4>(m, w, d, ch, col);
+template <int MAX>
+__global__ __launch_bounds__(256, 2) void w4_up_kernel(const int32_t* __restrict__ topk, const uint16_t* __restrict__ x,
+                                                    W4Mat m, uint16_t* __restrict__ act, W4Dims d) {
+    __shared__ uint4 lds[MAX * 1024];
+    __shared__ int member[MAX * kTile];
+    const int e = blockIdx.y;
+    for (int first = blockIdx.z * MAX * kTile;; first += gridDim.z * MAX * kTile) {
+        const int n = find_members(topk, d.T * d.K, e, first, MAX * kTile, member);
+        if (n == 0) return;
+        if (MAX >= 4 && n > 48) up_tiles<MAX >= 4 ? 4 : 1>(x, m, act, d, e, member, n, lds);
+        else if (MAX >= 4 && n > 32) up_tiles<MAX >= 4 ? 3 : 1>(x, m, act, d, e, member, n, lds);
+        else if (MAX >= 2 && n > 16) up_tiles<MAX >= 2 ? 2 : 1>(x, m, act, d, e, member, n, lds);
+        else up_tiles<1>(x, m, act, d, e, member, n, lds);
+        __syncthreads();
+    }
 }
 
-// y for one chunk; a wave takes 32 columns.
+// y for one expert; a wave takes kDownCols column tiles.  The rows are the two terms of 8 pairs a row tile.
 template <int RT>
-__device__ __forceinline__ void down_tiles(const W4Mat& m, const W4Ws& w, const W4Dims& d, const Chunk& ch, int col) {
-    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-    const size_t g = (size_t)ch.expert * m.nb + col, tile[2] = {g, g + 1};
-    f32x4_t acc[RT][2];
-    multiply_rows<RT, 2>(acc, m, tile, reinterpret_cast<const uint4*>(w.act) + (size_t)ch.tile * 2 * m.kb * 256);
+__device__ __forceinline__ void down_tiles(const uint16_t* act, const W4Mat& m, float* y, const W4Dims& d, int e,
+                                           const int* member, int n, uint4* lds) {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, last = d.H / kTile - 1;
+    const int col = (blockIdx.x * 4 + wave_of()) * kDownCols;
+    const uint16_t* row[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int t = 0; t < RT; ++t) {
+        const int term = t * kTile + (threadIdx.x >> 4);
+        row[t] = act + ((size_t)member[min(term / 2, n - 1)] * 2 + term % 2) * d.I + (threadIdx.x & 15) * 8;
+    }
+    size_t tile[kDownCols];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = r * 8 + q * 2 + i;
-            if (row >= ch.rows) continue;
-            float* o = w.y + (size_t)w.pair[ch.tile * kTile + row] * d.H + col * kTile + c;
-            o[0] = acc[r][0][2 * i] + acc[r][0][2 * i + 1];
-            o[kTile] = acc[r][1][2 * i] + acc[r][1][2 * i + 1];
-        }
+    for (int u = 0; u < kDownCols; ++u) tile[u] = (size_t)e * m.nb + min(col + u, last);
+    f32x4_t acc[RT][kDownCols];
+    multiply_many(acc, m, tile, lds, row);
+#pragma unroll
+    for (int u = 0; u < kDownCols; ++u) {
+        if (col + u > last) return;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = t * 8 + q * 2 + i;
+                if (r < n) y[(size_t)member[r] * d.H + (col + u) * kTile + c] = acc[t][u][2 * i] + acc[t][u][2 * i + 1];
+            }
+    }
 }
 
-__global__ __launch_bounds__(256) void w4_down_kernel(W4Mat m, W4Ws w, W4Dims d) {
-    if ((int)blockIdx.y >= w.nchunk[0]) return;
-    const Chunk ch = w.chunks[blockIdx.y];
-    const int col = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 2;
-    if (col >= d.H / kTile) return;
-    const int rt = (ch.rows + kTile / 2 - 1) / (kTile / 2);
-    if (rt == 1) down_tiles<1>(m, w, d, ch, col);
-    else if (rt == 2) down_tiles<2>(m, w, d, ch, col);
-    else if (rt <= 4) down_tiles<4>(m, w, d, ch, col);
-    else down_tiles<8>(m, w, d, ch, col);
+template <int MAX>
+__global__ __launch_bounds__(256, 2) void w4_down_kernel(const int32_t* __restrict__ topk,
+                                                      const uint16_t* __restrict__ act, W4Mat m,
+                                                      float* __restrict__ y, W4Dims d) {
+    __shared__ uint4 lds[MAX * 1024];
+    __shared__ int member[MAX * 8];
+    const int e = blockIdx.y;
+    for (int first = blockIdx.z * MAX * 8;; first += gridDim.z * MAX * 8) {
+        const int n = find_members(topk, d.T * d.K, e, first, MAX * 8, member);
+        if (n == 0) return;
+        if (MAX >= 4 && n > 24) down_tiles<MAX >= 4 ? 4 : 1>(act, m, y, d, e, member, n, lds);
+        else if (MAX >= 4 && n > 16) down_tiles<MAX >= 4 ? 3 : 1>(act, m, y, d, e, member, n, lds);
+        else if (MAX >= 2 && n > 8) down_tiles<MAX >= 2 ? 2 : 1>(act, m, y, d, e, member, n, lds);
+        else down_tiles<1>(act, m, y, d, e, member, n, lds);
+        __syncthreads();
+    }
 }
 
 // out = sum over k of gate * y, in k order, skipping ids that name no expert.
@@ -601,11 +698,13 @@ extern "C" int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, con
         MOONEP_LAUNCH_CHECK();
         return MOONEP_OK;
     }
-    hipLaunchKernelGGL(w4_gather_kernel, dim3(fours_of(d.H), d.E), dim3(256), 0, s, topk, xr, w, d);
+    constexpr int kUpMax = 4, kDownMax = 4;
+    const int ucols = 4 * kUpCols * kTile, dcols = 4 * kDownCols * kTile;
+    const dim3 ugrid((d.I + ucols - 1) / ucols, d.E, std::min(4, (d.T + kUpMax * 16 - 1) / (kUpMax * 16)));
+    const dim3 dgrid((d.H + dcols - 1) / dcols, d.E, std::min(4, (d.T + kDownMax * 8 - 1) / (kDownMax * 8)));
+    hipLaunchKernelGGL(w4_up_kernel<kUpMax>, ugrid, dim3(256), 0, s, topk, xr, up, w.act, d);
     MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(w4_up_kernel, dim3((d.I / kTile + 3) / 4, w.max_chunks), dim3(256), 0, s, up, w, d);
-    MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(w4_down_kernel, dim3((d.H / kTile + 7) / 8, w.max_chunks), dim3(256), 0, s, down, w, d);
+    hipLaunchKernelGGL(w4_down_kernel<kDownMax>, dgrid, dim3(256), 0, s, topk, w.act, down, w.y, d);
     MOONEP_LAUNCH_CHECK();
     hipLaunchKernelGGL(w4_join_kernel, dim3((d.H / 4 + 255) / 256, d.T), dim3(256), 0, s, topk, gates,
                        reinterpret_cast<const float4*>(w.y), static_cast<uint2*>(out), d);
