@@ -7,7 +7,7 @@
 // bf16 values, exactly, in one instruction; matrix instructions multiply them by the tokens' rows.
 //
 // Pairs (token, k) are grouped by expert, so that an expert's weights are read once for all its
-// tokens; each workgroup finds its expert's pairs among the ids itself.  A lane (column c = lane % 16,
+// tokens; up to kFewPairs pairs, each workgroup finds its group among the ids itself.  A lane (column c = lane % 16,
 // group q = lane / 16) of a wave loads 16 bytes: the 32 codes of group q of column c in a block of
 // 128 input values.  The matrix instruction of step i multiplies values q * 32 + i * 8 .. + 8 of each
 // group, which is an order of the input direction that both operands share.
@@ -40,23 +40,49 @@ struct W4Mat {
     int kin, kb, sb, nb;
 };
 
-// Scratch.
+// A run of an expert's pairs.
+struct Chunk {
+    int32_t expert, first, n;        // its pairs are pair[first] .. pair[first + n)
+};
+
+constexpr int kUpRows = 64;          // pairs a chunk of the first product
+constexpr int kDownPairs = 32;       // and of the second, whose rows are two a pair
+
+// Scratch; few pairs need only act.
 struct W4Ws {
     uint16_t* act;                   // [T*K][2][I] bf16: leading and trailing term
-    float* y;                        // [T*K][H]; none for few pairs
+    float* y;                        // [T*K][H]
+    int32_t* pair;                   // [T*K] by expert
+    int32_t* chunks;                 // how many of each
+    Chunk *up, *down;
+    int max_up, max_down;
 };
 
 static int blocks_of(int kin) { return (kin + kBlock - 1) / kBlock; }
 static int fours_of(int kin) { return (blocks_of(kin) + 3) / 4; }
 
 static size_t w4_ws_layout(const W4Dims& d, void* base, W4Ws* ws) {
-    const size_t pairs = (size_t)d.T * d.K;
-    const size_t act = align_up(pairs * 2 * d.I * 2, 256);
-    if (ws) {
-        ws->act = static_cast<uint16_t*>(base);
-        ws->y = reinterpret_cast<float*>(static_cast<char*>(base) + act);
+    const size_t pairs = (size_t)d.T * d.K, experts = std::min<size_t>(pairs, d.E);
+    W4Ws w{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) -> void* {
+        void* p = base ? static_cast<char*>(base) + off : nullptr;
+        off = align_up(off + bytes, 256);
+        return p;
+    };
+    w.act = (uint16_t*)take(pairs * 2 * d.I * 2);
+    if (pairs > kFewPairs) {
+        // an expert leaves less than one chunk partly empty
+        w.max_up = (int)(experts + pairs / kUpRows);
+        w.max_down = (int)(experts + pairs / kDownPairs);
+        w.y = (float*)take(pairs * d.H * 4);
+        w.pair = (int32_t*)take(pairs * 4);
+        w.chunks = (int32_t*)take(2 * 4);
+        w.up = (Chunk*)take(w.max_up * sizeof(Chunk));
+        w.down = (Chunk*)take(w.max_down * sizeof(Chunk));
     }
-    return act + (pairs <= kFewPairs ? 0 : pairs * d.H * 4);
+    if (ws) *ws = w;
+    return off;
 }
 
 // The wave's number, known to be the same for all its lanes: what follows from it stays in scalar registers.
@@ -87,119 +113,72 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t codes, float scale) {
 
 __device__ __forceinline__ uint32_t dword(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// A lane's codes and scales of four blocks of NT column tiles.
-template <int NT>
-struct Four {
-    uint4 codes[NT][4];
-    uint32_t scales[NT];
-};
+// The order of a product over fours first, first + step, ...  Rows come in PARTS parts of a four:
+// fetch(four, part, whole) asks for one, place() puts it into LDS.  load(four, blocks) asks for the
+// weights, and scales(then) for the next's scales, having kept the present ones.  blocks<THEN, J0,
+// J1>(n, then) multiplies blocks J0 .. J1 of four, of which n exist, and with THEN lets each block's
+// codes make room for the same block's of four `then`.  So rows, then weights, of the next are on
+// their way while one is multiplied.  The loop has no branches: a load whose register meets another
+// value at a join of two paths would be waited for there.
+template <bool V>
+using Flag = std::integral_constant<bool, V>;
+template <int V>
+using Int = std::integral_constant<int, V>;
 
-// Where a lane's codes and scales of a column tile lie.
-template <int NT>
-struct Weights {
-    const uint4* codes[NT];          // of the tile; the lane is added at each load, to keep these scalar
-    const uint32_t* scales[NT];
-    int kb, sb;
-
-    __device__ __forceinline__ Weights(const W4Mat& m, const size_t* tile) : kb(m.kb), sb(m.sb) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            codes[t] = m.codes + tile[t] * m.kb * 64;
-            scales[t] = m.scales + tile[t] * m.sb * 64;
-        }
-    }
-
-    __device__ __forceinline__ void load_scales(Four<NT>& f, int four) const {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) f.scales[t] = (scales[t] + four * 64)[threadIdx.x & 63];
-    }
-
-    __device__ __forceinline__ void load_codes(Four<NT>& f, int four, int j) const {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) f.codes[t][j] = ld_nt(codes[t] + (four * 4 + j) * 64 + (threadIdx.x & 63));
-    }
-
-    __device__ __forceinline__ void load(Four<NT>& f, int four, int blocks) const {
-        load_scales(f, four);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < blocks) load_codes(f, four, j);
-    }
-};
-
-// acc[r][t] += rows * weights of four blocks, or of the first `blocks` of them (a constant 4 but at the
-// end); a(r, j, i) is the operand of row tile r, block j and step i.  With THEN, each block's codes make
-// room for the same block's of four `then`.
-template <bool THEN, int RT, int NT, class A>
-__device__ __forceinline__ void multiply_four(f32x4_t (&acc)[RT][NT], Four<NT>& f, const Weights<NT>& w, int blocks,
-                                              int then, A a) {
-    uint32_t scales[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) scales[t] = f.scales[t];
-    if constexpr (THEN) w.load_scales(f, then);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j >= blocks) break;
-        float s[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = scale_of(scales[t], j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bf16x8_t b[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) b[t] = widen(dword(f.codes[t][j], i), s[t]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const bf16x8_t v = __builtin_bit_cast(bf16x8_t, a(r, j, i));
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[t], acc[r][t], 0, 0, 0);
-            }
-        }
-        if constexpr (THEN) w.load_codes(f, then, j);
-        // without it all blocks' operands are read ahead, into registers that spill
-        __builtin_amdgcn_sched_barrier(0);
-    }
-}
-
-// The order of a product over fours first, first + step, ...: fetch(four, whole) asks for the rows of
-// four blocks, place() puts them into LDS.  Rows, then weights, of the next four are on their way while
-// one is multiplied.  The loop has no branches: a load whose register meets another value at a join of
-// two paths would be waited for there.
-template <int RT, int NT, class Fetch, class Place, class A>
-__device__ __forceinline__ void multiply(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, int first,
-                                         int step, Fetch fetch, Place place, A a) {
-    const Weights<NT> w(m, tile);
+template <int PARTS, class Fetch, class Place, class Load, class Scales, class Blocks>
+__device__ __forceinline__ void over_fours(const W4Mat& m, int first, int step, Fetch fetch, Place place, Load load,
+                                           Scales scales, Blocks blocks) {
+    static_assert(PARTS == 1 || PARTS == 2, "");
     const int whole = m.kin / kFour;
-    Four<NT> f;
     int four = first;
     if (four < whole) {
-        fetch(four, true);
-        w.load(f, four, 4);
+        fetch(four, 0, true);
+        load(four, 4);
         for (; four + step < whole; four += step) {
+            const int then = four + step;
             place();
-            fetch(four + step, true);
-            multiply_four<true>(acc, f, w, 4, four + step, a);
+            if constexpr (PARTS == 2) {
+                fetch(four, 1, true);
+                scales(then, Flag<true>{});
+                blocks(Flag<true>{}, Int<0>{}, Int<2>{}, 4, then);
+                place();
+                fetch(then, 0, true);
+                blocks(Flag<true>{}, Int<2>{}, Int<4>{}, 4, then);
+            } else {
+                fetch(then, 0, true);
+                scales(then, Flag<true>{});
+                blocks(Flag<true>{}, Int<0>{}, Int<4>{}, 4, then);
+            }
         }
         place();
-        multiply_four<false>(acc, f, w, 4, 0, a);
+        scales(0, Flag<false>{});
+        if constexpr (PARTS == 2) {
+            fetch(four, 1, true);
+            blocks(Flag<false>{}, Int<0>{}, Int<2>{}, 4, 0);
+            place();
+            blocks(Flag<false>{}, Int<2>{}, Int<4>{}, 4, 0);
+        } else {
+            blocks(Flag<false>{}, Int<0>{}, Int<4>{}, 4, 0);
+        }
         four += step;
     }
     if (four < m.sb) {               // the end of the input direction, in part
-        const int blocks = m.kb - four * 4;
-        fetch(four, false);
-        w.load(f, four, blocks);
+        const int n = m.kb - four * 4;
+        fetch(four, 0, false);
+        load(four, n);
         place();
-        multiply_four<false>(acc, f, w, blocks, 0, a);
+        scales(0, Flag<false>{});
+        if constexpr (PARTS == 2) {
+            blocks(Flag<false>{}, Int<0>{}, Int<2>{}, n, 0);
+            if (n > 2) {
+                fetch(four, 1, false);
+                place();
+                blocks(Flag<false>{}, Int<2>{}, Int<4>{}, n, 0);
+            }
+        } else {
+            blocks(Flag<false>{}, Int<0>{}, Int<4>{}, n, 0);
+        }
     }
-}
-
-template <int RT, int NT>
-__device__ __forceinline__ void clear(f32x4_t (&acc)[RT][NT]) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
@@ -237,14 +216,30 @@ __device__ __forceinline__ int member_pair(unsigned long long members) {
 // RN rows of four blocks in `lds` (RN KiB of its own), 16-byte pieces swapped by row so that equal
 // pieces of different rows lie in different banks.  Rows past RN repeat the last.
 template <int RN, int NT, class Row>
-__device__ __forceinline__ void multiply_few(f32x4_t (&acc)[1][NT], const W4Mat& m, const size_t* tile, int first,
+__device__ __forceinline__ void multiply_few(f32x4_t (&acc)[NT], const W4Mat& m, const size_t* tile, int first,
                                              int step, uint4* lds, Row row) {
     const int lane = threadIdx.x & 63, q = lane >> 4, mine = min(lane & 15, RN - 1);
-    uint4 a[RN];
-    clear(acc);
-    multiply<1, NT>(
-        acc, m, tile, first, step,
-        [&](int four, bool whole) {
+    const uint4* base[NT];           // of the tiles, the lane is added at each load: these stay scalar
+    const uint32_t* sbase[NT];
+    uint4 a[RN], codes[NT][4];
+    uint32_t next[NT], now[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        base[t] = m.codes + tile[t] * m.kb * 64;
+        sbase[t] = m.scales + tile[t] * m.sb * 64;
+        acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    auto load_codes = [&](int four, int j) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) codes[t][j] = ld_nt(base[t] + (four * 4 + j) * 64 + lane);
+    };
+    auto load_scales = [&](int four) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) next[t] = (sbase[t] + four * 64)[lane];
+    };
+    over_fours<1>(
+        m, first, step,
+        [&](int four, int, bool whole) {
             const int k = four * kFour + lane * 8;
 #pragma unroll
             for (int r = 0; r < RN; ++r)
@@ -257,7 +252,42 @@ __device__ __forceinline__ void multiply_few(f32x4_t (&acc)[1][NT], const W4Mat&
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         },
-        [&](int, int j, int i) { return lds[mine * 64 + ((j * 16 + q * 4 + i) ^ mine)]; });
+        [&](int four, int n) {
+            load_scales(four);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) load_codes(four, j);
+        },
+        [&](int then, auto more) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) now[t] = next[t];
+            if constexpr (more.value) load_scales(then);
+        },
+        [&](auto more, auto, auto, int n, int then) {
+            auto read = [&](int step) {
+                return __builtin_bit_cast(bf16x8_t, lds[mine * 64 + ((step / 4 * 16 + q * 4 + step % 4) ^ mine)]);
+            };
+            bf16x8_t rows[2];        // of this step and the next
+            rows[0] = read(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= n) break;
+                float s[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[t] = scale_of(now[t], j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (j * 4 + i < 15) rows[(i + 1) & 1] = read(j * 4 + i + 1);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows[i & 1], widen(dword(codes[t][j], i), s[t]),
+                                                                         acc[t], 0, 0, 0);
+                    // without it more steps' operands are read ahead, into registers that spill
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if constexpr (more.value) load_codes(then, j);
+            }
+        });
 }
 
 // Calls f with the number of rows, 1, 2, 4 or 8, that n rows at most eight are computed as.
@@ -288,7 +318,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32
     const size_t g = (size_t)e * m.nb + blockIdx.x, tile[2] = {g, g + m.nb / 2};
     for (int r0 = 0; r0 < n; r0 += 8) {
         const int rows = min(8, n - r0);
-        f32x4_t acc[1][2];
+        f32x4_t acc[2];
         __syncthreads();
         with_rows(rows, [&](auto rn) {
             multiply_few<rn.value, 2>(acc, m, tile, wave, kUpWaves, lds[wave], [&](int r) {
@@ -299,7 +329,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32
         float4* part = reinterpret_cast<float4*>(lds[wave]);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            part[t * 64 + lane] = make_float4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]);
+            part[t * 64 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
         __syncthreads();
         const int r = threadIdx.x >> 4, to = __shfl(pair, min(r0 + r, n - 1), 64);
         if (r < rows) {
@@ -340,7 +370,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 3) void w4_few_down_kernel(const i
         const int n = __popcll(members), pair = member_pair(members);
         const size_t tile[1] = {(size_t)e * m.nb + blockIdx.x};
         for (int r0 = 0; r0 < n; r0 += 4) {
-            f32x4_t acc[1][1];
+            f32x4_t acc[1];
             with_rows(min(8, (n - r0) * 2), [&](auto rn) {
                 multiply_few<rn.value, 1>(acc, m, tile, 0, 1, lds[wave], [&](int r) {
                     const int p = __builtin_amdgcn_readlane(pair, min(r0 + r / 2, n - 1));
@@ -350,7 +380,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 3) void w4_few_down_kernel(const i
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = r0 + q * 2 + i, p = __shfl(pair, min(r, n - 1), 64);
-                if (q < 2 && r < n) y[p][c] = acc[0][0][2 * i] + acc[0][0][2 * i + 1];
+                if (q < 2 && r < n) y[p][c] = acc[0][2 * i] + acc[0][2 * i + 1];
             }
         }
     }
@@ -368,182 +398,218 @@ __global__ __launch_bounds__(64 * kDownWaves, 3) void w4_few_down_kernel(const i
 // many pairs
 // ---------------------------------------------------------------------------
 
-// Pairs first .. first + most of expert e, in order, into member[]; returns how many.  Workgroup of 256.
-__device__ __forceinline__ int find_members(const int32_t* __restrict__ topk, int pairs, int e, int first, int most,
-                                            int* member) {
-    __shared__ int before[MOONEP_W4_MAX_PAIRS / 64 + 1];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int waves = (pairs + 63) / 64;
-    for (int i = tid >> 6; i < waves; i += 4) {
-        const int p = i * 64 + lane;
-        const unsigned long long hits = __ballot(p < pairs && topk[p] == e);
-        if (lane == 0) before[i + 1] = __popcll(hits);
+__device__ __forceinline__ int wave_scan(int v) {    // inclusive prefix sum over the wave
+    const int lane = threadIdx.x & 63;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(v, o, 64);
+        if (lane >= o) v += u;
     }
-    __syncthreads();
-    if (tid < 64) {                  // prefix sums, 64 counts at a time
-        int sum = 0;
-        for (int i0 = 0; i0 < waves; i0 += 64) {
-            int v = i0 + lane < waves ? before[i0 + lane + 1] : 0;
-            for (int o = 1; o < 64; o <<= 1) {
-                const int u = __shfl_up(v, o, 64);
-                if (lane >= o) v += u;
-            }
-            if (i0 + lane < waves) before[i0 + lane + 1] = sum + v;
-            sum += __shfl(v, 63, 64);
-        }
-        if (lane == 0) before[0] = 0;
-    }
-    __syncthreads();
-    const int n = min(most, before[waves] - first);
-    if (n <= 0) return 0;
-    for (int i = tid >> 6; i < waves; i += 4) {
-        if (before[i + 1] <= first || before[i] >= first + n) continue;
-        const int p = i * 64 + lane;
-        const bool hit = p < pairs && topk[p] == e;
-        const unsigned long long hits = __ballot(hit);
-        const int at = before[i] + __popcll(hits & ((1ull << lane) - 1)) - first;
-        if (hit && at >= 0 && at < n) member[at] = p;
-    }
-    __syncthreads();
-    return n;
+    return v;
 }
 
-// acc = RT row tiles times two column tiles, a wave's own; the workgroup's 256 threads bring the rows
-// of four blocks to LDS, each 16 bytes of a row at a time: row[t] is the thread's row of tile t at its
+// Sorts the pairs by expert and cuts them into chunks for the two products: one workgroup, a thread an
+// expert.  The order of an expert's pairs depends on which thread's atomic comes first; a row's result
+// does not depend on its place.
+__global__ __launch_bounds__(1024) void w4_group_kernel(const int32_t* __restrict__ topk, W4Ws w, int pairs, int E) {
+    __shared__ int count[kMaxE], place[kMaxE];
+    __shared__ int sums[3][16];
+    const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
+    count[e] = 0;
+    __syncthreads();
+    for (int p = e; p < pairs; p += 1024) {
+        const int id = topk[p];
+        if ((unsigned)id < (unsigned)E) atomicAdd(&count[id], 1);
+    }
+    __syncthreads();
+    const int n = count[e], up = (n + kUpRows - 1) / kUpRows, down = (n + kDownPairs - 1) / kDownPairs;
+    const int s0 = wave_scan(n), s1 = wave_scan(up), s2 = wave_scan(down);
+    if (lane == 63) {
+        sums[0][wave] = s0;
+        sums[1][wave] = s1;
+        sums[2][wave] = s2;
+    }
+    __syncthreads();
+    int first = s0 - n, u0 = s1 - up, d0 = s2 - down;
+    for (int i = 0; i < wave; ++i) {
+        first += sums[0][i];
+        u0 += sums[1][i];
+        d0 += sums[2][i];
+    }
+    place[e] = first;
+    for (int i = 0; i < up; ++i) w.up[u0 + i] = Chunk{e, first + i * kUpRows, min(kUpRows, n - i * kUpRows)};
+    for (int i = 0; i < down; ++i) w.down[d0 + i] = Chunk{e, first + i * kDownPairs, min(kDownPairs, n - i * kDownPairs)};
+    if (e == 1023) {
+        w.chunks[0] = u0 + up;
+        w.chunks[1] = d0 + down;
+    }
+    __syncthreads();
+    for (int p = e; p < pairs; p += 1024) {
+        const int id = topk[p];
+        if ((unsigned)id < (unsigned)E) w.pair[atomicAdd(&place[id], 1)] = p;
+    }
+}
+
+// acc = RT row tiles times NT column tiles, a wave's own.  The workgroup's 256 threads bring the rows
+// of four blocks to LDS, 16 bytes of a row each at a time: rows(t) is the thread's row of tile t at its
 // piece.  Where a piece lies in LDS is swapped by row, so that neither side meets a bank twice.
-template <int RT, int NT>
+template <int RT, int NT, class Rows>
 __device__ __forceinline__ void multiply_many(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, uint4* lds,
-                                              const uint16_t* const* row) {
+                                              Rows rows) {
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
     const int piece = tid & 15, swapped = piece % 4 * 64 + piece / 4 * 16 + ((tid >> 4) ^ (piece % 4 * 4 + piece / 4));
-    uint4 a[RT][4];
-    clear(acc);
-    multiply<RT, NT>(
-        acc, m, tile, 0, 1,
-        [&](int four, bool whole) {
+    const uint4* base[NT];           // of the tiles, the lane is added at each load: these stay scalar
+    const uint32_t* sbase[NT];
+    const uint16_t* row[RT];
+    uint4 a[RT][4], codes[NT][4];
+    uint32_t next[NT], now[NT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < NT; ++t) {
+        base[t] = m.codes + tile[t] * m.kb * 64;
+        sbase[t] = m.scales + tile[t] * m.sb * 64;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) row[r] = rows(r);
+    auto load_codes = [&](int four, int j) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) codes[t][j] = ld_nt(base[t] + (four * 4 + j) * 64 + lane);
+    };
+    auto load_scales = [&](int four) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) next[t] = (sbase[t] + four * 64)[lane];
+    };
+    over_fours<1>(
+        m, 0, 1,
+        [&](int four, int, bool whole) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int k = four * kFour + j * kBlock;
-                    a[t][j] = whole || k + piece * 8 < m.kin ? *reinterpret_cast<const uint4*>(row[t] + k)
+                    a[r][j] = whole || k + piece * 8 < m.kin ? *reinterpret_cast<const uint4*>(row[r] + k)
                                                              : make_uint4(0, 0, 0, 0);
                 }
         },
         [&] {
             __syncthreads();
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) lds[(t * 4 + j) * 256 + swapped] = a[t][j];
+                for (int j = 0; j < 4; ++j) lds[(r * 4 + j) * 256 + swapped] = a[r][j];
             __syncthreads();
         },
-        [&](int t, int j, int i) { return lds[(t * 4 + j) * 256 + i * 64 + q * 16 + (c ^ (i * 4 + q))]; });
+        [&](int four, int n) {
+            load_scales(four);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) load_codes(four, j);
+        },
+        [&](int then, auto more) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) now[t] = next[t];
+            if constexpr (more.value) load_scales(then);
+        },
+        [&](auto more, auto, auto, int n, int then) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= n) break;
+                float s[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[t] = scale_of(now[t], j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    bf16x8_t b[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) b[t] = widen(dword(codes[t][j], i), s[t]);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const bf16x8_t v = __builtin_bit_cast(
+                            bf16x8_t, lds[(r * 4 + j) * 256 + i * 64 + q * 16 + (c ^ (i * 4 + q))]);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, b[t], acc[r][t], 0, 0, 0);
+                    }
+                }
+                if constexpr (more.value) load_codes(then, j);
+                // without it all blocks' operands are read ahead, into registers that spill
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        });
 }
 
-// act for one expert; a wave takes kUpCols column tiles of 16.
-constexpr int kUpCols = 1, kDownCols = 2;
-
+// act for one chunk; a wave takes 16 columns.
 template <int RT>
-__device__ __forceinline__ void up_tiles(const uint16_t* x, const W4Mat& m, uint16_t* act, const W4Dims& d, int e,
-                                         const int* member, int n, uint4* lds) {
+__device__ __forceinline__ void up_tiles(const uint16_t* x, const W4Mat& m, const W4Ws& w, const W4Dims& d,
+                                         const Chunk& ch, uint4* lds) {
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, last = d.I / kTile - 1;
-    const int col = (blockIdx.x * 4 + wave_of()) * kUpCols;
-    const uint16_t* row[RT];
+    const int col = blockIdx.x * 4 + wave_of();
+    const int* member = w.pair + ch.first;
+    const size_t g = (size_t)ch.expert * m.nb + min(col, last), tile[2] = {g, g + m.nb / 2};
+    f32x4_t acc[RT][2];
+    multiply_many<RT, 2>(acc, m, tile, lds, [&](int t) {
+        // rows past the chunk's compute with its last one; nothing of them is stored
+        const int r = min(t * kTile + (int)(threadIdx.x >> 4), ch.n - 1);
+        return x + (size_t)(member[r] / d.K) * d.H + (threadIdx.x & 15) * 8;
+    });
+    if (col > last) return;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = min(t * kTile + (int)(threadIdx.x >> 4), n - 1);
-        row[t] = x + (size_t)(member[r] / d.K) * d.H + (threadIdx.x & 15) * 8;
-    }
-    size_t tile[2 * kUpCols];
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-    for (int u = 0; u < kUpCols; ++u) {
-        tile[2 * u] = (size_t)e * m.nb + min(col + u, last);
-        tile[2 * u + 1] = tile[2 * u] + m.nb / 2;
-    }
-    f32x4_t acc[RT][2 * kUpCols];
-    multiply_many(acc, m, tile, lds, row);
-#pragma unroll
-    for (int u = 0; u < kUpCols; ++u) {
-        if (col + u > last) return;
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = t * kTile + q * 4 + i;
-                if (r >= n) continue;
-                uint16_t lead, rest;
-                two_terms(swiglu(acc[t][2 * u][i], acc[t][2 * u + 1][i]), lead, rest);
-                uint16_t* o = act + (size_t)member[r] * 2 * d.I + (col + u) * kTile + c;
-                o[0] = lead;
-                o[d.I] = rest;
-            }
-    }
+        for (int i = 0; i < 4; ++i) {
+            const int r = t * kTile + q * 4 + i;
+            if (r >= ch.n) continue;
+            uint16_t lead, rest;
+            two_terms(swiglu(acc[t][0][i], acc[t][1][i]), lead, rest);
+            uint16_t* o = w.act + (size_t)member[r] * 2 * d.I + col * kTile + c;
+            o[0] = lead;
+            o[d.I] = rest;
+        }
 }
 
-template <int MAX>
-__global__ __launch_bounds__(256, 2) void w4_up_kernel(const int32_t* __restrict__ topk, const uint16_t* __restrict__ x,
-                                                    W4Mat m, uint16_t* __restrict__ act, W4Dims d) {
-    __shared__ uint4 lds[MAX * 1024];
-    __shared__ int member[MAX * kTile];
-    const int e = blockIdx.y;
-    for (int first = blockIdx.z * MAX * kTile;; first += gridDim.z * MAX * kTile) {
-        const int n = find_members(topk, d.T * d.K, e, first, MAX * kTile, member);
-        if (n == 0) return;
-        if (MAX >= 4 && n > 48) up_tiles<MAX >= 4 ? 4 : 1>(x, m, act, d, e, member, n, lds);
-        else if (MAX >= 4 && n > 32) up_tiles<MAX >= 4 ? 3 : 1>(x, m, act, d, e, member, n, lds);
-        else if (MAX >= 2 && n > 16) up_tiles<MAX >= 2 ? 2 : 1>(x, m, act, d, e, member, n, lds);
-        else up_tiles<1>(x, m, act, d, e, member, n, lds);
-        __syncthreads();
-    }
+__global__ __launch_bounds__(256, 2) void w4_up_kernel(const uint16_t* __restrict__ x, W4Mat m, W4Ws w, W4Dims d) {
+    __shared__ uint4 lds[kUpRows / kTile * 1024];
+    if ((int)blockIdx.y >= w.chunks[0]) return;
+    const Chunk ch = w.up[blockIdx.y];
+    if (ch.n > 48) up_tiles<4>(x, m, w, d, ch, lds);
+    else if (ch.n > 32) up_tiles<3>(x, m, w, d, ch, lds);
+    else if (ch.n > 16) up_tiles<2>(x, m, w, d, ch, lds);
+    else up_tiles<1>(x, m, w, d, ch, lds);
 }
 
-// y for one expert; a wave takes kDownCols column tiles.  The rows are the two terms of 8 pairs a row tile.
+// y for one chunk; a wave takes 32 columns.  The rows are the two terms of 8 pairs a row tile.
 template <int RT>
-__device__ __forceinline__ void down_tiles(const uint16_t* act, const W4Mat& m, float* y, const W4Dims& d, int e,
-                                           const int* member, int n, uint4* lds) {
-    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, last = d.H / kTile - 1;
-    const int col = (blockIdx.x * 4 + wave_of()) * kDownCols;
-    const uint16_t* row[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
+__device__ __forceinline__ void down_tiles(const W4Mat& m, const W4Ws& w, const W4Dims& d, const Chunk& ch, uint4* lds) {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, last = d.H / kTile - 2;
+    const int col = (blockIdx.x * 4 + wave_of()) * 2;
+    const int* member = w.pair + ch.first;
+    const size_t g = (size_t)ch.expert * m.nb + min(col, last), tile[2] = {g, g + 1};
+    f32x4_t acc[RT][2];
+    multiply_many<RT, 2>(acc, m, tile, lds, [&](int t) {
         const int term = t * kTile + (threadIdx.x >> 4);
-        row[t] = act + ((size_t)member[min(term / 2, n - 1)] * 2 + term % 2) * d.I + (threadIdx.x & 15) * 8;
-    }
-    size_t tile[kDownCols];
+        return w.act + ((size_t)member[min(term / 2, ch.n - 1)] * 2 + term % 2) * d.I + (threadIdx.x & 15) * 8;
+    });
+    if (col > last) return;
 #pragma unroll
-    for (int u = 0; u < kDownCols; ++u) tile[u] = (size_t)e * m.nb + min(col + u, last);
-    f32x4_t acc[RT][kDownCols];
-    multiply_many(acc, m, tile, lds, row);
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-    for (int u = 0; u < kDownCols; ++u) {
-        if (col + u > last) return;
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = t * 8 + q * 2 + i;
-                if (r < n) y[(size_t)member[r] * d.H + (col + u) * kTile + c] = acc[t][u][2 * i] + acc[t][u][2 * i + 1];
-            }
-    }
+        for (int i = 0; i < 2; ++i) {
+            const int r = t * 8 + q * 2 + i;
+            if (r >= ch.n) continue;
+            float* o = w.y + (size_t)member[r] * d.H + col * kTile + c;
+            o[0] = acc[t][0][2 * i] + acc[t][0][2 * i + 1];
+            o[kTile] = acc[t][1][2 * i] + acc[t][1][2 * i + 1];
+        }
 }
 
-template <int MAX>
-__global__ __launch_bounds__(256, 2) void w4_down_kernel(const int32_t* __restrict__ topk,
-                                                      const uint16_t* __restrict__ act, W4Mat m,
-                                                      float* __restrict__ y, W4Dims d) {
-    __shared__ uint4 lds[MAX * 1024];
-    __shared__ int member[MAX * 8];
-    const int e = blockIdx.y;
-    for (int first = blockIdx.z * MAX * 8;; first += gridDim.z * MAX * 8) {
-        const int n = find_members(topk, d.T * d.K, e, first, MAX * 8, member);
-        if (n == 0) return;
-        if (MAX >= 4 && n > 24) down_tiles<MAX >= 4 ? 4 : 1>(act, m, y, d, e, member, n, lds);
-        else if (MAX >= 4 && n > 16) down_tiles<MAX >= 4 ? 3 : 1>(act, m, y, d, e, member, n, lds);
-        else if (MAX >= 2 && n > 8) down_tiles<MAX >= 2 ? 2 : 1>(act, m, y, d, e, member, n, lds);
-        else down_tiles<1>(act, m, y, d, e, member, n, lds);
-        __syncthreads();
-    }
+__global__ __launch_bounds__(256, 2) void w4_down_kernel(W4Mat m, W4Ws w, W4Dims d) {
+    __shared__ uint4 lds[kDownPairs / 8 * 1024];
+    if ((int)blockIdx.y >= w.chunks[1]) return;
+    const Chunk ch = w.down[blockIdx.y];
+    if (ch.n > 24) down_tiles<4>(m, w, d, ch, lds);
+    else if (ch.n > 16) down_tiles<3>(m, w, d, ch, lds);
+    else if (ch.n > 8) down_tiles<2>(m, w, d, ch, lds);
+    else down_tiles<1>(m, w, d, ch, lds);
 }
 
 // out = sum over k of gate * y, in k order, skipping ids that name no expert.
@@ -698,13 +764,11 @@ extern "C" int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, con
         MOONEP_LAUNCH_CHECK();
         return MOONEP_OK;
     }
-    constexpr int kUpMax = 4, kDownMax = 4;
-    const int ucols = 4 * kUpCols * kTile, dcols = 4 * kDownCols * kTile;
-    const dim3 ugrid((d.I + ucols - 1) / ucols, d.E, std::min(4, (d.T + kUpMax * 16 - 1) / (kUpMax * 16)));
-    const dim3 dgrid((d.H + dcols - 1) / dcols, d.E, std::min(4, (d.T + kDownMax * 8 - 1) / (kDownMax * 8)));
-    hipLaunchKernelGGL(w4_up_kernel<kUpMax>, ugrid, dim3(256), 0, s, topk, xr, up, w.act, d);
+    hipLaunchKernelGGL(w4_group_kernel, dim3(1), dim3(1024), 0, s, topk, w, d.T * d.K, d.E);
     MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(w4_down_kernel<kDownMax>, dgrid, dim3(256), 0, s, topk, w.act, down, w.y, d);
+    hipLaunchKernelGGL(w4_up_kernel, dim3((d.I + 63) / 64, w.max_up), dim3(256), 0, s, xr, up, w, d);
+    MOONEP_LAUNCH_CHECK();
+    hipLaunchKernelGGL(w4_down_kernel, dim3((d.H + 127) / 128, w.max_down), dim3(256), 0, s, down, w, d);
     MOONEP_LAUNCH_CHECK();
     hipLaunchKernelGGL(w4_join_kernel, dim3((d.H / 4 + 255) / 256, d.T), dim3(256), 0, s, topk, gates,
                        reinterpret_cast<const float4*>(w.y), static_cast<uint2*>(out), d);
