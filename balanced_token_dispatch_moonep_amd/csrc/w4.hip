@@ -7,7 +7,7 @@
 // bf16 values, exactly, in one instruction; matrix instructions multiply them by the tokens' rows.
 //
 // Pairs (token, k) are grouped by expert, so that an expert's weights are read once for all its
-// tokens; up to kFewPairs pairs, each workgroup finds its group among the ids itself.  A lane (column c = lane % 16,
+// tokens.  A lane (column c = lane % 16,
 // group q = lane / 16) of a wave loads 16 bytes: the 32 codes of group q of column c in a block of
 // 128 input values.  The matrix instruction of step i multiplies values q * 32 + i * 8 .. + 8 of each
 // group, which is an order of the input direction that both operands share.
@@ -27,7 +27,7 @@ constexpr int kGroup = 32;           // values a scale
 constexpr int kBlock = 128;          // input values of one wave's load
 constexpr int kFour = 4 * kBlock;    // input values of four blocks, whose scales come in one load
 constexpr int kTile = 16;            // rows a matrix instruction takes, columns of a tile
-constexpr int kFewPairs = 32;
+constexpr int kFewPairs = 64;        // one wave can look at all their ids
 
 struct W4Dims {
     int T, K, E, H, I;
@@ -58,6 +58,15 @@ struct W4Ws {
     int max_up, max_down;
 };
 
+// Whether the kernels for few pairs take a call.  They split an expert's weights finer, but read rows
+// and first terms once more for every 16 columns: 32 pairs over 23 of 32 experts of H 7168, I 2048
+// took 92 us there and 96 with the others, 64 pairs over 28 of them 122 and 114; where the others'
+// workgroups do not fill the chip, 64 pairs over 8 experts of H 1024, I 512 took 12 and 17.
+static bool w4_few(const W4Dims& d) {
+    const int pairs = d.T * d.K;
+    return pairs <= kFewPairs / 2 || (pairs <= kFewPairs && std::min(pairs, d.E) * ((d.I + 63) / 64) < 512);
+}
+
 static int blocks_of(int kin) { return (kin + kBlock - 1) / kBlock; }
 static int fours_of(int kin) { return (blocks_of(kin) + 3) / 4; }
 
@@ -71,7 +80,7 @@ static size_t w4_ws_layout(const W4Dims& d, void* base, W4Ws* ws) {
         return p;
     };
     w.act = (uint16_t*)take(pairs * 2 * d.I * 2);
-    if (pairs > kFewPairs) {
+    if (!w4_few(d)) {
         // an expert leaves less than one chunk partly empty
         w.max_up = (int)(experts + pairs / kUpRows);
         w.max_down = (int)(experts + pairs / kDownPairs);
@@ -755,7 +764,7 @@ extern "C" int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, con
     hipStream_t s = static_cast<hipStream_t>(stream);
     const W4Mat up = w4_mat(w13_codes, w13_scales, d.H, 2 * d.I), down = w4_mat(w2_codes, w2_scales, d.I, d.H);
     const uint16_t* xr = static_cast<const uint16_t*>(x);
-    if (d.T * d.K <= kFewPairs) {
+    if (w4_few(d)) {
         hipLaunchKernelGGL(w4_few_up_kernel, dim3(d.I / kTile, std::min(d.T * d.K, d.E)), dim3(64 * kUpWaves), 0, s,
                            topk, xr, up, w.act, d);
         MOONEP_LAUNCH_CHECK();

@@ -430,7 +430,7 @@ def _check_ffn(T, K, E, H, I, seed=0, R=1, **kw):
     (1, 1, 1, 32, 32), (1, 2, 4, 64, 96), (2, 2, 4, 128, 64), (3, 1, 2, 160, 32), (8, 1, 1, 96, 64),
     (9, 1, 1, 96, 64), (16, 1, 1, 128, 128), (17, 1, 1, 160, 96), (33, 2, 2, 192, 64), (65, 1, 1, 64, 32),
     (130, 2, 3, 96, 96), (5, 2, 16, 320, 192), (24, 4, 8, 288, 224), (7, 8, 8, 544, 160), (40, 3, 5, 640, 32),
-    (1, 8, 32, 1056, 544), (200, 16, 16, 32, 32),
+    (1, 8, 32, 1056, 544), (200, 16, 16, 32, 32), (32, 2, 64, 32, 512), (33, 1, 64, 64, 512), (64, 1, 2, 160, 96),
 ])
 def test_ffn(T, K, E, H, I):
     _check_ffn(T, K, E, H, I, seed=T + H)
@@ -466,10 +466,11 @@ def test_ffn_most_pairs():
         M.moonep_w4_ffn_workspace_bytes(d)
 
 
-def test_ffn_rows_do_not_mix():
-    """A NaN, an infinity or a poisoned weight group reaches its own tokens only, and a token's
-    result does not depend on the batch it is in."""
-    T, K, E, H, I = 21, 2, 5, 160, 96
+@pytest.mark.parametrize("T", [21, 70])
+def test_ffn_rows_do_not_mix(T):
+    """A NaN, an infinity or a poisoned weight group reaches its own tokens only; and a token's result
+    does not depend on the others of its batch (21: few pairs, 70: many)."""
+    K, E, H, I = 2, 5, 160, 96
     topk, gates, x, w13, w2 = _ffn_case(T, K, E, H, I, 6)
     p13, p2 = _packed(w13), _packed(w2)
     clean = _run_ffn(topk, gates, x, p13, p2, E, H, I)
@@ -481,10 +482,9 @@ def test_ffn_rows_do_not_mix():
     for t in range(T):
         if t not in (4, 9):
             assert torch.equal(out[t], clean[t])
-    for t in (0, 7, 20):
-        alone = _run_ffn(topk[t:t + 1], gates[t:t + 1], x[t:t + 1], p13, p2, E, H, I)
-        # the same products in the same order, whichever rows they are next to
-        assert torch.equal(alone[0], clean[t])
+    turn = np.random.default_rng(1).permutation(T)           # other neighbours, the same products in the same order
+    turned = _run_ffn(topk[turn], gates[turn], x[turn], p13, p2, E, H, I)
+    assert torch.equal(turned, clean[torch.from_numpy(turn).to(DEV)])
     w2 = w2.copy()
     w2[2, 40, 7] = 0x7F80
     out = _run_ffn(topk, gates, x, p13, _packed(w2), E, H, I)
