@@ -195,7 +195,7 @@ def _ptr(t, name, dtype=None, shape=None, numel=None, optional=False):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}; the library runs on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():

@@ -7,13 +7,26 @@
 // bf16 values, exactly, in one instruction; matrix instructions multiply them by the tokens' rows.
 //
 // Pairs (token, k) are grouped by expert, so that an expert's weights are read once for all its
-// tokens.  A lane (column c = lane % 16,
-// group q = lane / 16) of a wave loads 16 bytes: the 32 codes of group q of column c in a block of
-// 128 input values.  The matrix instruction of step i multiplies values q * 32 + i * 8 .. + 8 of each
-// group, which is an order of the input direction that both operands share.
+// tokens.  A lane (column c = lane % 16, group q = lane / 16) of a wave loads 16 bytes: the 32 codes
+// of group q of column c in a block of 128 input values.  The matrix instruction of step i multiplies
+// values q * 32 + i * 8 .. + 8 of each group, which is an order of the input direction that both
+// operands share.
+//
+// What bounds it is reading the weights: 0.53 bytes each, against about 6 TB/s.  Measured over 32
+// experts of H 7168, I 2048, 8 a token (one pass among others, weights not in the caches):
+//     tokens   experts read   us     TB/s of weights
+//        1           8        36.5     5.1
+//        8          28       110       5.9
+//       64          32       146       5.1
+//      128          32       212       3.5, 425 TFLOP/s
+// The loads skip the caches' keeping (ld_nt): with plain ones 16 tokens took 141 us instead of 125.
+// From about 16 rows an expert on, matrix instructions (115 us of the 212 without loads and LDS reads)
+// and LDS reads (60 us) add to that; the 32 x 32 x 16 instruction, alone 1.8 times as fast as the 16 x 16
+// x 32 one, gave 224 to 270 us in this loop.
 //
 // Rows go through LDS, and not from global memory to the operand: loads return in order, so a wait
-// for rows would be a wait for the weights that were asked for before them.
+// for rows would be a wait for the weights that were asked for before them.  This and a loop in which
+// no load is waited for early (over_fours) brought one token from 53 us to 38.
 #include "common.h"
 
 #include <type_traits>
@@ -45,8 +58,11 @@ struct Chunk {
     int32_t expert, first, n;        // its pairs are pair[first] .. pair[first + n)
 };
 
-constexpr int kUpRows = 64;          // pairs a chunk of the first product
-constexpr int kDownPairs = 32;       // and of the second, whose rows are two a pair
+// Pairs a chunk of the first product, and of the second, whose rows are two a pair.  Halves of these
+// took 237 us at 128 tokens instead of 208 (weights are read again for each chunk), three quarters 220,
+// twice 205 with registers spilled.
+constexpr int kUpRows = 64;
+constexpr int kDownPairs = 32;
 
 // Scratch; few pairs need only act.
 struct W4Ws {
@@ -122,71 +138,39 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t codes, float scale) {
 
 __device__ __forceinline__ uint32_t dword(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// The order of a product over fours first, first + step, ...  Rows come in PARTS parts of a four:
-// fetch(four, part, whole) asks for one, place() puts it into LDS.  load(four, blocks) asks for the
-// weights, and scales(then) for the next's scales, having kept the present ones.  blocks<THEN, J0,
-// J1>(n, then) multiplies blocks J0 .. J1 of four, of which n exist, and with THEN lets each block's
-// codes make room for the same block's of four `then`.  So rows, then weights, of the next are on
-// their way while one is multiplied.  The loop has no branches: a load whose register meets another
-// value at a join of two paths would be waited for there.
-template <bool V>
-using Flag = std::integral_constant<bool, V>;
-template <int V>
-using Int = std::integral_constant<int, V>;
-
-template <int PARTS, class Fetch, class Place, class Load, class Scales, class Blocks>
+// The order of a product over fours first, first + step, ...  fetch(four, whole) asks for the rows of
+// four blocks, place() puts them into LDS.  load(four, n) asks for the weights of its n blocks,
+// scales(then, more) takes over the present scales and asks for those of four `then`.  blocks(more, n,
+// then) multiplies n blocks and lets each block's codes make room for the same block's of four `then`.
+// So rows, then weights, of the next four are on their way while one is multiplied.  The loop has no
+// branches: a load whose register meets another value at a join of two paths would be waited for there.
+template <class Fetch, class Place, class Load, class Scales, class Blocks>
 __device__ __forceinline__ void over_fours(const W4Mat& m, int first, int step, Fetch fetch, Place place, Load load,
                                            Scales scales, Blocks blocks) {
-    static_assert(PARTS == 1 || PARTS == 2, "");
     const int whole = m.kin / kFour;
     int four = first;
     if (four < whole) {
-        fetch(four, 0, true);
+        fetch(four, true);
         load(four, 4);
         for (; four + step < whole; four += step) {
             const int then = four + step;
             place();
-            if constexpr (PARTS == 2) {
-                fetch(four, 1, true);
-                scales(then, Flag<true>{});
-                blocks(Flag<true>{}, Int<0>{}, Int<2>{}, 4, then);
-                place();
-                fetch(then, 0, true);
-                blocks(Flag<true>{}, Int<2>{}, Int<4>{}, 4, then);
-            } else {
-                fetch(then, 0, true);
-                scales(then, Flag<true>{});
-                blocks(Flag<true>{}, Int<0>{}, Int<4>{}, 4, then);
-            }
+            fetch(then, true);
+            scales(then, std::true_type{});
+            blocks(std::true_type{}, 4, then);
         }
         place();
-        scales(0, Flag<false>{});
-        if constexpr (PARTS == 2) {
-            fetch(four, 1, true);
-            blocks(Flag<false>{}, Int<0>{}, Int<2>{}, 4, 0);
-            place();
-            blocks(Flag<false>{}, Int<2>{}, Int<4>{}, 4, 0);
-        } else {
-            blocks(Flag<false>{}, Int<0>{}, Int<4>{}, 4, 0);
-        }
+        scales(0, std::false_type{});
+        blocks(std::false_type{}, 4, 0);
         four += step;
     }
     if (four < m.sb) {               // the end of the input direction, in part
         const int n = m.kb - four * 4;
-        fetch(four, 0, false);
+        fetch(four, false);
         load(four, n);
         place();
-        scales(0, Flag<false>{});
-        if constexpr (PARTS == 2) {
-            blocks(Flag<false>{}, Int<0>{}, Int<2>{}, n, 0);
-            if (n > 2) {
-                fetch(four, 1, false);
-                place();
-                blocks(Flag<false>{}, Int<2>{}, Int<4>{}, n, 0);
-            }
-        } else {
-            blocks(Flag<false>{}, Int<0>{}, Int<4>{}, n, 0);
-        }
+        scales(0, std::false_type{});
+        blocks(std::false_type{}, n, 0);
     }
 }
 
@@ -246,9 +230,9 @@ __device__ __forceinline__ void multiply_few(f32x4_t (&acc)[NT], const W4Mat& m,
 #pragma unroll
         for (int t = 0; t < NT; ++t) next[t] = (sbase[t] + four * 64)[lane];
     };
-    over_fours<1>(
+    over_fours(
         m, first, step,
-        [&](int four, int, bool whole) {
+        [&](int four, bool whole) {
             const int k = four * kFour + lane * 8;
 #pragma unroll
             for (int r = 0; r < RN; ++r)
@@ -272,7 +256,7 @@ __device__ __forceinline__ void multiply_few(f32x4_t (&acc)[NT], const W4Mat& m,
             for (int t = 0; t < NT; ++t) now[t] = next[t];
             if constexpr (more.value) load_scales(then);
         },
-        [&](auto more, auto, auto, int n, int then) {
+        [&](auto more, int n, int then) {
             auto read = [&](int step) {
                 return __builtin_bit_cast(bf16x8_t, lds[mine * 64 + ((step / 4 * 16 + q * 4 + step % 4) ^ mine)]);
             };
@@ -311,11 +295,13 @@ __device__ __forceinline__ void with_rows(int n, F f) {
 // act = silu(x G) * (x U) for one expert and 16 columns.  The waves deal out the input direction and
 // join their sums in order.  blockIdx.y: a pair, that leads its expert's group if it is the first of
 // it, or an expert where there are fewer experts than pairs.
+// Four waves, three to a SIMD (168 registers): 65 us at 2 tokens; five waves 73; four to a SIMD (128
+// registers, spilled) 97.
 constexpr int kUpWaves = 4;
 
 __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32_t* __restrict__ topk,
-                                                                  const uint16_t* __restrict__ x, W4Mat m,
-                                                                  uint16_t* __restrict__ act, W4Dims d) {
+                                                                     const uint16_t* __restrict__ x, W4Mat m,
+                                                                     uint16_t* __restrict__ act, W4Dims d) {
     __shared__ uint4 lds[kUpWaves][8 * 64];
     const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), c = lane & 15;
     const int id = pair_expert(topk, pairs, d.E);
@@ -360,12 +346,13 @@ __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32
 
 // out for 16 columns and all tokens: the waves take the experts in turn, each group's rows go to LDS,
 // and a token's are joined in k order.  The rows of a matrix instruction are the two terms of 4 pairs.
+// Eight waves: 37 us at one token, six 41.
 constexpr int kDownWaves = 8;
 
 __global__ __launch_bounds__(64 * kDownWaves, 3) void w4_few_down_kernel(const int32_t* __restrict__ topk,
-                                                                      const float* __restrict__ gates,
-                                                                      const uint16_t* __restrict__ act, W4Mat m,
-                                                                      uint16_t* __restrict__ out, W4Dims d) {
+                                                                         const float* __restrict__ gates,
+                                                                         const uint16_t* __restrict__ act, W4Mat m,
+                                                                         uint16_t* __restrict__ out, W4Dims d) {
     __shared__ uint4 lds[kDownWaves][8 * 64];
     __shared__ float y[kFewPairs][kTile];
     const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), c = lane & 15, q = lane >> 4;
@@ -488,9 +475,9 @@ __device__ __forceinline__ void multiply_many(f32x4_t (&acc)[RT][NT], const W4Ma
 #pragma unroll
         for (int t = 0; t < NT; ++t) next[t] = (sbase[t] + four * 64)[lane];
     };
-    over_fours<1>(
+    over_fours(
         m, 0, 1,
-        [&](int four, int, bool whole) {
+        [&](int four, bool whole) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -519,7 +506,7 @@ __device__ __forceinline__ void multiply_many(f32x4_t (&acc)[RT][NT], const W4Ma
             for (int t = 0; t < NT; ++t) now[t] = next[t];
             if constexpr (more.value) load_scales(then);
         },
-        [&](auto more, auto, auto, int n, int then) {
+        [&](auto more, int n, int then) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (j >= n) break;

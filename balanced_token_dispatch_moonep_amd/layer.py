@@ -200,11 +200,15 @@ class MoonEPLayer:
     # -- round the step --------------------------------------------------------
     def grads(self) -> list:
         """The weights' gradients that backward() leaves behind."""
+        if not self.training or self.d.I == 0:
+            raise ValueError("only a training layer with experts has gradients")
         norm = [self.dnorm_weight, self.dnorm_bias] if self.norm_weight is not None else []
         return [g for g in [self.dw13, self.dw2, *norm] if g is not None]
 
     def decoder(self, max_tokens: int) -> "W4Experts":
         """The same norm and experts for decoding, with 4-bit weights made from the present ones."""
+        if self.d.I == 0:
+            raise ValueError("a layer without experts has nothing to decode with")
         return W4Experts(self.w13, self.w2, self.d.K, max_tokens, self.norm_weight, self.norm_bias, self.norm_eps)
 
 
