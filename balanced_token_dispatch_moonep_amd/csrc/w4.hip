@@ -20,9 +20,9 @@
 //       64          32       146       5.1
 //      128          32       212       3.5, 425 TFLOP/s
 // The loads skip the caches' keeping (ld_nt): with plain ones 16 tokens took 141 us instead of 125.
-// From about 16 rows an expert on, matrix instructions (115 us of the 212 without loads and LDS reads)
-// and LDS reads (60 us) add to that; the 32 x 32 x 16 instruction, alone 1.8 times as fast as the 16 x 16
-// x 32 one, gave 224 to 270 us in this loop.
+// From about 16 rows an expert on, LDS reads and matrix instructions add to that (128 tokens: matrix
+// cores busy 30% of the time); the 32 x 32 x 16 instruction in place of the 16 x 16 x 32 one gave 224
+// to 270 us.
 //
 // Rows go through LDS, and not from global memory to the operand: loads return in order, so a wait
 // for rows would be a wait for the weights that were asked for before them.  This and a loop in which
