@@ -15,7 +15,7 @@
 // What bounds it is reading the weights: 0.53 bytes each, against about 6 TB/s.  Measured over 32
 // experts of H 7168, I 2048, 8 a token (one pass among others, weights not in the caches):
 //     tokens   experts read   us     TB/s of weights
-//        1           8        36.5     5.1
+//        1           8        35       5.3
 //        8          28       110       5.9
 //       64          32       146       5.1
 //      128          32       212       3.5, 425 TFLOP/s
@@ -346,10 +346,10 @@ __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32
 
 // out for 16 columns and all tokens: the waves take the experts in turn, each group's rows go to LDS,
 // and a token's are joined in k order.  The rows of a matrix instruction are the two terms of 4 pairs.
-// Eight waves: 37 us at one token, six 41.
-constexpr int kDownWaves = 8;
+// Four waves: 35.6 us at one token, 89 at four; eight 37.5 and 91 (one workgroup a CU), six 41.
+constexpr int kDownWaves = 4;
 
-__global__ __launch_bounds__(64 * kDownWaves, 3) void w4_few_down_kernel(const int32_t* __restrict__ topk,
+__global__ __launch_bounds__(64 * kDownWaves, 2) void w4_few_down_kernel(const int32_t* __restrict__ topk,
                                                                          const float* __restrict__ gates,
                                                                          const uint16_t* __restrict__ act, W4Mat m,
                                                                          uint16_t* __restrict__ out, W4Dims d) {
