@@ -465,7 +465,7 @@ class GradList:
         self.n = n
         self.device = self.tensors[0].device if n else None
         self._numel = [t.numel() for t in self.tensors]
-        self._at = self._c_at = None
+        self._at = (None, None)      # addresses of the last call, and the same for C
         self._c_numel = (ctypes.c_int64 * n)(*self._numel)
         self._c_dtype = (ctypes.c_int32 * n)(*(types[t.dtype] for t in self.tensors))
 
@@ -477,9 +477,11 @@ class GradList:
         if [t.numel() if t.is_contiguous() else -1 for t in self.tensors] != self._numel:
             raise ValueError("a gradient changed its size or layout since the list was made")
         at = [t.data_ptr() for t in self.tensors]
-        if at != self._at:
-            self._at, self._c_at = at, (ctypes.c_void_p * self.n)(*at)
-        return self.n, self._c_at, self._c_numel, self._c_dtype
+        known, c_at = self._at
+        if at != known:
+            c_at = (ctypes.c_void_p * self.n)(*at)
+            self._at = (at, c_at)
+        return self.n, c_at, self._c_numel, self._c_dtype
 
 
 def moonep_grad_norm_workspace_bytes(grads: GradList) -> int:

@@ -8,7 +8,6 @@
 #include "common.h"
 
 #include <cmath>
-#include <new>
 #include <vector>
 
 namespace moonep {
@@ -276,7 +275,7 @@ extern "C" int moonep_grad_clip(int32_t n, void* const* grads, const int64_t* nu
     MOONEP_CHECK_PTR(norm);
     try {
         if (overlap(n, grads, numel, dtype)) return MOONEP_EINVAL;
-    } catch (const std::bad_alloc&) {
+    } catch (...) {                  // no memory for the list of a host that has none left
         return MOONEP_EINVAL;
     }
     hipStream_t s = static_cast<hipStream_t>(stream);

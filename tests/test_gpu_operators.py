@@ -512,6 +512,71 @@ def test_ffn_deterministic_and_streams():
 
 
 # ----------------------------------------------------------------------------
+# offsets past 32 bits
+# ----------------------------------------------------------------------------
+
+def test_norm_past_32_bits():
+    """More than 2^31 elements: the last rows are what they are alone."""
+    H = 8192
+    rows = (1 << 31) // H + 3
+    x, dy = (torch.empty(1, rows, H, dtype=BF, device=DEV).normal_() for _ in range(2))
+    w, b = _params(H, 30)
+    y = torch.empty_like(x)
+    mean, rstd, dw, db = (torch.empty(n, device=DEV) for n in (rows, rows, H, H))
+    d = _norm_dims(rows, H, BF)
+    ws = torch.empty(M.moonep_layer_norm_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+    M.moonep_layer_norm(d, x, w, b, EPS, y, mean, rstd)
+    small = _norm_dims(5, H, BF)
+    part = torch.empty(1, 5, H, dtype=BF, device=DEV)
+    M.moonep_layer_norm(small, x[:, -5:].clone(), w, b, EPS, part)
+    assert torch.equal(part, y[:, -5:])
+    M.moonep_layer_norm_backward(d, dy, x, w, mean, rstd, y, dw, db, ws)
+    M.moonep_layer_norm_backward(small, dy[:, -5:].clone(), x[:, -5:].clone(), w, mean[-5:].clone(), rstd[-5:].clone(),
+                                 part, None, None)
+    assert torch.equal(part, y[:, -5:])
+    ref = torch.zeros(H, dtype=torch.float64, device=DEV)
+    mass = torch.zeros(H, dtype=torch.float64, device=DEV)
+    for at in range(0, rows, 1 << 15):
+        block = dy[0, at:at + (1 << 15)].double()
+        ref += block.sum(0)
+        mass += block.abs().sum(0)
+    # at most `rows` additions follow one another (and far fewer do)
+    assert bool(((db.double() - ref).abs() <= rows * U * mass).all())
+
+
+def test_clip_past_32_bits():
+    n = (1 << 31) + 5
+    g = torch.full((n,), 2.0 ** -10, device=DEV)
+    gl = M.GradList([g])
+    norm = _norm_of(gl)
+    want = np.sqrt(float(n)) * 2.0 ** -10
+    assert abs(float(norm) - want) <= want * U * 1.01
+    M.moonep_grad_clip(gl, norm, float(norm) / 4)            # an exact quarter
+    for part in (g[:7], g[n // 2:n // 2 + 7], g[-7:]):
+        assert torch.equal(part, torch.full((7,), 2.0 ** -12, device=DEV))
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_ffn_past_32_bits(T):
+    """Codes of more than 2^32 bytes: the last experts give what they give alone."""
+    E, K, H, I = 320, 2, 7168, 2048
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(31)
+    packed = []
+    for kin, n in ((H, 2 * I), (I, H)):
+        packed.append(torch.randint(0, 256, (E, M.moonep_w4_code_bytes(kin, n)), dtype=torch.uint8, device=DEV, generator=gen))
+        packed.append(torch.full((E, M.moonep_w4_scale_bytes(kin, n)), 120, dtype=torch.uint8, device=DEV))
+    assert packed[0].numel() > 1 << 32
+    rng = np.random.default_rng(32)
+    topk = np.stack([rng.permutation([0, E - 1]) for _ in range(T)]).astype(np.int32)
+    gates, x = rng.random((T, K)).astype(np.float32), _bits(rng.standard_normal((T, H)))
+    out = _run_ffn(topk, gates, x, packed[:2], packed[2:], E, H, I)
+    few = [p[[0, E - 1]].contiguous() for p in packed]
+    alone = _run_ffn(np.minimum(topk, 1), gates, x, few[:2], few[2:], 2, H, I)
+    assert torch.isfinite(out).all() and torch.equal(out, alone)
+
+
+# ----------------------------------------------------------------------------
 # a step of them together
 # ----------------------------------------------------------------------------
 
