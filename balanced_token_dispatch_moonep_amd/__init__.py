@@ -448,8 +448,10 @@ def moonep_layer_norm_backward(d: Dims, dy, x, weight, mean, rstd, dx, dweight, 
 
 class GradList:
     """The gradients that moonep_grad_norm and moonep_grad_clip work on: contiguous float32 or bf16
-    GPU tensors of any shape, made once and used step after step.  It keeps the tensors; every call
-    takes their addresses of that moment."""
+    GPU tensors of any shape, made once and used step after step.
+
+    Every call takes the addresses of that moment (a tensor given other memory is followed, if it is
+    of the same size); a tensor's extent is the one that it had when the list last met that memory."""
 
     def __init__(self, tensors):
         torch = _torch()
@@ -465,22 +467,22 @@ class GradList:
         self.n = n
         self.device = self.tensors[0].device if n else None
         self._numel = [t.numel() for t in self.tensors]
-        self._at = (None, None)      # addresses of the last call, and the same for C
         self._c_numel = (ctypes.c_int64 * n)(*self._numel)
         self._c_dtype = (ctypes.c_int32 * n)(*(types[t.dtype] for t in self.tensors))
+        self._met = (None, None, ())     # addresses, the same for C, and what keeps that memory alive
 
     def _arrays(self):
         torch = _torch()
         if self.n and self.device.index != torch.cuda.current_device():
             raise ValueError(f"the gradients are on {self.device}; the library runs on the current device "
                              f"cuda:{torch.cuda.current_device()}")
-        if [t.numel() if t.is_contiguous() else -1 for t in self.tensors] != self._numel:
-            raise ValueError("a gradient changed its size or layout since the list was made")
         at = [t.data_ptr() for t in self.tensors]
-        known, c_at = self._at
-        if at != known:
+        met, c_at, _ = self._met
+        if at != met:
+            if [t.numel() if t.is_contiguous() else -1 for t in self.tensors] != self._numel:
+                raise ValueError("a gradient changed its size or layout since the list was made")
             c_at = (ctypes.c_void_p * self.n)(*at)
-            self._at = (at, c_at)
+            self._met = (at, c_at, tuple(t.detach() for t in self.tensors))
         return self.n, c_at, self._c_numel, self._c_dtype
 
 

@@ -16,13 +16,14 @@
 // experts of H 7168, I 2048, 8 a token (one pass among others, weights not in the caches):
 //     tokens   experts read   us     TB/s of weights
 //        1           8        35       5.3
-//        8          28       110       5.9
-//       64          32       146       5.1
-//      128          32       212       3.5, 425 TFLOP/s
+//        8          28       108       6.0
+//       64          32       143       5.2
+//      128          32       201       3.7, 450 TFLOP/s
 // The loads skip the caches' keeping (ld_nt): with plain ones 16 tokens took 141 us instead of 125.
-// From about 16 rows an expert on, LDS reads and matrix instructions add to that (128 tokens: matrix
-// cores busy 30% of the time); the 32 x 32 x 16 instruction in place of the 16 x 16 x 32 one gave 224
-// to 270 us.
+// From about 16 rows an expert on, matrix instructions add to that: at 128 tokens, with two terms of
+// the activation and tiles of 16 rows in part empty, they do 1.6 times the 90 GFLOP of the
+// products themselves, at 0.74 PFLOP/s.  Operands read and widened a step ahead gave 202 us instead of 206,
+// the 32 x 32 x 16 instruction in place of the 16 x 16 x 32 one (as fast for each product) 224 to 270.
 //
 // Rows go through LDS, and not from global memory to the operand: loads return in order, so a wait
 // for rows would be a wait for the weights that were asked for before them.  This and a loop in which

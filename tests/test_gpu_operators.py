@@ -312,7 +312,13 @@ def test_grad_list_empty_and_refusals():
         M.GradList([g.view(8, 8).t()])
     h = torch.zeros(64, device=DEV)
     gl = M.GradList([h])
+    assert float(_norm_of(gl)) == 0.0
+    h.data = torch.ones(64, device=DEV)                      # other memory of the same size is followed
+    assert float(_norm_of(gl)) == 8.0
     h.data = torch.ones(32, device=DEV)
+    with pytest.raises(ValueError, match="changed"):
+        _norm_of(gl)
+    h.data = torch.ones(8, 8, device=DEV).t()[:, ::2].reshape(32).expand(2, 32)[:, :32]
     with pytest.raises(ValueError, match="changed"):
         _norm_of(gl)
 
