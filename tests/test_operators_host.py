@@ -140,6 +140,14 @@ def test_ffn_refuses():
     assert M.W4_MAX_PAIRS == 8192
 
 
+@pytest.mark.parametrize("E,K,H,I", [(32, 8, 7168, 2048), (8, 4, 1024, 512), (1, 1, 32, 32), (64, 2, 32, 512), (256, 8, 64, 32)])
+def test_ffn_workspace_serves_smaller_batches(E, K, H, I):
+    """A decoder's scratch for its largest batch serves the smaller ones."""
+    sizes = [M.moonep_w4_ffn_workspace_bytes(_dims(E=E, K=K, H=H, I=I, S=s)) for s in range(1, 8192 // K + 1, 3)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert all(n % 256 == 0 and n > 0 for n in sizes)
+
+
 def test_binding_refuses_cpu_tensors():
     torch = pytest.importorskip("torch")
     d = M.Dims.make(1, 1, 0, 4, 1, 64)
