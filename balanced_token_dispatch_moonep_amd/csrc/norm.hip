@@ -182,12 +182,21 @@ __global__ __launch_bounds__(LPR > 0 ? 256 : 1024) void norm_kernel(const uint4*
 
 // One pass over dy and x: dx, and the workgroup's share of the sums over rows in
 // ws[workgroup][0] = sum dy n, ws[workgroup][1] = sum dy (ws NULL: not wanted).
-template <bool F32, int LPR, int NV>
-__global__ __launch_bounds__(LPR > 0 ? 256 : 512) void norm_backward_kernel(
+// LONG, for rows of more than 8 waves, whose lanes have half the registers: the weights are read again for
+// each row (from the caches) and the next row is asked for at the end of a row, not at its start.  At 8192
+// rows of 16384 bf16 178 us, of 8200 105; with four vectors a lane and 8 waves, which spills, 203 and 165,
+// with the next row held across the sums 180 and 119.  At 4096 rows of 16384 fp32 155 us, where the kernels
+// for longer rows take 337.
+template <bool F32, int LPR, int NV, bool LONG>
+__global__ __launch_bounds__(LPR > 0 ? 256 : LONG ? 1024 : 512) void norm_backward_kernel(
     const uint4* __restrict__ dy, const uint4* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ mean, const float* __restrict__ rstd, uint4* __restrict__ dx, float* __restrict__ ws,
     int rows, int nv) {
     constexpr int N = RowVec<F32>::N;
+    // Lanes past the row read its last vector instead of none: no branches, 13 registers fewer and so
+    // nothing spilled (fp32, 16384 wide: 263 -> 161 us).  Elsewhere the branches are as fast or faster
+    // (7168 bf16: 245 us, without 250; 8200 bf16: 104, without 112).
+    constexpr bool CLAMP = F32 && LONG;
     __shared__ float lds[4][16];
     const int lanes = LPR > 0 ? LPR : blockDim.x;
     const int lane = LPR > 0 ? threadIdx.x & (LPR - 1) : threadIdx.x;
@@ -195,14 +204,15 @@ __global__ __launch_bounds__(LPR > 0 ? 256 : 512) void norm_backward_kernel(
     const int stride = gridDim.x * at_once;
     const float n = (float)nv * N;
     int row = blockIdx.x * at_once + (LPR > 0 ? threadIdx.x / LPR : 0);
-    float wf[NV][N], aw[NV][N], ab[NV][N];
+    float wf[LONG ? 1 : NV][N], aw[NV][N], ab[NV][N];
     uint4 nx[NV], nd[NV];
     float nm = 0.0f, nr = 0.0f;
     auto fetch = [&](int t) {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            const int v = lane + u * lanes;
-            if (v >= nv) continue;
+            int v = lane + u * lanes;
+            if (CLAMP) v = min(v, nv - 1);
+            else if (v >= nv) continue;
             nx[u] = x[(size_t)t * nv + v];
             nd[u] = dy[(size_t)t * nv + v];
         }
@@ -212,7 +222,7 @@ __global__ __launch_bounds__(LPR > 0 ? 256 : 512) void norm_backward_kernel(
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         const int v = lane + u * lanes;
-        if (v < nv) load_param<N>(w, v, 1.0f, wf[u]);
+        if (!LONG && v < nv) load_param<N>(w, v, 1.0f, wf[u]);
 #pragma unroll
         for (int i = 0; i < N; ++i) aw[u][i] = ab[u][i] = 0.0f;
     }
@@ -227,21 +237,31 @@ __global__ __launch_bounds__(LPR > 0 ? 256 : 512) void norm_backward_kernel(
                 unpack_row<F32>(nd[u], d[u]);
             } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) f[u][i] = d[u][i] = wf[u][i] = 0.0f;
+                for (int i = 0; i < N; ++i) f[u][i] = d[u][i] = wf[LONG ? 0 : u][i] = 0.0f;
             }
         }
-        if (row + stride < rows) fetch(row + stride);
+        if (!LONG && row + stride < rows) fetch(row + stride);
 #pragma unroll
-        for (int u = 0; u < NV; ++u)
+        for (int u = 0; u < NV; ++u) {
+            float* wu = wf[LONG ? 0 : u];
+            if (LONG) {
+                const bool in = lane + u * lanes < nv;
+                int at = in ? lane + u * lanes : nv - 1;
+                asm volatile("" : "+v"(at));     // not the same for each row: else the compiler keeps the weights
+                load_param<N>(w, at, 1.0f, wu);
+#pragma unroll
+                for (int i = 0; i < N; ++i) wu[i] = in ? wu[i] : 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 f[u][i] = (f[u][i] - m) * r;
                 aw[u][i] += d[u][i] * f[u][i];
                 ab[u][i] += d[u][i];
-                d[u][i] *= wf[u][i];
+                d[u][i] *= wu[i];
                 sg += d[u][i];
                 sn += d[u][i] * f[u][i];
             }
+        }
         float c1, c2;
         if constexpr (LPR > 0) {
             c1 = lanes_sum<LPR>(sg) / n;
@@ -271,6 +291,7 @@ __global__ __launch_bounds__(LPR > 0 ? 256 : 512) void norm_backward_kernel(
             for (int i = 0; i < N; ++i) f[u][i] = r * (d[u][i] - c1 - f[u][i] * c2);
             st_nt(pack_row<F32>(f[u]), dx + (size_t)row * nv + v);
         }
+        if (LONG && row + stride < rows) fetch(row + stride);
     }
     if (!ws) return;
     const size_t H = (size_t)nv * N;
@@ -467,25 +488,31 @@ static RowShape forward_shape(const moonep_dims_t* d) {
     return row_shape(d->H / (d->flags & MOONEP_F32_ROWS ? 4 : 8), 16);
 }
 
-// The backward holds two rows and its sums: workgroups of more than 8 waves would spill registers
-// (measured 336 us instead of 262 at 32768 rows of 7168 bf16).
+// The backward holds a row or two and its sums, 16 elements of each a lane: up to 8 waves with the weights
+// in registers too, up to 16 without them (LONG).
 static RowShape backward_shape(const moonep_dims_t* d) {
-    return row_shape(d->H / (d->flags & MOONEP_F32_ROWS ? 4 : 8), 8);
+    const bool f32 = (d->flags & MOONEP_F32_ROWS) != 0;
+    const int nv = d->H / (f32 ? 4 : 8), per = f32 ? 4 : 2, waves = (nv + 64 * per - 1) / (64 * per);
+    if (waves <= 8) return row_shape(nv, 8);
+    return waves <= 16 ? RowShape{0, waves, per} : RowShape{0, 4, 0};
 }
 
-// Workgroups of the backward, each with its share of the rows.  Eight waves a CU, 16 bytes of each row
-// a lane ahead: 244 us at 32768 x 7168 (16 waves 252, 24 waves 259), 43 us at 16384 x 2048 (16 waves 57):
-// fewer shares to write and join.
+// Workgroups of the backward, each with its share of the rows.  Eight waves a CU, or nine, 16 bytes of each
+// row a lane ahead: 244 us at 32768 x 7168 (16 waves 252, 24 waves 259), 43 us at 16384 x 2048 (16 waves
+// 57): fewer shares to write and join.  Workgroups of three waves: 52 us at 16384 x 2560 with three of them
+// a CU, 62 with two.  Of five: one a CU (105 us at 16384 x 5120, two 109), but two where a lane has 8
+// elements instead of 16 (16384 x 2056 fp32: 76 us, one 88).
 static int norm_splits(const moonep_dims_t* d) {
     const int rows = d->R * d->S;
     const RowShape s = backward_shape(d);
     if (s.per == 0) return std::min(rows, 2 * kCUs);
     const int at_once = s.lpr > 0 ? 256 / s.lpr : 1;
-    const int most = kCUs * (s.lpr > 0 ? 2 : std::max(1, 8 / s.waves));
+    const int waves = s.per == 2 && d->flags & MOONEP_F32_ROWS ? 8 + s.waves / 2 : 9;
+    const int most = kCUs * (s.lpr > 0 ? 2 : std::max(1, waves / s.waves));
     return std::min((rows + at_once - 1) / at_once, most);
 }
 
-template <bool F32, class F>
+template <class F>
 static void with_shape(const RowShape& s, F f) {
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
@@ -515,7 +542,7 @@ static void launch_norm(const moonep_dims_t* d, hipStream_t s, const uint4* x, c
     // 24 waves 83)
     const int most = kCUs * (sh.lpr > 0 ? 5 : std::max(1, 24 / sh.waves));
     const dim3 grid(std::min((rows + at_once - 1) / at_once, most));
-    with_shape<F32>(sh, [&](auto lpr, auto per) {
+    with_shape(sh, [&](auto lpr, auto per) {
         hipLaunchKernelGGL((norm_kernel<F32, lpr.value, per.value>), grid, dim3(64 * sh.waves), 0, s, x, w, b, y,
                            mean, rstd, rows, nv, eps);
     });
@@ -533,9 +560,16 @@ static void launch_norm_backward(const moonep_dims_t* d, hipStream_t s, const ui
                                rstd, ws, rows, nv);
         return;
     }
-    with_shape<F32>(sh, [&](auto lpr, auto per) {
-        hipLaunchKernelGGL((norm_backward_kernel<F32, lpr.value, per.value>), dim3(splits), dim3(64 * sh.waves), 0, s,
-                           dy, x, w, mean, rstd, dx, ws, rows, nv);
+    const dim3 grid(splits), block(64 * sh.waves);
+    if (sh.waves > 8) {
+        hipLaunchKernelGGL((norm_backward_kernel<F32, 0, F32 ? 4 : 2, true>), grid, block, 0, s, dy, x, w, mean, rstd,
+                           dx, ws, rows, nv);
+        return;
+    }
+    with_shape(sh, [&](auto lpr, auto per) {
+        if constexpr (F32 || per.value <= 2)
+            hipLaunchKernelGGL((norm_backward_kernel<F32, lpr.value, per.value, false>), grid, block, 0, s, dy, x, w,
+                               mean, rstd, dx, ws, rows, nv);
     });
 }
 

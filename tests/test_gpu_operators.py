@@ -169,6 +169,34 @@ def test_norm_backward_many_rows():
     _check_backward(3001, 1024, F32, seed=5)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,H", [(700, 2056), (520, 4104), (515, 5120), (300, 8200), (257, 12288), (513, 16384)])
+def test_norm_backward_several_rows_a_workgroup(rows, H, dtype):
+    _check_backward(rows, H, dtype, seed=6)
+    _check_backward(rows, H, dtype, weight=False, seed=7, accum=True)
+
+
+def test_norm_backward_of_an_infinite_weight():
+    """The last columns' weights are infinite and their dy is not zero: c1 is infinite in each row, and
+    the other columns' sums over rows stay finite."""
+    rows, H = 300, 8200
+    for dtype in (BF, F32):
+        x, dy = _rows(rows, H, dtype, 8), _rows(rows, H, dtype, 58)
+        dy[:, -1] = 1.0
+        w = torch.ones(H, device=DEV)
+        w[-1] = float("inf")
+        xs, ds = f64_of(x), f64_of(dy)
+        _, m, r = A.layer_norm(xs, None, None, EPS)
+        d = _norm_dims(rows, H, dtype)
+        ws = torch.full((M.moonep_layer_norm_workspace_bytes(d),), 255, dtype=torch.uint8, device=DEV)
+        dx, dw, db = torch.empty_like(x[None]), torch.empty(H, device=DEV), torch.empty(H, device=DEV)
+        M.moonep_layer_norm_backward(d, dy[None], x[None], w, f32(m), f32(r), dx, dw, db, ws)
+        torch.cuda.synchronize()
+        assert not np.isfinite(f64_of(dx)).any()
+        _far(f64_of(db), ds.sum(0), (rows + 16) * U * np.abs(ds).sum(0) + 2 * U * np.abs(ds.sum(0)), "dbias")
+        assert torch.isfinite(dw).all()
+
+
 def test_norm_gradient_against_differences():
     """dx, dweight and dbias predict how the library's own forward changes, in float32.
 
