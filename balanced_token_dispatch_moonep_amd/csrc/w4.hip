@@ -42,6 +42,7 @@ constexpr int kBlock = 128;          // input values of one wave's load
 constexpr int kFour = 4 * kBlock;    // input values of four blocks, whose scales come in one load
 constexpr int kTile = 16;            // rows a matrix instruction takes, columns of a tile
 constexpr int kFewPairs = 64;        // one wave can look at all their ids
+constexpr int kCUs = 256;
 
 struct W4Dims {
     int T, K, E, H, I;
@@ -75,13 +76,18 @@ struct W4Ws {
     int max_up, max_down;
 };
 
-// Whether the kernels for few pairs take a call.  They split an expert's weights finer, but read rows
-// and first terms once more for every 16 columns: 32 pairs over 23 of 32 experts of H 7168, I 2048
-// took 92 us there and 96 with the others, 64 pairs over 28 of them 122 and 114; where the others'
-// workgroups do not fill the chip, 64 pairs over 8 experts of H 1024, I 512 took 12 and 17.
+// Whether the kernels for few pairs take a call.  They are two launches instead of four and split an
+// expert's weights finer, but a workgroup of the second product goes through all pairs, I values each,
+// one after the other, and an expert's weights are read again for each eight of its pairs (four in the
+// second product).  us there and with the others: 32 pairs over 8 experts of H 4096, I 1024 17 and 23,
+// 64 pairs 25 and 23; 16 pairs over 7 of H 2048, I 2048 17 and 21, 64 pairs 32 and 23; 64 pairs over 28 of
+// H 4096, I 512 25 and 28.  Where reading the weights takes longer than that, some more pairs: 32 over 23
+// of 32 experts of H 7168, I 2048 89 and 93, over 12 of 16 experts 53 and 59, but over 4 of 4 39 and 31;
+// 48 over 24 of 32 100 and 97.
 static bool w4_few(const W4Dims& d) {
     const int pairs = d.T * d.K;
-    return pairs <= kFewPairs / 2 || (pairs <= kFewPairs && std::min(pairs, d.E) * ((d.I + 63) / 64) < 512);
+    if (pairs > kFewPairs) return false;
+    return (int64_t)pairs * d.I <= 24 * 2048 || (d.H > 4096 && pairs <= std::min(32, 2 * d.E));
 }
 
 static int blocks_of(int kin) { return (kin + kBlock - 1) / kBlock; }
@@ -296,14 +302,14 @@ __device__ __forceinline__ void with_rows(int n, F f) {
 // act = silu(x G) * (x U) for one expert and 16 columns.  The waves deal out the input direction and
 // join their sums in order.  blockIdx.y: a pair, that leads its expert's group if it is the first of
 // it, or an expert where there are fewer experts than pairs.
-// Four waves, three to a SIMD (168 registers): 65 us at 2 tokens; five waves 73; four to a SIMD (128
-// registers, spilled) 97.
-constexpr int kUpWaves = 4;
-
-__global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32_t* __restrict__ topk,
-                                                                     const uint16_t* __restrict__ x, W4Mat m,
-                                                                     uint16_t* __restrict__ act, W4Dims d) {
-    __shared__ uint4 lds[kUpWaves][8 * 64];
+// WAVES: four, three to a SIMD (168 registers): 65 us at 2 tokens; five waves 73; four to a SIMD (128
+// registers, spilled) 97.  Two where H has no more than two fours, and more waves would only wait (H 1024,
+// I 2048, 16 pairs over 14 experts: 19.9 us, four 22.1).
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 3) void w4_few_up_kernel(const int32_t* __restrict__ topk,
+                                                                  const uint16_t* __restrict__ x, W4Mat m,
+                                                                  uint16_t* __restrict__ act, W4Dims d) {
+    __shared__ uint4 lds[WAVES][8 * 64];
     const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), c = lane & 15;
     const int id = pair_expert(topk, pairs, d.E);
     const int e = pairs <= d.E ? __builtin_amdgcn_readlane(id, blockIdx.y) : blockIdx.y;
@@ -317,7 +323,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32
         f32x4_t acc[2];
         __syncthreads();
         with_rows(rows, [&](auto rn) {
-            multiply_few<rn.value, 2>(acc, m, tile, wave, kUpWaves, lds[wave], [&](int r) {
+            multiply_few<rn.value, 2>(acc, m, tile, wave, WAVES, lds[wave], [&](int r) {
                 return x + (size_t)(__builtin_amdgcn_readlane(pair, min(r0 + r, n - 1)) / d.K) * d.H;
             });
         });
@@ -332,7 +338,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32
             const int at = (r / 4 * 16 + c) * 4 + r % 4;
             float gate = 0.0f, up = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kUpWaves; ++w) {
+            for (int w = 0; w < WAVES; ++w) {
                 gate += reinterpret_cast<const float*>(lds[w])[at];
                 up += reinterpret_cast<const float*>(lds[w])[256 + at];
             }
@@ -347,14 +353,15 @@ __global__ __launch_bounds__(64 * kUpWaves, 3) void w4_few_up_kernel(const int32
 
 // out for 16 columns and all tokens: the waves take the experts in turn, each group's rows go to LDS,
 // and a token's are joined in k order.  The rows of a matrix instruction are the two terms of 4 pairs.
-// Four waves: 35.6 us at one token, 89 at four; eight 37.5 and 91 (one workgroup a CU), six 41.
-constexpr int kDownWaves = 4;
-
-__global__ __launch_bounds__(64 * kDownWaves, 2) void w4_few_down_kernel(const int32_t* __restrict__ topk,
-                                                                         const float* __restrict__ gates,
-                                                                         const uint16_t* __restrict__ act, W4Mat m,
-                                                                         uint16_t* __restrict__ out, W4Dims d) {
-    __shared__ uint4 lds[kDownWaves][8 * 64];
+// WAVES: four where there are more workgroups than CUs (H 7168: 35.6 us at one token, 89 at four; eight
+// 37.5 and 91, as a CU holds one workgroup of them, six 41), else eight (H 4096, I 512, 64 pairs over 28
+// experts: 24 us, four 28).
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void w4_few_down_kernel(const int32_t* __restrict__ topk,
+                                                                    const float* __restrict__ gates,
+                                                                    const uint16_t* __restrict__ act, W4Mat m,
+                                                                    uint16_t* __restrict__ out, W4Dims d) {
+    __shared__ uint4 lds[WAVES][8 * 64];
     __shared__ float y[kFewPairs][kTile];
     const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), c = lane & 15, q = lane >> 4;
     const int id = pair_expert(topk, pairs, d.E);
@@ -363,7 +370,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void w4_few_down_kernel(const i
         const int e = __builtin_amdgcn_readlane(id, __ffsll(left) - 1);
         const unsigned long long members = __ballot(id == e);
         left &= ~members;
-        if (turn % kDownWaves != wave) continue;
+        if (turn % WAVES != wave) continue;
         const int n = __popcll(members), pair = member_pair(members);
         const size_t tile[1] = {(size_t)e * m.nb + blockIdx.x};
         for (int r0 = 0; r0 < n; r0 += 4) {
@@ -382,7 +389,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void w4_few_down_kernel(const i
         }
     }
     __syncthreads();
-    for (int v = threadIdx.x; v < d.T * kTile; v += 64 * kDownWaves) {
+    for (int v = threadIdx.x; v < d.T * kTile; v += 64 * WAVES) {
         const int t = v / kTile, col = v % kTile;
         float s = 0.0f;
         for (int p = t * d.K; p < (t + 1) * d.K; ++p)
@@ -753,11 +760,18 @@ extern "C" int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, con
     const W4Mat up = w4_mat(w13_codes, w13_scales, d.H, 2 * d.I), down = w4_mat(w2_codes, w2_scales, d.I, d.H);
     const uint16_t* xr = static_cast<const uint16_t*>(x);
     if (w4_few(d)) {
-        hipLaunchKernelGGL(w4_few_up_kernel, dim3(d.I / kTile, std::min(d.T * d.K, d.E)), dim3(64 * kUpWaves), 0, s,
-                           topk, xr, up, w.act, d);
+        const dim3 up_grid(d.I / kTile, std::min(d.T * d.K, d.E));
+        if (d.H > 2 * kFour)
+            hipLaunchKernelGGL(w4_few_up_kernel<4>, up_grid, dim3(64 * 4), 0, s, topk, xr, up, w.act, d);
+        else
+            hipLaunchKernelGGL(w4_few_up_kernel<2>, up_grid, dim3(64 * 2), 0, s, topk, xr, up, w.act, d);
         MOONEP_LAUNCH_CHECK();
-        hipLaunchKernelGGL(w4_few_down_kernel, dim3(d.H / kTile), dim3(64 * kDownWaves), 0, s, topk, gates, w.act,
-                           down, static_cast<uint16_t*>(out), d);
+        uint16_t* o = static_cast<uint16_t*>(out);
+        const dim3 grid(d.H / kTile);
+        if (grid.x > kCUs)
+            hipLaunchKernelGGL(w4_few_down_kernel<4>, grid, dim3(64 * 4), 0, s, topk, gates, w.act, down, o, d);
+        else
+            hipLaunchKernelGGL(w4_few_down_kernel<8>, grid, dim3(64 * 8), 0, s, topk, gates, w.act, down, o, d);
         MOONEP_LAUNCH_CHECK();
         return MOONEP_OK;
     }

@@ -470,6 +470,16 @@ def test_ffn(T, K, E, H, I):
     _check_ffn(T, K, E, H, I, seed=T + H)
 
 
+# both sides of what decides between the ways of a call: 64 and 65 pairs, H of 1024 and 4096 and more,
+# pairs times I of 49152 and more
+@pytest.mark.parametrize("T,K,E,H,I", [
+    (8, 8, 32, 1024, 96), (8, 8, 32, 1056, 96), (13, 5, 32, 1056, 96), (16, 4, 4, 4096, 64), (16, 4, 4, 4128, 64),
+    (16, 3, 16, 96, 1024), (17, 3, 16, 96, 1024), (3, 1, 2, 8224, 32),
+])
+def test_ffn_ways(T, K, E, H, I):
+    _check_ffn(T, K, E, H, I, seed=T + H)
+
+
 @pytest.mark.parametrize("R", [2, 4])
 def test_ffn_ranks(R):
     _check_ffn(8, 2, 6, 128, 64, seed=1, R=R)
