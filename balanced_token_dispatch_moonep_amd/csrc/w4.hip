@@ -60,11 +60,18 @@ struct Chunk {
     int32_t expert, first, n;        // its pairs are pair[first] .. pair[first + n)
 };
 
-// Pairs a chunk of the first product, and of the second, whose rows are two a pair.  Halves of these
+// Most pairs a chunk of the first product, and of the second, whose rows are two a pair.  Halves of these
 // took 237 us at 128 tokens instead of 208 (weights are read again for each chunk), three quarters 220,
 // twice 205 with registers spilled.
 constexpr int kUpRows = 64;
 constexpr int kDownPairs = 32;
+
+// Pairs a chunk of the first product.  Where a chunk of each expert is less than a round of workgroups (two
+// a CU), weights read again cost less than CUs without work: 256 pairs over 4 experts of H 7168, I 2048
+// 54 us with chunks of 32 and 67 of 64, 800 over 16 of H 4096, I 1024 58 and 67, 200 over 8 of H 4096, I 512 28
+// and 33; with a round or more, 1024 pairs over 32 of H 7168, I 2048 229 and 207.  Less than a round but not
+// much, 256 pairs over 8 of H 4096, I 2048 52 and 49, 512 pairs 71 and 74.
+static int w4_up_rows(const W4Dims& d) { return d.E * ((d.I + 63) / 64) < 2 * kCUs ? kUpRows / 2 : kUpRows; }
 
 // Scratch; few pairs need only act.
 struct W4Ws {
@@ -74,6 +81,7 @@ struct W4Ws {
     int32_t* chunks;                 // how many of each
     Chunk *up, *down;
     int max_up, max_down;
+    int up_rows;
 };
 
 // Whether the kernels for few pairs take a call.  They are two launches instead of four and split an
@@ -105,7 +113,8 @@ static size_t w4_ws_layout(const W4Dims& d, void* base, W4Ws* ws) {
     w.act = (uint16_t*)take(pairs * 2 * d.I * 2);
     if (!w4_few(d)) {
         // an expert leaves less than one chunk partly empty
-        w.max_up = (int)(experts + pairs / kUpRows);
+        w.up_rows = w4_up_rows(d);
+        w.max_up = (int)(experts + pairs / w.up_rows);
         w.max_down = (int)(experts + pairs / kDownPairs);
         w.y = (float*)take(pairs * d.H * 4);
         w.pair = (int32_t*)take(pairs * 4);
@@ -425,7 +434,7 @@ __global__ __launch_bounds__(1024) void w4_group_kernel(const int32_t* __restric
         if ((unsigned)id < (unsigned)E) atomicAdd(&count[id], 1);
     }
     __syncthreads();
-    const int n = count[e], up = (n + kUpRows - 1) / kUpRows, down = (n + kDownPairs - 1) / kDownPairs;
+    const int n = count[e], up = (n + w.up_rows - 1) / w.up_rows, down = (n + kDownPairs - 1) / kDownPairs;
     const int s0 = wave_scan(n), s1 = wave_scan(up), s2 = wave_scan(down);
     if (lane == 63) {
         sums[0][wave] = s0;
@@ -440,7 +449,7 @@ __global__ __launch_bounds__(1024) void w4_group_kernel(const int32_t* __restric
         d0 += sums[2][i];
     }
     place[e] = first;
-    for (int i = 0; i < up; ++i) w.up[u0 + i] = Chunk{e, first + i * kUpRows, min(kUpRows, n - i * kUpRows)};
+    for (int i = 0; i < up; ++i) w.up[u0 + i] = Chunk{e, first + i * w.up_rows, min(w.up_rows, n - i * w.up_rows)};
     for (int i = 0; i < down; ++i) w.down[d0 + i] = Chunk{e, first + i * kDownPairs, min(kDownPairs, n - i * kDownPairs)};
     if (e == 1023) {
         w.chunks[0] = u0 + up;

@@ -480,6 +480,18 @@ def test_ffn_ways(T, K, E, H, I):
     _check_ffn(T, K, E, H, I, seed=T + H)
 
 
+@pytest.mark.parametrize("E", [511, 512])
+@pytest.mark.parametrize("used", [2, 5, 9])
+def test_ffn_chunks(E, used):
+    """Up to 200 rows an expert, of 511 experts of 32 (in chunks of 32 rows) and of 512 (of 64)."""
+    topk, gates, x, w13, w2 = _ffn_case(200, 2, E, 96, 32, seed=used)
+    topk = topk % used * 37
+    out = _run_ffn(topk, gates, x, _packed(w13), _packed(w2), E, 96, 32)
+    torch.cuda.synchronize()
+    ref, off = A.w4_ffn(W.bf16_to_f32(x), topk, gates, _values(w13), _values(w2))
+    _far(f64_of(out), ref, off + 2.0 ** -8 * np.abs(ref) * (1 + 1e-2), "out")
+
+
 @pytest.mark.parametrize("R", [2, 4])
 def test_ffn_ranks(R):
     _check_ffn(8, 2, 6, 128, 64, seed=1, R=R)
