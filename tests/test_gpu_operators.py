@@ -351,6 +351,23 @@ def test_grad_list_empty_and_refusals():
         _norm_of(gl)
 
 
+@pytest.mark.parametrize("change", [lambda t: t.bfloat16(), lambda t: t.cpu(), lambda t: t[:16],
+                                    lambda t: t.view(torch.int32)], ids=["type", "host", "part", "type in place"])
+def test_grad_list_refuses_a_changed_tensor(change):
+    """Neither call launches anything: the tensors and the norm stay as they were."""
+    g, h = torch.ones(64, device=DEV), torch.full((5,), 2.0, device=DEV)
+    gl = M.GradList([g, h])
+    ws = torch.empty(M.moonep_grad_norm_workspace_bytes(gl), dtype=torch.uint8, device=DEV)
+    norm = torch.full((1,), 100.0, device=DEV)
+    g.data = change(g.data)
+    now = g.detach().clone()
+    with pytest.raises(ValueError, match="changed"):
+        M.moonep_grad_norm(gl, ws, norm)
+    with pytest.raises(ValueError, match="changed"):
+        M.moonep_grad_clip(gl, norm, 1.0)
+    assert torch.equal(g, now) and float(norm) == 100.0 and bool((h == 2.0).all())
+
+
 # ----------------------------------------------------------------------------
 # 4-bit weights
 # ----------------------------------------------------------------------------

@@ -171,3 +171,39 @@ def test_new_constants_match_header():
     found = dict(re.findall(r"#define MOONEP_([A-Z0-9_]+) (\d+)\n", text))
     assert int(found["W4_MAX_PAIRS"]) == M.W4_MAX_PAIRS
     assert (int(found["GRAD_F32"]), int(found["GRAD_BF16"])) == (0, 1)
+
+
+CHANGES = {
+    "type": lambda t, torch: t.bfloat16(),
+    "type at the same address": lambda t, torch: t.view(torch.int32),
+    "type and length at the same address": lambda t, torch: t.view(torch.bfloat16)[:64],
+    "part at the same address": lambda t, torch: t[:16],
+    "one element, repeated": lambda t, torch: t[:1].expand(64),
+    "other order": lambda t, torch: t.view(8, 8).t(),
+}
+
+
+@pytest.mark.parametrize("name", [*CHANGES, "resized"])
+def test_grad_list_refuses_a_changed_tensor(monkeypatch, name):
+    """Whatever the kernels take for granted of a tensor is looked at in each call, at an old address
+    too.  Host tensors stand for the GPU's; nothing is launched."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(M, "_ptr", lambda t, *a, **k: t.data_ptr())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    g, h = torch.zeros(64), torch.zeros(3)
+    gl = M.GradList([h, g])
+    n, at, numel, dtype = gl._arrays()
+    assert (n, list(at), list(numel), list(dtype)) == (2, [h.data_ptr(), g.data_ptr()], [3, 64], [0, 0])
+    g.data = torch.zeros(64)                                 # other memory of the same form is followed
+    assert list(gl._arrays()[1]) == [h.data_ptr(), g.data_ptr()]
+    keep = g.data
+    if name == "resized":
+        g.resize_(16)
+    else:
+        g.data = CHANGES[name](keep, torch)
+    with pytest.raises(ValueError, match="changed"):
+        gl._arrays()
+    with pytest.raises(ValueError, match="changed"):         # and stays refused
+        gl._arrays()
+    g.data = keep if name != "resized" else torch.zeros(64)
+    assert list(gl._arrays()[1]) == [h.data_ptr(), g.data_ptr()]
