@@ -33,6 +33,11 @@ def _nbytes(shape, itemsize):
     return n
 
 
+def _within(x, buf) -> bool:
+    """Whether x begins in the memory of buf, a whole allocation."""
+    return 0 <= x.data_ptr() - buf.data_ptr() < buf.nbytes
+
+
 class MoonEPPool:
     """Process-global prefetch slots shared by every layer [AT, TL;DR; TD, memory contract].
 
@@ -76,7 +81,8 @@ class MoonEPLayer:
     With ``norm_weight`` [H] (float32; ``norm_bias`` [H] or None) the rows are layer-normed before
     they are dispatched, and ``backward`` returns the gradient of the rows before the norm; it also
     writes ``dnorm_weight`` and ``dnorm_bias``.  A router that reads the normed rows calls ``norm(x)``
-    itself; ``forward`` given what that returned does not norm again.
+    itself; ``forward`` given what that returned does not norm again, and given a copy of it does not
+    with ``normed=True``.  ``backward`` goes back to the rows of the last ``norm(x)``.
     """
 
     def __init__(self, dims: Dims, w13=None, w2=None, training: bool = False, device="cuda", pool=None,
@@ -140,7 +146,10 @@ class MoonEPLayer:
 
     # -- steps ---------------------------------------------------------------
     def norm(self, x):
-        """Layer norm of the rows [R, S, H]; x must stay as it is until the backward."""
+        """Layer norm of the rows [R, S, H] (a static buffer, replaced by the next call); x must stay as
+        it is until the backward."""
+        if _within(x, self.normed):
+            raise ValueError("norm of rows that norm() returned: it would write over what it reads")
         moonep_layer_norm(self.d, x, self.norm_weight, self.norm_bias, self.norm_eps, self.normed, self.mean,
                           self.rstd)
         self.x = x
@@ -166,10 +175,15 @@ class MoonEPLayer:
     def combine(self, gates):
         moonep_combine(self.d, self.dest, self.y, gates, self.out)
 
-    def forward(self, x, topk, gates):
-        """Returns the [R, S, H] output (a view of a static buffer, replaced by the next call)."""
-        if self.norm_weight is not None and x.data_ptr() != self.normed.data_ptr():
-            x = self.norm(x)
+    def forward(self, x, topk, gates, normed=False):
+        """Returns the [R, S, H] output (a view of a static buffer, replaced by the next call).
+
+        ``normed``: x is a copy of what norm() returned last (what it returned itself need not say so)."""
+        if self.norm_weight is not None:
+            if not normed and not _within(x, self.normed):
+                x = self.norm(x)
+            elif self.training and self.x is None:
+                raise ValueError("normed rows without a call of norm(), whose rows the backward goes back to")
         self.plan(topk)
         self.prefetch()
         self.dispatch(x)
@@ -255,20 +269,23 @@ class W4Experts:
         return Dims.make(1, self.E, 0, T, self.K, self.H, self.I)
 
     def norm(self, x):
-        """Layer norm of the tokens x [T, H] (a view of a static buffer)."""
+        """Layer norm of the tokens x [T, H] (a view of a static buffer, replaced by the next call)."""
+        if _within(x, self.normed):
+            raise ValueError("norm of rows that norm() returned: it would write over what it reads")
         T = x.shape[0]
         d = Dims.make(1, 1, 0, T, 1, self.H)
         moonep_layer_norm(d, x.unsqueeze(0), self.norm_weight, self.norm_bias, self.norm_eps,
                           self.normed[:T].unsqueeze(0))
         return self.normed[:T]
 
-    def forward(self, x, topk, gates):
-        """x [T, H] bf16 (before the norm, or what norm(x) returned), topk [T, K] int32 (-1: nothing),
-        gates [T, K] float32 -> [T, H] bf16 (a view of a static buffer)."""
+    def forward(self, x, topk, gates, normed=False):
+        """x [T, H] bf16, topk [T, K] int32 (-1: nothing), gates [T, K] float32 -> [T, H] bf16 (a view of a
+        static buffer).  x is what comes before the norm, or what norm() returned or some of its tokens,
+        or with ``normed`` a copy of such."""
         T = x.shape[0]
         if not 1 <= T <= self.max_tokens:
             raise ValueError(f"{T} tokens: this decoder takes 1 to {self.max_tokens}")
-        if self.norm_weight is not None and x.data_ptr() != self.normed.data_ptr():
+        if self.norm_weight is not None and not normed and not _within(x, self.normed):
             x = self.norm(x)
         d = self._dims(T)
         ws = self.ws[:moonep_w4_ffn_workspace_bytes(d)]

@@ -740,6 +740,38 @@ def test_decoding_follows_the_layer():
         dec.forward(x[:33], i32(topk.reshape(-1, cfg.K)[:33]), f32(gates.reshape(-1, cfg.K)[:33]))
 
 
+def test_decoding_normed_rows_in_parts():
+    """The normed rows in two calls, as a copy, and over themselves.  All calls are of few pairs, whose
+    sums do not depend on the batch: the same bits."""
+    layer, topk, gates, _, _ = _layer(CFG, False)
+    T, K = 24, CFG.K
+    x, tk, g = _rows(T, CFG.H, BF, 13), i32(topk.reshape(-1, K)[:T]), f32(gates.reshape(-1, K)[:T])
+    dec = layer.decoder(max_tokens=32)
+    want = dec.forward(x, tk, g).clone()
+    n = dec.norm(x)
+    parts = [dec.forward(n[lo:hi], tk[lo:hi], g[lo:hi]).clone() for lo, hi in ((0, 9), (9, T))]
+    assert torch.equal(torch.cat(parts), want)
+    assert torch.equal(dec.forward(n.clone(), tk, g, normed=True), want)
+    with pytest.raises(ValueError, match="norm"):
+        dec.norm(n[9:])
+
+
+def test_layer_copy_of_normed_rows():
+    """A copy of the normed rows gives the output and the gradients of the rows themselves."""
+    layer, topk, gates, _, _ = _layer(CFG, True)
+    plain, _, _, _, _ = _layer(CFG, True)
+    x = _rows(CFG.R * CFG.S, CFG.H, BF, 14).reshape(CFG.R, CFG.S, CFG.H)
+    dout = bf16_from_bits(W.grad_rows(CFG.R, CFG.S, CFG.H, 2, "bf16"))
+    tk, g = i32(topk), f32(gates)
+    with pytest.raises(ValueError, match="norm"):
+        layer.forward(x, tk, g, normed=True)
+    copy = layer.norm(x).clone()
+    assert torch.equal(layer.forward(copy, tk, g, normed=True), plain.forward(x, tk, g))
+    assert torch.equal(layer.backward(dout, g), plain.backward(dout, g))
+    for u, v in zip(layer.grads(), plain.grads()):
+        assert torch.equal(u, v)
+
+
 def test_captured_steps():
     """A decode step and a clipped gradient in one graph, replayed with new inputs and with eager work
     between the replays; two graphs share the scratch and run one after another."""

@@ -207,3 +207,63 @@ def test_grad_list_refuses_a_changed_tensor(monkeypatch, name):
         gl._arrays()
     g.data = keep if name != "resized" else torch.zeros(64)
     assert list(gl._arrays()[1]) == [h.data_ptr(), g.data_ptr()]
+
+
+@pytest.fixture
+def host_layer(monkeypatch):
+    """The layer module on host tensors: the norm doubles rows and counts them, the experts and the
+    dispatch copy them."""
+    torch = pytest.importorskip("torch")
+    from balanced_token_dispatch_moonep_amd import layer as L
+    normed = []
+
+    def norm(d, x, w, b, eps, y, mean=None, rstd=None):
+        normed.append(x.clone())
+        y.copy_(2 * x)
+
+    monkeypatch.setattr(L, "moonep_layer_norm", norm)
+    monkeypatch.setattr(L, "moonep_quantize_w4", lambda *a: None)
+    monkeypatch.setattr(L, "moonep_w4_ffn", lambda d, topk, gates, x, a, b, c, e, ws, out: out.copy_(x))
+    monkeypatch.setattr(L, "moonep_plan", lambda *a: None)
+    monkeypatch.setattr(L, "moonep_dispatch", lambda d, dest, x, s, recv: recv.copy_(x.reshape(recv.shape)))
+    monkeypatch.setattr(L, "moonep_combine", lambda d, dest, y, g, out: out.copy_(y.reshape(out.shape)))
+    return torch, L, normed
+
+
+def test_decoder_norms_rows_once(host_layer):
+    """What norm() returned, whole or in parts, is not normed again; neither is a copy that says so."""
+    torch, L, seen = host_layer
+    H, T = 32, 6
+    w = torch.zeros(2, H, 64, dtype=torch.bfloat16), torch.zeros(2, 32, H, dtype=torch.bfloat16)
+    dec = L.W4Experts(*w, K=1, max_tokens=8, norm_weight=torch.ones(H))
+    x = torch.arange(T * H).reshape(T, H).bfloat16()
+    topk, gates = torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1)
+    want = dec.forward(x, topk, gates).clone()
+    assert torch.equal(want, 2 * x) and len(seen) == 1
+    n = dec.norm(x)
+    for lo, hi in ((0, T), (0, 2), (2, T), (5, 6)):
+        assert torch.equal(dec.forward(n[lo:hi], topk[lo:hi], gates[lo:hi]), want[lo:hi])
+    assert len(seen) == 2
+    assert torch.equal(dec.forward(n.clone(), topk, gates, normed=True), want) and len(seen) == 2
+    assert torch.equal(dec.forward(n.clone(), topk, gates), 4 * x)       # rows that only happen to be normed
+    for rows in (n, n[2:]):                                              # over the rows that it reads
+        with pytest.raises(ValueError, match="norm"):
+            dec.norm(rows)
+
+
+def test_layer_norms_rows_once(host_layer):
+    torch, L, seen = host_layer
+    d = M.Dims.make(2, 2, 0, 3, 1, 16)
+    x = torch.arange(96).reshape(2, 3, 16).bfloat16()
+    layer = L.MoonEPLayer(d, device="cpu", training=True, norm_weight=torch.ones(16))
+    with pytest.raises(ValueError, match="norm"):            # its backward would have no rows to go to
+        layer.forward(x.clone(), None, None, normed=True)
+    want = layer.forward(x, None, None).clone()
+    assert torch.equal(want, 2 * x) and len(seen) == 1
+    n = layer.norm(x)
+    assert torch.equal(layer.forward(n, None, None), want)
+    assert torch.equal(layer.forward(n.clone(), None, None, normed=True), want)
+    assert len(seen) == 2 and layer.x is x
+    with pytest.raises(ValueError, match="norm"):
+        layer.norm(n)
+    assert torch.equal(layer.forward(x + 1, None, None), 2 * (x + 1)) and len(seen) == 3
