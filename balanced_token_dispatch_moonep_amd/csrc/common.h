@@ -149,6 +149,22 @@ inline int check_dims(const moonep_dims_t* d, bool need_ffn) {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Memory of a call; NULL overlaps nothing.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+// Whether one of the first `outs` spans overlaps any other of the n.
+inline bool outputs_overlap(const Span* s, int outs, int n) {
+    for (int i = 0; i < outs; ++i)
+        for (int j = i + 1; j < n; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p), b = reinterpret_cast<uintptr_t>(s[j].p);
+            if (a && b && a < b + s[j].bytes && b < a + s[i].bytes) return true;
+        }
+    return false;
+}
+
 #define MOONEP_CHECK_PTR(p)                         \
     do {                                            \
         if (!(p)) return MOONEP_EINVAL;             \

@@ -573,6 +573,12 @@ static void launch_norm_backward(const moonep_dims_t* d, hipStream_t s, const ui
     });
 }
 
+static size_t row_bytes(const moonep_dims_t* d) {
+    return (size_t)d->R * d->S * d->H * (d->flags & MOONEP_F32_ROWS ? 4 : 2);
+}
+static size_t stat_bytes(const moonep_dims_t* d) { return (size_t)d->R * d->S * sizeof(float); }
+static size_t param_bytes(const moonep_dims_t* d) { return (size_t)d->H * sizeof(float); }
+
 }  // namespace moonep
 
 using namespace moonep;
@@ -586,6 +592,10 @@ extern "C" int moonep_layer_norm(const moonep_dims_t* dims, const void* x, const
     MOONEP_CHECK_PTR(y);
     if (!aligned16(weight) || !aligned16(bias) || !aligned16(mean) || !aligned16(rstd)) return MOONEP_EALIGN;
     const bool f32 = (dims->flags & MOONEP_F32_ROWS) != 0;
+    // workgroups read their next row while they write one
+    const size_t rows = row_bytes(dims), stats = stat_bytes(dims), params = param_bytes(dims);
+    const Span all[] = {{y, rows}, {mean, stats}, {rstd, stats}, {x, rows}, {weight, params}, {bias, params}};
+    if (outputs_overlap(all, 3, 6)) return MOONEP_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const uint4* xv = static_cast<const uint4*>(x);
     uint4* yv = static_cast<uint4*>(y);
@@ -614,6 +624,11 @@ extern "C" int moonep_layer_norm_backward(const moonep_dims_t* dims, const void*
     const bool sums = dweight || dbias;
     if (sums) MOONEP_CHECK_PTR(ws);
     const bool f32 = (dims->flags & MOONEP_F32_ROWS) != 0;
+    const size_t rows = row_bytes(dims), stats = stat_bytes(dims), params = param_bytes(dims);
+    const Span all[] = {{dx, rows}, {dweight, params}, {dbias, params},
+                        {sums ? ws : nullptr, moonep_layer_norm_workspace_bytes(dims)},
+                        {dy, rows}, {x, rows}, {weight, params}, {mean, stats}, {rstd, stats}};
+    if (outputs_overlap(all, 4, 9)) return MOONEP_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const uint4 *dv = static_cast<const uint4*>(dy), *xv = static_cast<const uint4*>(x);
     uint4* ov = static_cast<uint4*>(dx);

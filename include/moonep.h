@@ -250,7 +250,8 @@ int moonep_reduce_grad(const moonep_dims_t* dims, const void* plan_ws,
  *   eps    finite, >= 0.  With 0 a constant row gives NaN, as the formula does.
  *   y      [R, S, H] out, same type as x
  *   mean, rstd [R*S] float32 out, for the backward; both NULL if it is not needed
- * A row that holds an infinity or a NaN gives NaN in its own row only.  y must not overlap x. */
+ * A row that holds an infinity or a NaN gives NaN in its own row only.  Outputs must not overlap inputs
+ * or each other (MOONEP_EINVAL). */
 int moonep_layer_norm(const moonep_dims_t* dims, const void* x, const float* weight, const float* bias,
                       float eps, void* y, float* mean, float* rstd, void* stream);
 
@@ -266,7 +267,7 @@ size_t moonep_layer_norm_workspace_bytes(const moonep_dims_t* dims);
  *   dweight, dbias [H] float32 out, or NULL where not needed.  Written, or with MOONEP_GRAD_ACCUM
  *             added to what they hold.
  *   ws     moonep_layer_norm_workspace_bytes() bytes; NULL if dweight and dbias are
- * Outputs must not overlap inputs or each other. */
+ * Outputs and ws must not overlap inputs or each other (MOONEP_EINVAL). */
 int moonep_layer_norm_backward(const moonep_dims_t* dims, const void* dy, const void* x, const float* weight,
                                const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
                                void* ws, void* stream);

@@ -94,6 +94,31 @@ def test_norm_without_parameters(H, weight, bias):
     _check_norm(4, H, BF, weight, bias, seed=3)
 
 
+def test_norm_buffers_side_by_side():
+    """Inputs and outputs cut out of one buffer with nothing between them."""
+    rows, H = 5, 64
+    n = rows * H
+    buf = torch.full((4 * n + 64,), 7.0, device=DEV)
+    x, y, dx, dy = (buf[i * n:(i + 1) * n].view(1, rows, H) for i in range(4))
+    xs, ds = _rows(rows, H, F32, 15), _rows(rows, H, F32, 16)
+    x.copy_(xs), dy.copy_(ds)
+    w, b = _params(H, 15)
+    mean, rstd, dw, db = (torch.empty(k, device=DEV) for k in (rows, rows, H, H))
+    d = _norm_dims(rows, H, F32)
+    ws = torch.empty(M.moonep_layer_norm_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+    M.moonep_layer_norm(d, x, w, b, EPS, y, mean, rstd)
+    M.moonep_layer_norm_backward(d, dy, x, w, mean, rstd, dx, dw, db, ws)
+    alone = [torch.empty(1, rows, H, device=DEV) for _ in range(2)]
+    M.moonep_layer_norm(d, xs[None], w, b, EPS, alone[0])
+    M.moonep_layer_norm_backward(d, ds[None], xs[None], w, mean, rstd, alone[1], None, None)
+    assert torch.equal(y, alone[0]) and torch.equal(dx, alone[1])
+    assert torch.equal(x[0], xs) and torch.equal(dy[0], ds) and bool((buf[4 * n:] == 7.0).all())
+    with pytest.raises(M.MoonEPError):
+        M.moonep_layer_norm(d, x, w, b, EPS, x)
+    with pytest.raises(M.MoonEPError):
+        M.moonep_layer_norm_backward(d, dy, x, w, mean, rstd, dy, None, None)
+
+
 def test_norm_far_from_zero():
     """A mean a thousand times the spread: the variance is that of the centred row."""
     for dtype in (F32, BF):

@@ -50,6 +50,38 @@ def test_norm_backward_refuses():
         assert call(**{n: MIS}) == EALIGN
 
 
+def test_norm_refuses_overlap():
+    """64 rows of 1024 bf16, 131072 bytes, each buffer far from the others but for those named."""
+    d = _dims(S=64, H=1024)
+    at = {n: VP((i + 1) << 20) for i, n in enumerate(("x", "w", "b", "y", "mean", "rstd"))}
+    end = 64 * 1024 * 2
+    for y in (1 << 20, (1 << 20) + end - 16, (1 << 20) - end + 16):       # all of x, its end, its beginning
+        assert _norm(d, **{**at, "y": VP(y)}) == EINVAL
+    assert _norm(d, **{**at, "y": VP((2 << 20) - end + 16)}) == EINVAL     # the weight
+    assert _norm(d, **{**at, "mean": VP((4 << 20) + end - 16)}) == EINVAL  # y's end
+    assert _norm(d, **{**at, "rstd": VP((5 << 20) + 240)}) == EINVAL       # the means' end
+
+
+def test_norm_backward_refuses_overlap():
+    d = _dims(S=64, H=1024)
+    names = ("dy", "x", "weight", "mean", "rstd", "dx", "dweight", "dbias", "ws")
+    at = {n: (i + 1) << 22 for i, n in enumerate(names)}
+    end = 64 * 1024 * 2
+
+    def call(**kw):
+        return M.lib.moonep_layer_norm_backward(ctypes.byref(d), *(VP({**at, **kw}[n]) for n in names), None)
+
+    for over in ("dy", "x"):
+        for off in (0, end - 16, 16 - end):
+            assert call(dx=at[over] + off) == EINVAL
+    assert call(dweight=at["weight"]) == EINVAL
+    assert call(dbias=at["dweight"] + 4096 - 16) == EINVAL
+    assert call(ws=at["x"] + end - 16) == EINVAL
+    assert call(ws=at["mean"] + 64) == EINVAL
+    assert call(ws=at["dx"] + end - 16) == EINVAL
+    assert call(dweight=at["ws"]) == EINVAL
+
+
 def test_norm_workspace():
     one, many = (M.moonep_layer_norm_workspace_bytes(_dims(S=s)) for s in (1, 1 << 15))
     assert 2 * 7168 * 4 <= one < many < 64 << 20
