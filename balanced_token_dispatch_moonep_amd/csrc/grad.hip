@@ -237,6 +237,17 @@ static bool overlap(int32_t n, const void* const* grads, const int64_t* numel, c
     return false;
 }
 
+// Whether a gradient and the `bytes` at p share memory.
+static bool touches(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dtype, const void* p,
+                    size_t bytes) {
+    for (int i = 0; i < n; ++i) {
+        if (numel[i] == 0) continue;
+        const Span both[] = {{p, bytes}, {grads[i], (size_t)numel[i] * (dtype[i] == MOONEP_GRAD_BF16 ? 2 : 4)}};
+        if (outputs_overlap(both, 1, 2)) return true;
+    }
+    return false;
+}
+
 }  // namespace moonep
 
 using namespace moonep;
@@ -252,6 +263,9 @@ extern "C" int moonep_grad_norm(int32_t n, const void* const* grads, const int64
     if (rc != MOONEP_OK) return rc;
     MOONEP_CHECK_PTR(ws);
     MOONEP_CHECK_PTR(norm);
+    if (touches(n, grads, numel, dtype, ws, moonep_grad_norm_workspace_bytes(n)) ||
+        touches(n, grads, numel, dtype, norm, sizeof(float)))
+        return MOONEP_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(stream);
     double* part = static_cast<double*>(ws);
     const bool stream_past = streams(n, numel, dtype);
@@ -273,6 +287,7 @@ extern "C" int moonep_grad_clip(int32_t n, void* const* grads, const int64_t* nu
     if (rc != MOONEP_OK) return rc;
     if (!(max_norm >= 0.0f)) return MOONEP_EINVAL;
     MOONEP_CHECK_PTR(norm);
+    if (touches(n, grads, numel, dtype, norm, sizeof(float))) return MOONEP_EINVAL;   // read by all, written by one
     try {
         if (overlap(n, grads, numel, dtype)) return MOONEP_EINVAL;
     } catch (...) {                  // no memory for the list of a host that has none left

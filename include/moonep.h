@@ -286,7 +286,7 @@ size_t moonep_grad_norm_workspace_bytes(int32_t n);
  *   grads  host array [n] of device pointers; numel host array [n], each >= 0 (a pointer may be
  *          NULL where it is 0); dtype host array [n] of MOONEP_GRAD_*.  The arrays are read before
  *          the call returns.  n may be 0.
- *   norm   [1] float32 out, on the device */
+ *   norm   [1] float32 out, on the device; neither it nor ws may overlap a gradient (MOONEP_EINVAL) */
 int moonep_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* dtype,
                      void* ws, float* norm, void* stream);
 
@@ -295,8 +295,8 @@ int moonep_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, 
  * nearest even; nothing is read or written where norm <= max_norm.  A NaN norm makes every gradient
  * NaN, an infinite one makes finite elements 0.
  *   max_norm  >= 0 (may be infinite)
- *   other arguments as for moonep_grad_norm.  MOONEP_EINVAL if two gradients overlap: a shared
- *   gradient would be scaled more than once. */
+ *   other arguments as for moonep_grad_norm.  MOONEP_EINVAL if two gradients overlap, as a shared
+ *   gradient would be scaled more than once, or if norm lies in one. */
 int moonep_grad_clip(int32_t n, void* const* grads, const int64_t* numel, const int32_t* dtype,
                      const float* norm, float max_norm, void* stream);
 

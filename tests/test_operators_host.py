@@ -126,6 +126,19 @@ def test_grad_clip_refuses():
     assert f(*_grads([0x30000, 0x20000, 0x10000], [4, 0x8001, 4], [1, 1, 0]), G, 1.0, None) == EINVAL
 
 
+def test_grads_apart_from_norm_and_scratch():
+    """100 float32 (400 bytes) and 100 bf16 (200 bytes); what a call writes or goes by lies elsewhere."""
+    norm, clip = M.lib.moonep_grad_norm, M.lib.moonep_grad_clip
+    g = _grads([0x100000, 0x200000], [100, 100], [0, 1])
+    far, ws = VP(0x300000), VP(0x400000)
+    for at in (0x100000, 0x100000 + 384, 0x200000, 0x200000 + 192):
+        assert norm(*g, ws, VP(at), None) == EINVAL
+        assert norm(*g, VP(at), far, None) == EINVAL
+        assert clip(*g, VP(at), 1.0, None) == EINVAL
+    size = M.lib.moonep_grad_norm_workspace_bytes(2)
+    assert norm(*g, VP(0x100000 - size + 16), far, None) == EINVAL
+
+
 def test_w4_sizes():
     assert M.moonep_w4_code_bytes(7168, 4096) == 7168 * 4096 // 2
     assert M.moonep_w4_scale_bytes(7168, 4096) == 7168 * 4096 // 32
