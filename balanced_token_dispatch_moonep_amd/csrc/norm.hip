@@ -573,6 +573,16 @@ static void launch_norm_backward(const moonep_dims_t* d, hipStream_t s, const ui
     });
 }
 
+// The dims that a norm has: the rows (2^30 at most), their length and type.
+static int check_rows(const moonep_dims_t* d) {
+    if (!d) return MOONEP_EINVAL;
+    if (d->R < 1 || d->R > kMaxR || d->S < 1 || d->H < 8 || d->H % 8 != 0) return MOONEP_EINVAL;
+    if ((int64_t)d->R * d->S > (int64_t)1 << 30) return MOONEP_EINVAL;
+    if (d->flags & ~(MOONEP_TRAINING | MOONEP_F32_ROWS | MOONEP_GRAD_ACCUM | MOONEP_PLAN_LOWMIG | kPhaseBits))
+        return MOONEP_EINVAL;
+    return MOONEP_OK;
+}
+
 static size_t row_bytes(const moonep_dims_t* d) {
     return (size_t)d->R * d->S * d->H * (d->flags & MOONEP_F32_ROWS ? 4 : 2);
 }
@@ -585,7 +595,7 @@ using namespace moonep;
 
 extern "C" int moonep_layer_norm(const moonep_dims_t* dims, const void* x, const float* weight, const float* bias,
                                  float eps, void* y, float* mean, float* rstd, void* stream) {
-    const int rc = check_dims(dims, false);
+    const int rc = check_rows(dims);
     if (rc != MOONEP_OK) return rc;
     if (!(eps >= 0.0f) || std::isinf(eps) || !mean != !rstd) return MOONEP_EINVAL;
     MOONEP_CHECK_PTR(x);
@@ -606,14 +616,14 @@ extern "C" int moonep_layer_norm(const moonep_dims_t* dims, const void* x, const
 }
 
 extern "C" size_t moonep_layer_norm_workspace_bytes(const moonep_dims_t* dims) {
-    if (check_dims(dims, false) != MOONEP_OK) return 0;
+    if (check_rows(dims) != MOONEP_OK) return 0;
     return (size_t)norm_splits(dims) * 2 * dims->H * sizeof(float);
 }
 
 extern "C" int moonep_layer_norm_backward(const moonep_dims_t* dims, const void* dy, const void* x,
                                           const float* weight, const float* mean, const float* rstd, void* dx,
                                           float* dweight, float* dbias, void* ws, void* stream) {
-    const int rc = check_dims(dims, false);
+    const int rc = check_rows(dims);
     if (rc != MOONEP_OK) return rc;
     MOONEP_CHECK_PTR(dy);
     MOONEP_CHECK_PTR(x);

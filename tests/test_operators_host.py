@@ -50,6 +50,23 @@ def test_norm_backward_refuses():
         assert call(**{n: MIS}) == EALIGN
 
 
+def test_norm_dims_that_count():
+    """Only R, S, H and the row type: the planner's limits on experts, K and B are not the norm's."""
+    want = M.moonep_layer_norm_workspace_bytes(_dims())
+    for other in (dict(E=256), dict(E=0), dict(E=5000), dict(K=0), dict(K=64), dict(B=100), dict(I=-1)):
+        assert M.moonep_layer_norm_workspace_bytes(_dims(**other)) == want
+        assert _norm(_dims(**other), x=None) == EINVAL and _norm(_dims(**other), x=MIS) == EALIGN
+    assert M.moonep_layer_norm_workspace_bytes(_dims(R=3)) == M.moonep_layer_norm_workspace_bytes(_dims(S=24))
+    # the most rows (of 8 bf16 each, 17 GB)
+    assert M.moonep_layer_norm_workspace_bytes(_dims(S=1 << 30, H=8)) > 0
+    for bad in (dict(R=0), dict(R=65), dict(S=0), dict(S=-5), dict(H=0), dict(H=-8), dict(H=12), dict(R=2, S=1 << 30)):
+        assert M.lib.moonep_layer_norm_workspace_bytes(ctypes.byref(_dims(**bad))) == 0
+        assert _norm(_dims(**bad), x=MIS) == EINVAL
+    bad = _dims()
+    bad.flags = 1024
+    assert _norm(bad, x=MIS) == EINVAL
+
+
 def test_norm_refuses_overlap():
     """64 rows of 1024 bf16, 131072 bytes, each buffer far from the others but for those named."""
     d = _dims(S=64, H=1024)
