@@ -394,16 +394,21 @@ def moonep_reduce_grad(d: Dims, plan_ws, dw13_home, dw2_home, dw13_red, dw2_red,
 # round the layer: norm, gradient clipping, decoding with 4-bit experts
 # ----------------------------------------------------------------------------
 
-def _bytes(n: int, where: str) -> int:
+def _bytes(n: int, where: str, code=lambda: -1) -> int:
+    """What a size function said; its 0 is raised as the code that the sizes' own call returns for them."""
     if n == 0:
-        raise MoonEPError(-1, where)
+        raise MoonEPError(code(), where)
     return int(n)
 
 
 @functools.lru_cache(maxsize=1024)
 def _dims_bytes(name: str, dims: bytes) -> int:
     """What the size function `name` says for these dims (a pure function of them)."""
-    return _bytes(getattr(_lib(), name)(ctypes.byref(Dims.from_buffer_copy(dims))), name)
+    d = ctypes.byref(Dims.from_buffer_copy(dims))
+    # sizes are looked at before the pointers, and a NULL one ends the call: nothing is enqueued
+    call = dict(moonep_w4_ffn_workspace_bytes=lambda: _lib().moonep_w4_ffn(d, *[None] * 10),
+                moonep_layer_norm_workspace_bytes=lambda: _lib().moonep_layer_norm(d, *[None] * 3, 0.0, *[None] * 4))
+    return _bytes(getattr(_lib(), name)(d), name, call[name])
 
 
 def moonep_layer_norm(d: Dims, x, weight, bias, eps, y, mean=None, rstd=None, stream=None) -> None:
@@ -511,14 +516,18 @@ def moonep_grad_clip(grads: GradList, norm, max_norm, stream=None) -> None:
     _check(_lib().moonep_grad_clip(*grads._arrays(), norm, float(max_norm), _stream(stream)), "moonep_grad_clip")
 
 
+def _matrix_code(Kin: int, N: int) -> int:
+    return _lib().moonep_quantize_w4(1, Kin, N, None, None, None, None)
+
+
 @functools.lru_cache(maxsize=1024)
 def moonep_w4_code_bytes(Kin: int, N: int) -> int:
-    return _bytes(_lib().moonep_w4_code_bytes(Kin, N), "moonep_w4_code_bytes")
+    return _bytes(_lib().moonep_w4_code_bytes(Kin, N), "moonep_w4_code_bytes", lambda: _matrix_code(Kin, N))
 
 
 @functools.lru_cache(maxsize=1024)
 def moonep_w4_scale_bytes(Kin: int, N: int) -> int:
-    return _bytes(_lib().moonep_w4_scale_bytes(Kin, N), "moonep_w4_scale_bytes")
+    return _bytes(_lib().moonep_w4_scale_bytes(Kin, N), "moonep_w4_scale_bytes", lambda: _matrix_code(Kin, N))
 
 
 def moonep_quantize_w4(w, codes, scales, stream=None) -> None:

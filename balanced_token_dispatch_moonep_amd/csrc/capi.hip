@@ -4,7 +4,7 @@
 extern "C" const char* moonep_strerror(int code) {
     switch (code) {
         case MOONEP_OK: return "ok";
-        case MOONEP_EINVAL: return "invalid argument (dims or NULL pointer)";
+        case MOONEP_EINVAL: return "invalid argument (dims, NULL pointer or overlapping buffers)";
         case MOONEP_EALIGN: return "pointer not 16-byte aligned";
         case MOONEP_EHIP: return "HIP launch failed";
         case MOONEP_ENOTSUP: return "unsupported combination of dims/flags";

@@ -82,7 +82,7 @@ typedef struct moonep_dims {
 
 enum {
     MOONEP_OK = 0,
-    MOONEP_EINVAL = -1,   /* bad dims or NULL pointer       */
+    MOONEP_EINVAL = -1,   /* bad dims, NULL pointer or buffers that overlap where they must not */
     MOONEP_EALIGN = -2,   /* pointer not 16-byte aligned    */
     MOONEP_EHIP = -3,     /* a HIP launch failed            */
     MOONEP_ENOTSUP = -4,  /* combination not supported      */

@@ -167,6 +167,24 @@ def test_w4_sizes():
             M.moonep_w4_code_bytes(kin, n)
 
 
+def test_refused_sizes_say_why():
+    """A size that the call would not support is ENOTSUP, one that is none is EINVAL."""
+    def code(f, *a):
+        with pytest.raises(M.MoonEPError) as e:
+            f(*a)
+        return e.value.code
+
+    for f in (M.moonep_w4_code_bytes, M.moonep_w4_scale_bytes):
+        assert code(f, 72, 64) == code(f, 64, 16) == ENOTSUP
+        assert code(f, 0, 64) == code(f, 64, -32) == EINVAL
+    for bad in (dict(H=7176), dict(I=2056), dict(f32_rows=True), dict(S=1025)):
+        assert code(M.moonep_w4_ffn_workspace_bytes, _dims(**bad)) == ENOTSUP
+    for bad in (dict(S=0), dict(K=0), dict(E=2000)):
+        assert code(M.moonep_w4_ffn_workspace_bytes, _dims(**bad)) == EINVAL
+    assert code(M.moonep_layer_norm_workspace_bytes, _dims(H=4)) == EINVAL
+    assert code(M.moonep_plan_workspace_bytes, _dims(E=0)) == EINVAL
+
+
 def test_quantize_refuses():
     f = M.lib.moonep_quantize_w4
     for e, kin, n in ((0, 64, 64), (1025, 64, 64), (1, 0, 64), (1, 64, -1)):
