@@ -38,6 +38,11 @@ def _within(x, buf) -> bool:
     return 0 <= x.data_ptr() - buf.data_ptr() < buf.nbytes
 
 
+def _aligned(t):
+    """t, or where its rows begin between 16-byte addresses (later tokens of a batch) a copy."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class MoonEPPool:
     """Process-global prefetch slots shared by every layer [AT, TL;DR; TD, memory contract].
 
@@ -290,5 +295,6 @@ class W4Experts:
         d = self._dims(T)
         ws = self.ws[:moonep_w4_ffn_workspace_bytes(d)]
         out = self.out[:T]
-        moonep_w4_ffn(d, topk.unsqueeze(0), gates.unsqueeze(0), x.unsqueeze(0), *self.packed, ws, out.unsqueeze(0))
+        moonep_w4_ffn(d, _aligned(topk).unsqueeze(0), _aligned(gates).unsqueeze(0), x.unsqueeze(0), *self.packed, ws,
+                      out.unsqueeze(0))
         return out
