@@ -7,6 +7,7 @@
 // float64 sums cost nothing beside the loads (loads of 4 bytes and one accumulator: 1556 us for both).
 #include "common.h"
 
+#include <cfloat>
 #include <cmath>
 #include <vector>
 
@@ -107,18 +108,25 @@ __device__ __forceinline__ void span_squares(const void* g, int n, double& s, do
     if (j < n) add_square(s, one<BF16>(g, j));
 }
 
+// A float32 times the factor, rounded to float32 once.  The factor is a float64, which costs nothing beside
+// the loads and stores: max_norm / norm may lie where float32 has few bits left or none, with a product
+// that does not.
+__device__ __forceinline__ float scaled(float g, double f) { return (float)((double)g * f); }
+
 template <bool BF16>
-__device__ __forceinline__ uint4 times(uint4 v, float f) {
+__device__ __forceinline__ uint4 times(uint4 v, double f) {
     if constexpr (BF16)
-        return make_uint4(pack_bf16(bf16_lo(v.x) * f, bf16_hi(v.x) * f), pack_bf16(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
-                          pack_bf16(bf16_lo(v.z) * f, bf16_hi(v.z) * f), pack_bf16(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
+        return make_uint4(pack_bf16(scaled(bf16_lo(v.x), f), scaled(bf16_hi(v.x), f)),
+                          pack_bf16(scaled(bf16_lo(v.y), f), scaled(bf16_hi(v.y), f)),
+                          pack_bf16(scaled(bf16_lo(v.z), f), scaled(bf16_hi(v.z), f)),
+                          pack_bf16(scaled(bf16_lo(v.w), f), scaled(bf16_hi(v.w), f)));
     else
-        return make_uint4(__float_as_uint(__uint_as_float(v.x) * f), __float_as_uint(__uint_as_float(v.y) * f),
-                          __float_as_uint(__uint_as_float(v.z) * f), __float_as_uint(__uint_as_float(v.w) * f));
+        return make_uint4(__float_as_uint(scaled(__uint_as_float(v.x), f)), __float_as_uint(scaled(__uint_as_float(v.y), f)),
+                          __float_as_uint(scaled(__uint_as_float(v.z), f)), __float_as_uint(scaled(__uint_as_float(v.w), f)));
 }
 
 template <bool BF16, bool STREAM>
-__device__ __forceinline__ void span_times(void* g, int n, float f) {
+__device__ __forceinline__ void span_times(void* g, int n, double f) {
     constexpr int N = BF16 ? 8 : 4;
     uint4* p = static_cast<uint4*>(g);
     const int nv = n / N;
@@ -133,7 +141,7 @@ __device__ __forceinline__ void span_times(void* g, int n, float f) {
     for (; v < nv; v += 256) p[v] = times<BF16>(p[v], f);
     const int j = nv * N + threadIdx.x;
     if (j < n) {
-        const float r = one<BF16>(g, j) * f;
+        const float r = scaled(one<BF16>(g, j), f);
         if constexpr (BF16) static_cast<uint16_t*>(g)[j] = (uint16_t)pack_bf16(r, 0.0f);
         else static_cast<float*>(g)[j] = r;
     }
@@ -169,7 +177,8 @@ template <bool STREAM>
 __global__ __launch_bounds__(256) void grad_clip_kernel(GradTable t, const float* __restrict__ norm, float most) {
     const float s = norm[0];
     if (s <= most) return;
-    const float f = most / s;        // NaN for a NaN norm, 0 for an infinite one
+    const float q = most / s;        // NaN for a NaN norm, 0 for an infinite one
+    const double f = q < FLT_MIN ? (double)most / (double)s : (double)q;
     const int spans = t.first[t.n];
     for (int c = blockIdx.x; c < spans; c += gridDim.x) {
         const int i = find_grad(t, c);

@@ -291,9 +291,10 @@ int moonep_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, 
                      void* ws, float* norm, void* stream);
 
 /* Clips n gradients in place by the norm on the device (of moonep_grad_norm, or one joined from
- * several devices): g *= max_norm / norm where norm > max_norm, product in float32, rounded to
- * nearest even; nothing is read or written where norm <= max_norm.  A NaN norm makes every gradient
- * NaN, an infinite one makes finite elements 0.
+ * several devices): g *= max_norm / norm where norm > max_norm, the quotient in float32 (in float64
+ * where it is below float32's smallest normal number), the product rounded to float32 and then to the
+ * gradient's type, to nearest even; nothing is read or written where norm <= max_norm.  A NaN norm
+ * makes every gradient NaN, an infinite one makes finite elements 0.
  *   max_norm  >= 0 (may be infinite)
  *   other arguments as for moonep_grad_norm.  MOONEP_EINVAL if two gradients overlap, as a shared
  *   gradient would be scaled more than once, or if norm lies in one. */

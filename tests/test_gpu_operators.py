@@ -328,6 +328,22 @@ def test_norm_range():
     assert abs(float(_norm_of(M.GradList([g]))) - 3 * float(g[0])) <= 2.0 ** -149
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("size,most", [(1e38, 1.0), (1e38, 1e-5), (1e30, 1e-12), (1e20, 1e-18), (1e38, 1e-38)])
+def test_clip_by_a_factor_that_float32_holds_badly(size, most, dtype):
+    """max_norm / norm below the smallest normal float32: its steps of 2^-149 are large beside it.  The
+    clipped values are off by a rounding each of norm, quotient and product, and by half a step of 2^-149
+    (bf16: 2^-133) where they are below the smallest normal themselves."""
+    g = f32([size, -size / 2, size / 3, 0.0, size / 1000]).to(dtype)
+    v = f64_of(g)
+    gl = M.GradList([g])
+    norm = _norm_of(gl)
+    M.moonep_grad_clip(gl, norm, most)
+    want = v * (float(np.float32(most)) / A.grad_norm([v]))
+    tol = np.abs(want) * (3.01 * U + (2.0 ** -8 if dtype == BF else 0.0)) + 2.0 ** (-134 if dtype == BF else -150) * 1.01
+    _far(f64_of(g), want, tol, "clipped")
+
+
 def test_clip_not_finite():
     g = f32([1.0, -2.0, np.inf, 0.0])
     gl = M.GradList([g])
