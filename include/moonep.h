@@ -244,7 +244,8 @@ int moonep_reduce_grad(const moonep_dims_t* dims, const void* plan_ws,
 /* Layer norm of the R*S rows of H elements: with m the mean and v the variance (divided by H) of a
  * row, y = (x - m) * rstd * weight + bias, rstd = 1 / sqrt(v + eps).  Only R, S, H and the row type
  * (MOONEP_F32_ROWS) of dims matter to it.  Statistics in float32, two passes (the variance is that
- * of the centred row); y is rounded to nearest even once.
+ * of the centred row, whose sum of squares must stay in float32's range); y is rounded to nearest even
+ * once.
  *   x      [R, S, H] bf16 (float32 with MOONEP_F32_ROWS)
  *   weight [H] float32 or NULL (ones), bias [H] float32 or NULL (zeros)
  *   eps    finite, >= 0.  With 0 a constant row gives NaN, as the formula does.
@@ -281,8 +282,9 @@ int moonep_layer_norm_backward(const moonep_dims_t* dims, const void* dy, const 
 size_t moonep_grad_norm_workspace_bytes(int32_t n);
 
 /* Global norm of n gradients: norm[0] = sqrt(sum over all elements of g^2), squares and sums in
- * float64 (no finite gradient overflows, none is lost to underflow), rounded once to float32; in an
- * order that n and numel alone fix.  An infinity or a NaN in a gradient is one in the norm.
+ * float64 (no square overflows, none is lost to underflow), rounded once to float32: infinite where the
+ * norm itself is more than float32 holds; in an order that n and numel alone fix.  An infinity or a
+ * NaN in a gradient is one in the norm.
  *   grads  host array [n] of device pointers; numel host array [n], each >= 0 (a pointer may be
  *          NULL where it is 0); dtype host array [n] of MOONEP_GRAD_*.  The arrays are read before
  *          the call returns.  n may be 0.
@@ -324,7 +326,9 @@ int moonep_quantize_w4(int32_t E, int32_t Kin, int32_t N, const void* w, void* c
  *   out[r,s] = sum over k (in k order) of gates[r,s,k] * ((silu(x G) * (x U)) D)  of expert topk[r,s,k],
  * G | U the columns of its w13, D its w2.  Products in matrix instructions on exact bf16 weights
  * (code times scale) with float32 accumulation; the activation is kept as two bf16 terms (16 bits or
- * more); the result is rounded to nearest even once.  Needs no plan: dims' R, S, K, E, H and I count,
+ * more); the result is rounded to nearest even once.  Calls of few pairs (R*S*K) and calls of more add
+ * in different orders: a token has the same bits whatever else its call holds as long as the call is of
+ * the same kind (dims decide), and may differ in its last bits between the two.  Needs no plan: dims' R, S, K, E, H and I count,
  * the planner's limits on E/R and B do not apply.
  *   topk  [R, S, K] int32: an id outside [0, E) adds nothing, whatever its gate (rows of ended
  *         sequences: all ids -1, their output is zero); an id named twice counts twice

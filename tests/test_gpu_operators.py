@@ -608,6 +608,98 @@ def test_ffn_rows_do_not_mix(T):
     assert torch.equal(out, clean)
 
 
+def test_ffn_batch_does_not_matter_within_a_way():
+    """A token has the same bits in every call of few pairs, and in every one of more."""
+    K, E, H, I = 2, 5, 1056, 96
+    topk, gates, x, w13, w2 = _ffn_case(90, K, E, H, I, 8)
+    p13, p2 = _packed(w13), _packed(w2)
+    for whole, parts in ((90, (33, 40, 61)), (32, (1, 5, 17, 31))):
+        want = _run_ffn(topk[:whole], gates[:whole], x[:whole], p13, p2, E, H, I)
+        for T in parts:
+            assert torch.equal(_run_ffn(topk[:T], gates[:T], x[:T], p13, p2, E, H, I), want[:T])
+
+
+# ----------------------------------------------------------------------------
+# wide experts, from their codes
+# ----------------------------------------------------------------------------
+
+def _random_packed(E, Kin, N, gen):
+    """Random codes [E, Kin, N], scale bytes [E, Kin/32, N] and the two in the header's layout."""
+    codes = torch.randint(0, 16, (E, Kin, N), dtype=torch.uint8, device=DEV, generator=gen)
+    scales = torch.randint(118, 122, (E, Kin // 32, N), dtype=torch.uint8, device=DEV, generator=gen)
+    kb, sb, nb = -(-Kin // 128), -(-Kin // 512), N // 16
+    c = torch.nn.functional.pad(codes, (0, 0, 0, kb * 128 - Kin)).view(E, kb, 4, 16, 2, nb, 16)
+    c = (c[:, :, :, :, 0] | c[:, :, :, :, 1] << 4).permute(0, 4, 1, 2, 5, 3)
+    s = torch.nn.functional.pad(scales, (0, 0, 0, sb * 16 - Kin // 32), value=127).view(E, sb, 4, 4, nb, 16)
+    s = s.permute(0, 4, 1, 3, 5, 2)
+    return codes, scales, (c.reshape(E, -1).contiguous(), s.reshape(E, -1).contiguous())
+
+
+def _values64(codes, scales):
+    """One matrix in float64 on the GPU."""
+    table = torch.tensor(np.concatenate([A.E2M1, -A.E2M1]), device=DEV)
+    v = table[codes.int()].view(scales.shape[0], 32, -1) * torch.exp2(scales.double() - 127).unsqueeze(1)
+    return v.view(codes.shape)
+
+
+def test_random_packed_is_the_headers_layout():
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(40)
+    for Kin, N in ((160, 32), (576, 64)):
+        codes, scales, (c, s) = _random_packed(2, Kin, N, gen)
+        for e in range(2):
+            wc, wsc = A.pack_w4(codes[e].cpu().numpy(), scales[e].cpu().numpy())
+            np.testing.assert_array_equal(c[e].cpu().numpy(), wc)
+            np.testing.assert_array_equal(s[e].cpu().numpy(), wsc)
+            got = A.w4_values(codes[e].cpu().numpy(), scales[e].cpu().numpy())
+            np.testing.assert_array_equal(_values64(codes[e], scales[e]).cpu().numpy(), got)
+
+
+# Few pairs of wide experts and both sides of what decides about them (H over 4096, at most 32 pairs, at most
+# two an expert, more than 49152 pairs times I), 8 to 100 rows an expert, and experts wider than their input.
+@pytest.mark.parametrize("T,K,E,H,I", [
+    (4, 8, 16, 4128, 2048), (5, 8, 16, 4128, 2048), (2, 13, 13, 4128, 2048), (3, 13, 13, 4128, 2048),
+    (16, 2, 4, 4128, 2048), (4, 8, 16, 4096, 2048), (1, 8, 8, 7168, 2048), (8, 8, 8, 7168, 2048),
+    (100, 4, 4, 7168, 2048), (1, 2, 2, 4096, 14336), (2, 2, 2, 4096, 14336), (4, 2, 4, 2880, 2880),
+    (1, 1, 2, 512, 32768),
+])
+def test_ffn_wide(T, K, E, H, I):
+    """Against float64.  A matrix instruction adds 32 products to the sum, in at most 33 steps that are off
+    by a step of float32 each (2 u: cut or rounded), and a sum has a 32nd of its length in instructions,
+    then at most 8 waves' parts: chains of n / 32 + 48.  The activation: |silu'| < 1.1, eight roundings,
+    and two bf16 terms of 16 bits together."""
+    say("ffn wide", T, K, E, H, I)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(T * 1000 + H + I)
+    c13, s13, p13 = _random_packed(E, H, 2 * I, gen)
+    c2, s2, p2 = _random_packed(E, I, H, gen)
+    rng = np.random.default_rng(T + I)
+    topk = np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
+    gates, x = rng.random((T, K)).astype(np.float32), _bits(rng.standard_normal((T, H)) * 0.25)
+    got = _run_ffn(topk, gates, x, p13, p2, E, H, I).double()
+    xs, gs, ids = bf16_from_bits(x).double(), f32(gates).double(), i32(topk)
+    out, off, mass = (torch.zeros(T, H, dtype=torch.float64, device=DEV) for _ in range(3))
+    n1, n2 = (H / 32 + 48) * 2 * U, (2 * I / 32 + 48) * 2 * U
+    for e in range(E):
+        t, k = (ids == e).nonzero(as_tuple=True)
+        if not len(t):
+            continue
+        w = _values64(c13[e], s13[e])
+        gu, dgu = xs[t] @ w, n1 * (xs[t].abs() @ w.abs())
+        g, v = gu[:, :I], gu[:, I:]
+        s = g * torch.sigmoid(g)
+        a = s * v
+        da = 1.1 * dgu[:, :I] * (v.abs() + dgu[:, I:]) + s.abs() * dgu[:, I:] + a.abs() * (8 * U + 2.0 ** -15)
+        w = _values64(c2[e], s2[e])
+        y, dy = a @ w, da @ w.abs() + n2 * ((a.abs() + da) @ w.abs())
+        share = gs[t, k, None]
+        out.index_add_(0, t, share * y)
+        off.index_add_(0, t, share * dy)
+        mass.index_add_(0, t, share * (y.abs() + dy))
+    tol = off + (K + 1) * U * mass + 2.0 ** -8 * out.abs() * (1 + 1e-2)
+    _far(got.cpu().numpy(), out.cpu().numpy(), tol.cpu().numpy(), "out")
+
+
 def test_ffn_deterministic_and_streams():
     T, K, E, H, I = 50, 4, 6, 256, 128
     topk, gates, x, w13, w2 = _ffn_case(T, K, E, H, I, 7)
@@ -868,6 +960,63 @@ def test_captured_steps():
             torch.cuda.synchronize()
             for a, b in zip(got, want[i]):
                 assert torch.equal(a, b)
+
+
+def test_launches_go_to_the_stream_given():
+    """Each call, given a stream that is being captured while another is current: all its launches are in
+    the graph, in order, and none ran before the replay."""
+    T, K, E, H, I = 6, 2, 3, 64, 64
+    topk, gates, x, w13, w2 = _ffn_case(40, K, E, H, I, 9)
+    rows = _rows(T, H, F32, 17)[None]
+    dy = _rows(T, H, F32, 18)[None]
+    w, b = _params(H, 17)
+    nd = _norm_dims(T, H, F32)
+    y, dx = torch.zeros_like(rows), torch.zeros_like(rows)
+    mean, rstd, dw, db = (torch.zeros(n, device=DEV) for n in (T, T, H, H))
+    nws = torch.zeros(M.moonep_layer_norm_workspace_bytes(nd), dtype=torch.uint8, device=DEV)
+    gl = M.GradList([dx, dw, db])
+    gws, norm = torch.zeros(M.moonep_grad_norm_workspace_bytes(gl), dtype=torch.uint8, device=DEV), torch.zeros(1, device=DEV)
+    packed = [torch.zeros((E, f(k, n)), dtype=torch.uint8, device=DEV) for k, n in ((H, 2 * I), (I, H))
+              for f in (M.moonep_w4_code_bytes, M.moonep_w4_scale_bytes)]
+    weights = bf16_from_bits(w13), bf16_from_bits(w2)
+    few = (M.Dims.make(1, E, 0, T, K, H, I), T)
+    many = (M.Dims.make(1, E, 0, 40, K, H, I), 40)
+    tk, g, xr = i32(topk), f32(gates), bf16_from_bits(x)
+    ffn = [(d, tk[None, :n], g[None, :n], xr[None, :n],
+            torch.zeros(M.moonep_w4_ffn_workspace_bytes(d), dtype=torch.uint8, device=DEV),
+            torch.zeros(1, n, H, dtype=BF, device=DEV)) for d, n in (few, many)]
+    outs = [y, mean, rstd, dx, dw, db, norm, *packed, ffn[0][5], ffn[1][5]]
+
+    def calls(stream):
+        M.moonep_layer_norm(nd, rows, w, b, EPS, y, mean, rstd, stream=stream)
+        M.moonep_layer_norm_backward(nd, dy, rows, w, mean, rstd, dx, dw, db, nws, stream=stream)
+        M.moonep_grad_norm(gl, gws, norm, stream=stream)
+        M.moonep_grad_clip(gl, norm, 1e-3, stream=stream)
+        M.moonep_quantize_w4(weights[0], *packed[:2], stream=stream)
+        M.moonep_quantize_w4(weights[1], *packed[2:], stream=stream)
+        for d, ids, gate, xs, ws, out in ffn:
+            M.moonep_w4_ffn(d, ids, gate, xs, *packed, ws, out, stream=stream)
+
+    calls(None)
+    torch.cuda.synchronize()
+    want = [v.clone() for v in outs]
+    assert all(bool(v.bool().any()) for v in want)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    for v in outs:
+        v.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            calls(side)
+    torch.cuda.synchronize()
+    assert not any(bool(v.bool().any()) for v in outs)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for v, ref in zip(outs, want):
+            assert torch.equal(v, ref)
+            v.zero_()
 
 
 def test_another_stream_waits_for_nothing():
