@@ -3,7 +3,7 @@
 // Both are streams over memory: the norm reads every gradient once, clipping reads and writes it
 // once (or leaves it alone where the norm is small enough).  The gradients' addresses travel in the
 // kernel arguments, kTable of them a launch, so a call needs no device table and can be captured.
-// On one MI355X, 1409 MB of float32 gradients: norm 208 us (6.8 TB/s), clipping 536 us (5.3 TB/s); the
+// On one MI355X, 1409 MB of float32 gradients: norm 208 us (6.8 TB/s), clipping 528 us (5.3 TB/s); the
 // float64 sums cost nothing beside the loads (loads of 4 bytes and one accumulator: 1556 us for both).
 #include "common.h"
 

@@ -537,9 +537,10 @@ static void launch_norm(const moonep_dims_t* d, hipStream_t s, const uint4* x, c
         return;
     }
     const int at_once = sh.lpr > 0 ? 256 / sh.lpr : 1;
-    // as many workgroups as are resident: 24 waves a CU (32768 x 7168: 163 us; 16 waves 194, 32 waves
-    // 206, one round of resident ones and part of another); rows within a wave 20 (200000 x 512: 74 us;
-    // 24 waves 83)
+    // as many workgroups as are resident: up to 24 waves a CU in whole workgroups (32768 x 7168 bf16, 7 waves a
+    // row: 161 us with 21 waves a CU; 16 asked for 194, 32 asked for 206, one round of resident ones and part
+    // of another), so one workgroup of 13 to 16 (32768 x 7168 float32: 348 us, 5.4 TB/s; 16384 x 16384 bf16:
+    // 224 us, 4.8 TB/s); rows within a wave 20 (200000 x 512: 74 us; 24 waves 83)
     const int most = kCUs * (sh.lpr > 0 ? 5 : std::max(1, 24 / sh.waves));
     const dim3 grid(std::min((rows + at_once - 1) / at_once, most));
     with_shape(sh, [&](auto lpr, auto per) {

@@ -15,15 +15,20 @@
 // What bounds it is reading the weights: 0.53 bytes each, against about 6 TB/s.  Measured over 32
 // experts of H 7168, I 2048, 8 a token (one pass among others, weights not in the caches):
 //     tokens   experts read   us     TB/s of weights
-//        1           8        35       5.3
-//        8          28       108       6.0
-//       64          32       143       5.2
-//      128          32       201       3.7, 450 TFLOP/s
+//        1           8        36       5.2
+//        8          28       110       6.0
+//       64          32       147       5.1
+//      128          32       206       3.6, 438 TFLOP/s
 // The loads skip the caches' keeping (ld_nt): with plain ones 16 tokens took 141 us instead of 125.
-// From about 16 rows an expert on, matrix instructions add to that: at 128 tokens, with two terms of
-// the activation and tiles of 16 rows in part empty, they do 1.6 times the 90 GFLOP of the
-// products themselves, at 0.74 PFLOP/s.  Operands read and widened a step ahead gave 202 us instead of 206,
-// the 32 x 32 x 16 instruction in place of the 16 x 16 x 32 one (as fast for each product) 224 to 270.
+// From about 16 rows an expert on, feeding the matrix instructions adds to that: at 128 tokens, with two
+// terms of the activation and tiles of 16 rows in part empty, they do 1.6 times the 90 GFLOP of the
+// products themselves.  They are busy for 28 and 31 % of the two products, and LDS as much; without the
+// weights' loads it took 193 us, without the operands' LDS reads as well 115 to 132: the waits for operands
+// are most of it, on two waves a SIMD.  The second product also reads its weights 1.46 times.  Operands read
+// and widened a step ahead gave 202 us instead of 206, the 32 x 32 x 16 instruction in place of the
+// 16 x 16 x 32 one (as fast for each product) 224 to 270.
+// From about 7000 pairs on the bf16 layer (moonep_grouped_ffn) takes less time: 8192 pairs 1170 us and 1020,
+// 6144 pairs 901 and 962.
 //
 // Rows go through LDS, and not from global memory to the operand: loads return in order, so a wait
 // for rows would be a wait for the weights that were asked for before them.  This and a loop in which
@@ -192,8 +197,10 @@ __device__ __forceinline__ void over_fours(const W4Mat& m, int first, int step, 
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// a as two bf16 terms, at least 16 bits together.  The leading one is cut, not rounded, so that it
-// cannot overflow; the rest is exact before its own rounding.
+// a as two bf16 terms, at least 16 bits together: the matrix instruction takes bf16, one term of 8 bits would
+// show in the output (1.4 times the error that its own rounding to bf16 has), two do not (1.6e-3, as with a
+// float32 activation), a third would be half as many matrix instructions more for nothing.  The leading one
+// is cut, not rounded, so that it cannot overflow; the rest is exact before its own rounding.
 __device__ __forceinline__ void two_terms(float a, uint16_t& lead, uint16_t& rest) {
     const uint32_t hi = __float_as_uint(a) & 0xffff0000u;
     const float lo = (hi & 0x7f800000u) == 0x7f800000u ? 0.0f : a - __uint_as_float(hi);
@@ -464,7 +471,8 @@ __global__ __launch_bounds__(1024) void w4_group_kernel(const int32_t* __restric
 
 // acc = RT row tiles times NT column tiles, a wave's own.  The workgroup's 256 threads bring the rows
 // of four blocks to LDS, 16 bytes of a row each at a time: rows(t) is the thread's row of tile t at its
-// piece.  Where a piece lies in LDS is swapped by row, so that neither side meets a bank twice.
+// piece.  Where a piece lies in LDS is swapped by row, so that 16 lanes side by side meet 16 different
+// groups of four banks; a quarter of LDS's active cycles are counted as conflicts all the same.
 template <int RT, int NT, class Rows>
 __device__ __forceinline__ void multiply_many(f32x4_t (&acc)[RT][NT], const W4Mat& m, const size_t* tile, uint4* lds,
                                               Rows rows) {

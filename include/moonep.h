@@ -328,15 +328,15 @@ int moonep_quantize_w4(int32_t E, int32_t Kin, int32_t N, const void* w, void* c
  * (code times scale) with float32 accumulation; the activation is kept as two bf16 terms (16 bits or
  * more); the result is rounded to nearest even once.  Calls of few pairs (R*S*K) and calls of more add
  * in different orders: a token has the same bits whatever else its call holds as long as the call is of
- * the same kind (dims decide), and may differ in its last bits between the two.  Needs no plan: dims' R, S, K, E, H and I count,
- * the planner's limits on E/R and B do not apply.
+ * the same kind (dims decide), and may differ in its last bits between the two.  Needs no plan: dims'
+ * R, S, K, E, H and I count, the planner's limits on E/R and B do not apply.
  *   topk  [R, S, K] int32: an id outside [0, E) adds nothing, whatever its gate (rows of ended
  *         sequences: all ids -1, their output is zero); an id named twice counts twice
  *   gates [R, S, K] float32;  x [R, S, H] bf16;  out [R, S, H] bf16 out
  *   w13_codes, w13_scales: E matrices [H, 2I];  w2_codes, w2_scales: E matrices [I, H]
  *   ws    moonep_w4_ffn_workspace_bytes() bytes, scratch (same rules as above)
  * MOONEP_ENOTSUP if H or I is not a multiple of 32, with MOONEP_F32_ROWS, or if R*S*K is more than
- * MOONEP_W4_MAX_PAIRS (such a batch is no longer bound by its weights: use moonep_grouped_ffn). */
+ * MOONEP_W4_MAX_PAIRS (with 256 pairs an expert moonep_grouped_ffn on bf16 weights is the faster one). */
 #define MOONEP_W4_MAX_PAIRS 8192
 size_t moonep_w4_ffn_workspace_bytes(const moonep_dims_t* dims);
 int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* gates, const void* x,
