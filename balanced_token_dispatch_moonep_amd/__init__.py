@@ -30,6 +30,8 @@ __all__ = [
     "GradList", "moonep_grad_norm_workspace_bytes", "moonep_grad_norm", "moonep_grad_clip",
     "W4_MAX_PAIRS", "moonep_w4_code_bytes", "moonep_w4_scale_bytes", "moonep_quantize_w4",
     "moonep_w4_ffn_workspace_bytes", "moonep_w4_ffn",
+    "ROUTE_SOFTMAX", "ROUTE_SOFTMAX_ALL", "ROUTE_SIGMOID", "moonep_route", "moonep_route_backward",
+    "moonep_sort_workspace_bytes", "moonep_sort", "moonep_combine_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoonep.so")
@@ -51,6 +53,9 @@ STAT_NAMES = (
 )
 NOALLOC_WS_BYTES = 8 << 20     # static plan workspace of moonep_plan_noalloc, per GPU
 W4_MAX_PAIRS = 8192            # (token, k) pairs of one moonep_w4_ffn call, at most
+# gates of moonep_route: over the picked logits, over all E, or sigmoids divided by their sum
+ROUTE_SOFTMAX, ROUTE_SOFTMAX_ALL, ROUTE_SIGMOID = 0, 1, 2
+_ROUTE_BF16 = 16
 EXPORTED = (
     "moonep_plan_workspace_bytes", "moonep_plan", "moonep_plan_noalloc", "moonep_prefetch", "moonep_dispatch",
     "moonep_combine", "moonep_dispatch_staged", "moonep_combine_staged", "moonep_grouped_ffn",
@@ -59,6 +64,7 @@ EXPORTED = (
     "moonep_grad_norm_workspace_bytes", "moonep_grad_norm", "moonep_grad_clip",
     "moonep_w4_code_bytes", "moonep_w4_scale_bytes", "moonep_quantize_w4",
     "moonep_w4_ffn_workspace_bytes", "moonep_w4_ffn",
+    "moonep_route", "moonep_route_backward", "moonep_sort_workspace_bytes", "moonep_sort", "moonep_combine_backward",
 )
 
 
@@ -129,6 +135,15 @@ def _load():
         getattr(L, n).restype = SZ
     for n in ("moonep_layer_norm", "moonep_layer_norm_backward", "moonep_grad_norm", "moonep_grad_clip",
               "moonep_quantize_w4", "moonep_w4_ffn"):
+        getattr(L, n).restype = I32
+    U32 = ctypes.c_uint32
+    L.moonep_route.argtypes = [P, U32, F32] + [VP] * 5
+    L.moonep_route_backward.argtypes = [P, U32, F32] + [VP] * 5
+    L.moonep_sort_workspace_bytes.argtypes = [P]
+    L.moonep_sort_workspace_bytes.restype = SZ
+    L.moonep_sort.argtypes = [P] + [VP] * 6
+    L.moonep_combine_backward.argtypes = [P] + [VP] * 7
+    for n in ("moonep_route", "moonep_route_backward", "moonep_sort", "moonep_combine_backward"):
         getattr(L, n).restype = I32
     L.moonep_strerror.argtypes = [I32]
     L.moonep_strerror.restype = ctypes.c_char_p
@@ -407,7 +422,8 @@ def _dims_bytes(name: str, dims: bytes) -> int:
     d = ctypes.byref(Dims.from_buffer_copy(dims))
     # sizes are looked at before the pointers, and a NULL one ends the call: nothing is enqueued
     call = dict(moonep_w4_ffn_workspace_bytes=lambda: _lib().moonep_w4_ffn(d, *[None] * 10),
-                moonep_layer_norm_workspace_bytes=lambda: _lib().moonep_layer_norm(d, *[None] * 3, 0.0, *[None] * 4))
+                moonep_layer_norm_workspace_bytes=lambda: _lib().moonep_layer_norm(d, *[None] * 3, 0.0, *[None] * 4),
+                moonep_sort_workspace_bytes=lambda: _lib().moonep_sort(d, *[None] * 6))
     return _bytes(getattr(_lib(), name)(d), name, call[name])
 
 
@@ -564,3 +580,82 @@ def moonep_w4_ffn(d: Dims, topk, gates, x, w13_codes, w13_scales, w2_codes, w2_s
         _ptr(out, "out", bf, (d.R, d.S, d.H)),
     )
     _check(_lib().moonep_w4_ffn(ctypes.byref(d), *args, _stream(stream)), "moonep_w4_ffn")
+
+
+# ----------------------------------------------------------------------------
+# routing, and experts without a plan
+# ----------------------------------------------------------------------------
+
+def _logits(d: Dims, logits, mode):
+    """The address of the logits [R, S, E], float32 or bf16, and the mode with their type."""
+    torch = _torch()
+    at = _ptr(logits, "logits", None, (d.R, d.S, d.E))
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if mode not in (ROUTE_SOFTMAX, ROUTE_SOFTMAX_ALL, ROUTE_SIGMOID):
+        raise ValueError(f"unknown mode {mode!r}")
+    return at, mode | (_ROUTE_BF16 if logits.dtype == torch.bfloat16 else 0)
+
+
+def moonep_route(d: Dims, logits, bias, topk, gates, mode=ROUTE_SOFTMAX, scale=1.0, stream=None) -> None:
+    """topk and gates [R, S, K] of the logits [R, S, E] (float32 or bf16), best first; bias [E] float32 or
+    None moves the choice only.  Where fewer than K logits are above -inf: id -1, gate 0."""
+    torch = _torch()
+    at, mode = _logits(d, logits, mode)
+    args = (
+        at,
+        _ptr(bias, "bias", torch.float32, (d.E,), optional=True),
+        _ptr(topk, "topk", torch.int32, (d.R, d.S, d.K)),
+        _ptr(gates, "gates", torch.float32, (d.R, d.S, d.K)),
+    )
+    _check(_lib().moonep_route(ctypes.byref(d), mode, float(scale), *args, _stream(stream)), "moonep_route")
+
+
+def moonep_route_backward(d: Dims, dgates, logits, topk, dlogits, mode=ROUTE_SOFTMAX, scale=1.0, stream=None) -> None:
+    """dlogits [R, S, E] (type of the logits) from dgates [R, S, K] float32, for the topk of the forward."""
+    torch = _torch()
+    at, mode = _logits(d, logits, mode)
+    args = (
+        _ptr(dgates, "dgates", torch.float32, (d.R, d.S, d.K)),
+        at,
+        _ptr(topk, "topk", torch.int32, (d.R, d.S, d.K)),
+        _ptr(dlogits, "dlogits", logits.dtype, (d.R, d.S, d.E)),
+    )
+    _check(_lib().moonep_route_backward(ctypes.byref(d), mode, float(scale), *args, _stream(stream)),
+           "moonep_route_backward")
+
+
+def moonep_sort_workspace_bytes(d: Dims) -> int:
+    return _dims_bytes("moonep_sort_workspace_bytes", bytes(d))
+
+
+def moonep_sort(d: Dims, topk, ws, offsets, dest, pair=None, stream=None) -> None:
+    """Rows grouped by expert without a plan: offsets [E + 1], dest [R, S, K] (-1 for an id outside [0, E)),
+    pair [R*S*K] (the pair of each row; None if not needed), all int32."""
+    torch = _torch()
+    i32 = torch.int32
+    args = (
+        _ptr(topk, "topk", i32, (d.R, d.S, d.K)),
+        _ptr(ws, "ws", torch.uint8, numel=moonep_sort_workspace_bytes(d)),
+        _ptr(offsets, "offsets", i32, (d.E + 1,)),
+        _ptr(dest, "dest", i32, (d.R, d.S, d.K)),
+        _ptr(pair, "pair", i32, (d.R * d.S * d.K,), optional=True),
+    )
+    _check(_lib().moonep_sort(ctypes.byref(d), *args, _stream(stream)), "moonep_sort")
+
+
+def moonep_combine_backward(d: Dims, dest, y, gates, dout, dy, dgates, stream=None) -> None:
+    """dy [R*S*K, H] = gates * dout at each pair's row, dgates [R, S, K] = <dout, y> of each pair; either may be
+    None, y too without dgates."""
+    torch = _torch()
+    rt, f32 = _rows_dtype(d), torch.float32
+    M = d.R * d.S * d.K
+    args = (
+        _ptr(dest, "dest", torch.int32, (d.R, d.S, d.K)),
+        _ptr(y, "y", rt, (M, d.H), optional=dgates is None),
+        _ptr(gates, "gates", f32, (d.R, d.S, d.K), optional=True),
+        _ptr(dout, "dout", rt, (d.R, d.S, d.H)),
+        _ptr(dy, "dy", rt, (M, d.H), optional=True),
+        _ptr(dgates, "dgates", f32, (d.R, d.S, d.K), optional=True),
+    )
+    _check(_lib().moonep_combine_backward(ctypes.byref(d), *args, _stream(stream)), "moonep_combine_backward")

@@ -147,6 +147,22 @@ inline int check_dims(const moonep_dims_t* d, bool need_ffn) {
     return MOONEP_OK;
 }
 
+// Flags that no call knows.
+inline int check_flags(const moonep_dims_t* d) {
+    constexpr uint32_t known =
+        MOONEP_TRAINING | MOONEP_F32_ROWS | MOONEP_GRAD_ACCUM | MOONEP_PLAN_LOWMIG | kPhaseBits;
+    return d->flags & ~known ? MOONEP_EINVAL : MOONEP_OK;
+}
+
+// What the movement of rows by dest needs of dims: R, S, K, H and the row type.
+inline int check_row_dims(const moonep_dims_t* d) {
+    if (!d || check_flags(d) != MOONEP_OK) return MOONEP_EINVAL;
+    if (d->R < 1 || d->R > kMaxR || d->S < 1 || d->K < 1 || d->K > kMaxK) return MOONEP_EINVAL;
+    if ((int64_t)d->R * d->S * d->K > (int64_t)1 << 30) return MOONEP_EINVAL;
+    if (d->H < 8 || d->H % 8 != 0) return MOONEP_EINVAL;
+    return MOONEP_OK;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Memory of a call; NULL overlaps nothing.

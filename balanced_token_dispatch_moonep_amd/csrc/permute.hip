@@ -15,6 +15,8 @@
 // (fully coalesced).  The token's source row is read once and written K times
 // (dispatch); the K rows of a token are gathered one after another, a chunk of the row
 // at a time, into float32 accumulators (combine).
+#include <type_traits>
+
 #include "common.h"
 
 namespace moonep {
@@ -118,6 +120,19 @@ __device__ __forceinline__ void acc_vec(float* a, uint4 v, float g) {
         a[5] += g * bf16_hi(v.z);
         a[6] += g * bf16_lo(v.w);
         a[7] += g * bf16_hi(v.w);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ float dot_vec(uint4 a, uint4 b) {
+    if constexpr (F32) {
+        return __uint_as_float(a.x) * __uint_as_float(b.x) + __uint_as_float(a.y) * __uint_as_float(b.y) +
+               (__uint_as_float(a.z) * __uint_as_float(b.z) + __uint_as_float(a.w) * __uint_as_float(b.w));
+    } else {
+        return bf16_lo(a.x) * bf16_lo(b.x) + bf16_hi(a.x) * bf16_hi(b.x) +
+               (bf16_lo(a.y) * bf16_lo(b.y) + bf16_hi(a.y) * bf16_hi(b.y)) +
+               (bf16_lo(a.z) * bf16_lo(b.z) + bf16_hi(a.z) * bf16_hi(b.z) +
+                (bf16_lo(a.w) * bf16_lo(b.w) + bf16_hi(a.w) * bf16_hi(b.w)));
     }
 }
 
@@ -229,13 +244,94 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const int32_t* __rest
     }
 }
 
+// The gradient of the weighted combine, one wave per token: dy[dest[p]] = g * dout[token(p)] as dispatch with a
+// row scale, and dgates[p] = <dout[token(p)], y[dest[p]]> in float32, so dout is read once for both.
+// NV > 0: a lane keeps its NV vectors of the token's dout in registers for all k; 0: rows are longer than
+// that, and dout is read again for each k (from the caches).  DY, DG: which of the two are wanted.
+// The K rows are taken one after another, as in combine_kernel; every lane adds its own products first,
+// then the wave joins them: the same order for all rows of a length.
+template <bool F32, bool GATES, bool DY, bool DG, int NV>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const int32_t* __restrict__ dest,
+                                                               const uint4* __restrict__ y,
+                                                               const float* __restrict__ gates,
+                                                               const uint4* __restrict__ dout, uint4* __restrict__ dy,
+                                                               float* __restrict__ dgates, int ntok, int K,
+                                                               int rowvec, long long nrows) {
+    const int tok = blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (tok >= ntok) return;
+    const int32_t* dp = dest + (size_t)tok * K;
+    const uint4* d = dout + (size_t)tok * rowvec;
+    constexpr int VB = NV > 0 ? NV : 8;
+    uint4 x[VB];
+    auto load = [&](int v0) {
+#pragma unroll
+        for (int u = 0; u < VB; ++u) {
+            const int v = v0 + u * 64 + lane;
+            x[u] = v < rowvec ? d[v] : make_uint4(0, 0, 0, 0);
+        }
+    };
+    if constexpr (NV > 0) load(0);
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+        const int row = dp[k];
+        const float g = GATES ? gates[(size_t)tok * K + k] : 1.0f;
+        float dot = 0.0f;
+        if ((unsigned long long)(long long)row < (unsigned long long)nrows) {
+            const uint4* yr = y + (size_t)row * rowvec;
+            uint4* o = dy + (size_t)row * rowvec;
+            for (int v0 = 0; v0 < (NV > 0 ? 1 : rowvec); v0 += 64 * VB) {
+                if constexpr (NV == 0) load(v0);
+                uint4 z[VB];
+                if constexpr (DG) {
+#pragma unroll
+                    for (int u = 0; u < VB; ++u) {
+                        const int v = v0 + u * 64 + lane;
+                        z[u] = v < rowvec ? ld_nt(yr + v) : make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if constexpr (DY) {
+#pragma unroll
+                    for (int u = 0; u < VB; ++u) {
+                        const int v = v0 + u * 64 + lane;
+                        if (v < rowvec) o[v] = scale_vec<F32, GATES>(x[u], g);
+                    }
+                }
+                if constexpr (DG) {
+#pragma unroll
+                    for (int u = 0; u < VB; ++u) dot += dot_vec<F32>(x[u], z[u]);
+                }
+            }
+        }
+        if constexpr (DG) {
+            dot = wave_sum(dot);
+            if (lane == 0) dgates[(size_t)tok * K + k] = dot;
+        }
+    }
+}
+
+template <bool F32, bool GATES, bool DY, bool DG>
+static void launch_combine_backward(int K, hipStream_t s, const int32_t* dest, const uint4* y, const float* gates,
+                                    const uint4* dout, uint4* dy, float* dgates, int ntok, int rowvec,
+                                    long long nrows) {
+    const dim3 grid((ntok + kWavesPerBlock - 1) / kWavesPerBlock);
+    const auto go = [&](auto nv) {
+        hipLaunchKernelGGL((combine_backward_kernel<F32, GATES, DY, DG, decltype(nv)::value>), grid, dim3(256), 0, s, dest,
+                           y, gates, dout, dy, dgates, ntok, K, rowvec, nrows);
+    };
+    if (rowvec <= 2 * 64) go(std::integral_constant<int, 2>{});
+    else if (rowvec <= 8 * 64) go(std::integral_constant<int, 8>{});
+    else if (rowvec <= 14 * 64) go(std::integral_constant<int, 14>{});
+    else go(std::integral_constant<int, 0>{});
+}
+
 }  // namespace moonep
 
 using namespace moonep;
 
 extern "C" int moonep_dispatch(const moonep_dims_t* dims, const int32_t* dest, const void* src,
                                const float* row_scale, void* recv, void* stream) {
-    const int rc = check_dims(dims, false);
+    const int rc = check_row_dims(dims);
     if (rc != MOONEP_OK) return rc;
     MOONEP_CHECK_PTR(dest);
     MOONEP_CHECK_PTR(src);
@@ -262,7 +358,7 @@ extern "C" int moonep_dispatch(const moonep_dims_t* dims, const int32_t* dest, c
 
 extern "C" int moonep_combine(const moonep_dims_t* dims, const int32_t* dest, const void* y,
                               const float* gates, void* out, void* stream) {
-    const int rc = check_dims(dims, false);
+    const int rc = check_row_dims(dims);
     if (rc != MOONEP_OK) return rc;
     MOONEP_CHECK_PTR(dest);
     MOONEP_CHECK_PTR(y);
@@ -350,6 +446,45 @@ extern "C" int moonep_combine_staged(const moonep_dims_t* dims, const int32_t* d
     } else {
         if (gates) launch_combine<false, true, true>(dims->K, grid, s, dest, tv, gates, ov, ntok, rowvec, nrows);
         else launch_combine<false, false, true>(dims->K, grid, s, dest, tv, gates, ov, ntok, rowvec, nrows);
+    }
+    MOONEP_LAUNCH_CHECK();
+    return MOONEP_OK;
+}
+
+extern "C" int moonep_combine_backward(const moonep_dims_t* dims, const int32_t* dest, const void* y,
+                                       const float* gates, const void* dout, void* dy, float* dgates, void* stream) {
+    const int rc = check_row_dims(dims);
+    if (rc != MOONEP_OK) return rc;
+    if (!dy && !dgates) return MOONEP_EINVAL;
+    MOONEP_CHECK_PTR(dest);
+    MOONEP_CHECK_PTR(dout);
+    if (dgates && !y) return MOONEP_EINVAL;
+    for (const void* p : {y, static_cast<const void*>(gates), static_cast<const void*>(dy), static_cast<const void*>(dgates)})
+        if (!aligned16(p)) return MOONEP_EALIGN;
+    const bool f32 = (dims->flags & MOONEP_F32_ROWS) != 0;
+    const int ntok = dims->R * dims->S, K = dims->K;
+    const size_t row = (size_t)dims->H * (f32 ? 4 : 2), pairs = (size_t)ntok * K;
+    const Span spans[] = {{dy, pairs * row}, {dgates, pairs * 4}, {dest, pairs * 4}, {dgates ? y : nullptr, pairs * row},
+                          {gates, pairs * 4}, {dout, ntok * row}};
+    if (outputs_overlap(spans, 2, 6)) return MOONEP_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const auto go = [&](auto type, auto scaled, auto rows, auto weights) {
+        launch_combine_backward<decltype(type)::value, decltype(scaled)::value, decltype(rows)::value,
+                                decltype(weights)::value>(K, s, dest, static_cast<const uint4*>(y), gates,
+                                                          static_cast<const uint4*>(dout), static_cast<uint4*>(dy), dgates,
+                                                          ntok, (int)(row / 16), (long long)pairs);
+    };
+    const auto outputs = [&](auto type, auto scaled) {
+        if (dy && dgates) go(type, scaled, std::true_type{}, std::true_type{});
+        else if (dy) go(type, scaled, std::true_type{}, std::false_type{});
+        else go(type, scaled, std::false_type{}, std::true_type{});
+    };
+    if (f32) {
+        if (gates) outputs(std::true_type{}, std::true_type{});
+        else outputs(std::true_type{}, std::false_type{});
+    } else {
+        if (gates) outputs(std::false_type{}, std::true_type{});
+        else outputs(std::false_type{}, std::false_type{});
     }
     MOONEP_LAUNCH_CHECK();
     return MOONEP_OK;

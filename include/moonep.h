@@ -343,6 +343,68 @@ int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* g
                   const void* w13_codes, const void* w13_scales, const void* w2_codes, const void* w2_scales,
                   void* ws, void* out, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Routing, and experts without a plan.  As above, the formulas are the definition.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Which gates moonep_route gives; or-ed with MOONEP_ROUTE_BF16 where the logits are bf16. */
+#define MOONEP_ROUTE_SOFTMAX 0     /* softmax over the picked logits                       */
+#define MOONEP_ROUTE_SOFTMAX_ALL 1 /* the picked entries of the softmax over the E logits  */
+#define MOONEP_ROUTE_SIGMOID 2     /* sigmoids of the picked logits, divided by their sum  */
+#define MOONEP_ROUTE_BF16 16
+
+/* The router's top K.  A token's K experts are those of the largest keys, in descending order, equal keys to
+ * the lower id.  The key is the logit; with a bias the logit plus the bias, or in SIGMOID the logit's sigmoid
+ * plus the bias, in float64 (the bias moves the choice only, no gate).  A logit or a bias of -inf is never
+ * picked; where fewer than K are left the id is -1 and the gate 0 (moonep_sort and the decoders take
+ * such ids, moonep_plan does not).  A NaN key ranks above all others, and a NaN or +inf among the logits
+ * that gates are made of makes the token's gates NaN.  Gates in float32, times scale (finite).
+ * Only R, S, K and E of dims matter (E to 1024, K to min(E, 16)).
+ *   logits [R, S, E] float32 or bf16;  bias [E] float32 or NULL
+ *   topk   [R, S, K] int32 out;  gates [R, S, K] float32 out
+ * Outputs must not overlap inputs or each other (MOONEP_EINVAL). */
+int moonep_route(const moonep_dims_t* dims, uint32_t mode, float scale, const void* logits, const float* bias,
+                 int32_t* topk, float* gates, void* stream);
+
+/* Backward of moonep_route for given topk (which has no gradient): dlogits from dgates.  With p_k = g_k / scale,
+ * D = sum over the picks of p_i dg_i:
+ *   SOFTMAX      dlogit = scale * p_k (dg_k - D) at pick k, 0 elsewhere
+ *   SOFTMAX_ALL  dlogit = scale * ([picked] p dg - p D), p the softmax over the E logits
+ *   SIGMOID      dlogit = scale * p_k (1 - sigmoid_k) (dg_k - D) at pick k, 0 elsewhere
+ * An id outside [0, E) is no pick, whatever its dgate; an id named twice gets both in k order.  A token without picks
+ * gets zeros.
+ *   dgates [R, S, K] float32;  logits, topk as for and from the forward
+ *   dlogits [R, S, E] out, type of the logits, each written (rounded once) */
+int moonep_route_backward(const moonep_dims_t* dims, uint32_t mode, float scale, const float* dgates,
+                          const void* logits, const int32_t* topk, void* dlogits, void* stream);
+
+/* Tokens sorted by expert, for experts that need no balance over ranks: where each (token, k) pair's row goes
+ * if the rows of expert 0 come first, then those of expert 1, and so on, pairs of one expert in the order of
+ * topk.  dest is what moonep_dispatch, moonep_combine and moonep_combine_backward take.  Only R, S, K and E of
+ * dims matter (E to 1024).
+ *   topk    [R, S, K] int32: a pair with an id outside [0, E) gets no row
+ *   ws      moonep_sort_workspace_bytes() bytes, scratch (calls that may overlap need one each)
+ *   offsets [E + 1] int32 out: expert e's rows are offsets[e] .. offsets[e + 1]
+ *   dest    [R, S, K] int32 out: the pair's row, or -1
+ *   pair    [R*S*K] int32 out or NULL: pair[dest[p]] = p; past offsets[E] left as it was
+ * Outputs and ws must not overlap topk or each other (MOONEP_EINVAL). */
+size_t moonep_sort_workspace_bytes(const moonep_dims_t* dims);
+int moonep_sort(const moonep_dims_t* dims, const int32_t* topk, void* ws, int32_t* offsets, int32_t* dest,
+                int32_t* pair, void* stream);
+
+/* Backward of moonep_combine, for rows and gates in one pass:
+ *   dy[dest[p]] = gates[p] * dout[token(p)]  (the same bits as moonep_dispatch with gates as row_scale)
+ *   dgates[p]   = sum over the row of dout[token(p)] * y[dest[p]]  (float32; 0 where dest is -1)
+ * Only R, S, K, H and the row type of dims matter.
+ *   y      [R*S*K, H] as for moonep_combine; NULL where dgates is
+ *   gates  [R, S, K] float32 or NULL (ones)
+ *   dout   [R, S, H] type of the rows
+ *   dy     [R*S*K, H] out, type of the rows, or NULL; rows that no dest names are left as they were
+ *   dgates [R, S, K] float32 out, or NULL; not both NULL
+ * Outputs must not overlap inputs or each other (MOONEP_EINVAL). */
+int moonep_combine_backward(const moonep_dims_t* dims, const int32_t* dest, const void* y, const float* gates,
+                            const void* dout, void* dy, float* dgates, void* stream);
+
 /* Static description of an error code. */
 const char* moonep_strerror(int code);
 
