@@ -32,6 +32,8 @@ __all__ = [
     "moonep_w4_ffn_workspace_bytes", "moonep_w4_ffn",
     "ROUTE_SOFTMAX", "ROUTE_SOFTMAX_ALL", "ROUTE_SIGMOID", "moonep_route", "moonep_route_backward",
     "moonep_sort_workspace_bytes", "moonep_sort", "moonep_combine_backward",
+    "FP8_MAX_PAIRS", "moonep_fp8_code_bytes", "moonep_fp8_scale_bytes", "moonep_quantize_fp8",
+    "moonep_fp8_ffn_workspace_bytes", "moonep_fp8_ffn",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoonep.so")
@@ -53,6 +55,7 @@ STAT_NAMES = (
 )
 NOALLOC_WS_BYTES = 8 << 20     # static plan workspace of moonep_plan_noalloc, per GPU
 W4_MAX_PAIRS = 8192            # (token, k) pairs of one moonep_w4_ffn call, at most
+FP8_MAX_PAIRS = 1 << 22        # (token, k) pairs of one moonep_fp8_ffn call, at most
 # gates of moonep_route: over the picked logits, over all E, or sigmoids divided by their sum
 ROUTE_SOFTMAX, ROUTE_SOFTMAX_ALL, ROUTE_SIGMOID = 0, 1, 2
 _ROUTE_BF16 = 16
@@ -65,6 +68,8 @@ EXPORTED = (
     "moonep_w4_code_bytes", "moonep_w4_scale_bytes", "moonep_quantize_w4",
     "moonep_w4_ffn_workspace_bytes", "moonep_w4_ffn",
     "moonep_route", "moonep_route_backward", "moonep_sort_workspace_bytes", "moonep_sort", "moonep_combine_backward",
+    "moonep_fp8_code_bytes", "moonep_fp8_scale_bytes", "moonep_quantize_fp8",
+    "moonep_fp8_ffn_workspace_bytes", "moonep_fp8_ffn",
 )
 
 
@@ -143,7 +148,14 @@ def _load():
     L.moonep_sort_workspace_bytes.restype = SZ
     L.moonep_sort.argtypes = [P] + [VP] * 6
     L.moonep_combine_backward.argtypes = [P] + [VP] * 7
-    for n in ("moonep_route", "moonep_route_backward", "moonep_sort", "moonep_combine_backward"):
+    L.moonep_fp8_code_bytes.argtypes = L.moonep_fp8_scale_bytes.argtypes = [N32, N32]
+    L.moonep_quantize_fp8.argtypes = [N32, N32, N32] + [VP] * 4
+    L.moonep_fp8_ffn_workspace_bytes.argtypes = [P]
+    L.moonep_fp8_ffn.argtypes = [P] + [VP] * 10
+    for n in ("moonep_fp8_code_bytes", "moonep_fp8_scale_bytes", "moonep_fp8_ffn_workspace_bytes"):
+        getattr(L, n).restype = SZ
+    for n in ("moonep_route", "moonep_route_backward", "moonep_sort", "moonep_combine_backward",
+              "moonep_quantize_fp8", "moonep_fp8_ffn"):
         getattr(L, n).restype = I32
     L.moonep_strerror.argtypes = [I32]
     L.moonep_strerror.restype = ctypes.c_char_p
@@ -423,6 +435,7 @@ def _dims_bytes(name: str, dims: bytes) -> int:
     # sizes are looked at before the pointers, and a NULL one ends the call: nothing is enqueued
     call = dict(moonep_w4_ffn_workspace_bytes=lambda: _lib().moonep_w4_ffn(d, *[None] * 10),
                 moonep_layer_norm_workspace_bytes=lambda: _lib().moonep_layer_norm(d, *[None] * 3, 0.0, *[None] * 4),
+                moonep_fp8_ffn_workspace_bytes=lambda: _lib().moonep_fp8_ffn(d, *[None] * 10),
                 moonep_sort_workspace_bytes=lambda: _lib().moonep_sort(d, *[None] * 6))
     return _bytes(getattr(_lib(), name)(d), name, call[name])
 
@@ -659,3 +672,54 @@ def moonep_combine_backward(d: Dims, dest, y, gates, dout, dy, dgates, stream=No
         _ptr(dgates, "dgates", f32, (d.R, d.S, d.K), optional=True),
     )
     _check(_lib().moonep_combine_backward(ctypes.byref(d), *args, _stream(stream)), "moonep_combine_backward")
+
+
+def _fp8_code(Kin: int, N: int) -> int:
+    return _lib().moonep_quantize_fp8(1, Kin, N, None, None, None, None)
+
+
+@functools.lru_cache(maxsize=1024)
+def moonep_fp8_code_bytes(Kin: int, N: int) -> int:
+    return _bytes(_lib().moonep_fp8_code_bytes(Kin, N), "moonep_fp8_code_bytes", lambda: _fp8_code(Kin, N))
+
+
+@functools.lru_cache(maxsize=1024)
+def moonep_fp8_scale_bytes(Kin: int, N: int) -> int:
+    return _bytes(_lib().moonep_fp8_scale_bytes(Kin, N), "moonep_fp8_scale_bytes", lambda: _fp8_code(Kin, N))
+
+
+def moonep_quantize_fp8(w, codes, scales, stream=None) -> None:
+    """Quantises w [E, Kin, N] bf16 to 8 bits: codes [E, moonep_fp8_code_bytes(Kin, N)] and scales
+    [E, moonep_fp8_scale_bytes(Kin, N)], both uint8."""
+    torch = _torch()
+    pw = _ptr(w, "w", torch.bfloat16)
+    if w.dim() != 3:
+        raise ValueError(f"w must have shape (E, Kin, N), got {tuple(w.shape)}")
+    E, Kin, N = w.shape
+    args = (pw, _ptr(codes, "codes", torch.uint8, (E, moonep_fp8_code_bytes(Kin, N))),
+            _ptr(scales, "scales", torch.uint8, (E, moonep_fp8_scale_bytes(Kin, N))))
+    _check(_lib().moonep_quantize_fp8(E, Kin, N, *args, _stream(stream)), "moonep_quantize_fp8")
+
+
+def moonep_fp8_ffn_workspace_bytes(d: Dims) -> int:
+    return _dims_bytes("moonep_fp8_ffn_workspace_bytes", bytes(d))
+
+
+def moonep_fp8_ffn(d: Dims, topk, gates, x, w13_codes, w13_scales, w2_codes, w2_scales, ws, out, stream=None) -> None:
+    """out [R, S, H] = the gated sum of each token's experts' FFN, weights and rows in 8 bits
+    (moonep_quantize_fp8 of w13 [E, H, 2I] and w2 [E, I, H]).  Ids outside [0, E) add nothing."""
+    torch = _torch()
+    u8, bf = torch.uint8, torch.bfloat16
+    wsb = moonep_fp8_ffn_workspace_bytes(d)
+    args = (
+        _ptr(topk, "topk", torch.int32, (d.R, d.S, d.K)),
+        _ptr(gates, "gates", torch.float32, (d.R, d.S, d.K)),
+        _ptr(x, "x", bf, (d.R, d.S, d.H)),
+        _ptr(w13_codes, "w13_codes", u8, (d.E, moonep_fp8_code_bytes(d.H, 2 * d.I))),
+        _ptr(w13_scales, "w13_scales", u8, (d.E, moonep_fp8_scale_bytes(d.H, 2 * d.I))),
+        _ptr(w2_codes, "w2_codes", u8, (d.E, moonep_fp8_code_bytes(d.I, d.H))),
+        _ptr(w2_scales, "w2_scales", u8, (d.E, moonep_fp8_scale_bytes(d.I, d.H))),
+        _ptr(ws, "ws", u8, numel=wsb),
+        _ptr(out, "out", bf, (d.R, d.S, d.H)),
+    )
+    _check(_lib().moonep_fp8_ffn(ctypes.byref(d), *args, _stream(stream)), "moonep_fp8_ffn")

@@ -1,0 +1,450 @@
+// The experts' FFN in 8-bit floating point.
+//
+//   out[t] = sum_k gate[t,k] * (q((silu(q(x_t) G_e) * (q(x_t) U_e))) D_e),  e = topk[t,k]
+//
+// G, U, D are e4m3 codes times a power of two for each block of 128 x 128; q() rounds a row the same way, a
+// power of two for each 128 values along it.  The matrix instruction v_mfma_scale_f32_32x32x64_f8f6f4 multiplies
+// such codes and applies both powers itself, so a product needs no arithmetic beside it; that is why the scales
+// are powers of two and not floats (which would cost a multiply-add for every accumulator and block).
+#include "sort.h"
+
+#include <type_traits>
+
+namespace moonep {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr int kBlk = 128;            // values a scale, along both directions of a weight
+constexpr int kCols = 32;            // columns of a tile of the layout
+constexpr int kTileBytes = kCols * kBlk;
+
+struct F8Dims {
+    int T, K, E, H, I;
+};
+
+// A matrix in the 8-bit layout.
+struct F8Mat {
+    const uint4* codes;              // [E][N/32][kb][8 pieces][32 columns]
+    const uint8_t* scales;           // [E][nb][kbp]
+    int kin, n, kb, kbp, nb;
+};
+
+// Rows in 8 bits: codes [rows][kb * 128], scale bytes [rows][sp].
+struct F8Rows {
+    uint8_t* codes;
+    uint8_t* scales;
+    int pitch, sp;
+};
+
+struct F8Ws {
+    int32_t *hist, *offsets, *dest, *pair, *nruns;
+    Run* runs;
+    int max_runs, run_rows;
+    F8Rows x, act;                   // [T], [P]
+    float* y;                        // [P][H]
+};
+
+__host__ __device__ static constexpr int blks(int n) { return (n + kBlk - 1) / kBlk; }
+
+constexpr int kThinRows = 32;
+
+static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
+    const size_t pairs = (size_t)d.T * d.K, experts = std::min<size_t>(pairs, d.E);
+    F8Ws w{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) -> uint8_t* {
+        uint8_t* p = base ? static_cast<uint8_t*>(base) + off : nullptr;
+        off = align_up(off + bytes, 256);
+        return p;
+    };
+    auto rows = [&](size_t n, int k) {
+        F8Rows r{};
+        r.pitch = blks(k) * kBlk;
+        r.sp = (blks(k) + 31) / 32 * 32;
+        r.codes = take(n * r.pitch);
+        r.scales = take(n * r.sp);
+        return r;
+    };
+    w.run_rows = kThinRows;
+    w.max_runs = (int)(experts + pairs / w.run_rows);
+    w.hist = (int32_t*)take(sort_hist_bytes(sort_args((int)pairs, d.E)));
+    w.offsets = (int32_t*)take((size_t)(d.E + 1) * 4);
+    w.dest = (int32_t*)take(pairs * 4);
+    w.pair = (int32_t*)take(pairs * 4);
+    w.nruns = (int32_t*)take(4);
+    w.runs = (Run*)take(w.max_runs * sizeof(Run));
+    w.x = rows(d.T, d.H);
+    w.act = rows(pairs, d.I);
+    w.y = (float*)take(pairs * d.H * 4);
+    if (ws) *ws = w;
+    return off;
+}
+
+// ---------------------------------------------------------------------------
+// rounding
+// ---------------------------------------------------------------------------
+
+// The scale byte of a block whose largest magnitude has the bits `top`: the smallest power of two that 448
+// of hold it, at least 2^-126.  A block that is not finite: 127, and codes that are NaN.
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+    const int e = (int)(top >> 23);
+    if (e == 255) return 127;
+    return max(e - 8 + ((top & 0x7fffffu) > 0x600000u), 1);
+}
+// What values of that block are multiplied by: exact.
+__device__ __forceinline__ float to_codes(uint32_t top) {
+    return (top >> 23) == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(254 - scale_byte(top)) << 23);
+}
+// Four values as codes, to nearest even.
+__device__ __forceinline__ uint32_t four_codes(float a, float b, float c, float d, float m) {
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * m, b * m, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * m, d * m, r, true);
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t max_turned(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xf, 0xf, true));
+}
+// Largest of 16 lanes, in each of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    v = max_turned<8>(v);
+    v = max_turned<4>(v);
+    v = max_turned<2>(v);
+    return max_turned<1>(v);
+}
+
+// Eight values of a row by each of 16 lanes that hold one block: rounds them and writes codes and scale.
+__device__ __forceinline__ void put_block(const float (&v)[8], const F8Rows& r, size_t row, int block, int lane16) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = max16(top);
+    const float m = to_codes(top);
+    *reinterpret_cast<uint2*>(r.codes + row * r.pitch + block * kBlk + lane16 * 8) =
+        make_uint2(four_codes(v[0], v[1], v[2], v[3], m), four_codes(v[4], v[5], v[6], v[7], m));
+    if (lane16 == 0) r.scales[row * r.sp + block] = (uint8_t)scale_byte(top);
+}
+
+__global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ x, F8Rows r, int H, int kb) {
+    const int at = blockIdx.y * 16 + threadIdx.x / 16, lane16 = threadIdx.x % 16, k = at * kBlk + lane16 * 8;
+    const size_t row = blockIdx.x;
+    if (at >= kb) return;
+    const uint4 u = k < H ? *reinterpret_cast<const uint4*>(x + row * H + k) : make_uint4(0, 0, 0, 0);
+    const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
+                        bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+    put_block(v, r, row, at, lane16);
+}
+
+// A workgroup a block of 128 x 128.  A thread reads eight columns of eight rows; the codes are turned in
+// LDS so that 16 along the input direction lie together.
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t* __restrict__ w, uint4* __restrict__ codes,
+                                                           uint8_t* __restrict__ scales, int kin, int N, int kb,
+                                                           int kbp) {
+    __shared__ __attribute__((aligned(16))) uint8_t turn[kBlk][kBlk + 16];   // [column][k]
+    __shared__ uint32_t tops[4];
+    const int tid = threadIdx.x, b = blockIdx.x, nblk = blockIdx.y;
+    const size_t e = blockIdx.z;
+    const int c8 = tid % 16 * 8, n = nblk * kBlk + c8, k0 = b * kBlk + tid / 16 * 8;
+    uint8_t* scale = scales + (e * gridDim.y + nblk) * kbp;
+    if (b >= kb) {                   // scales past the matrix
+        if (tid == 0 && b < kbp) scale[b] = 127;
+        return;
+    }
+    uint4 v[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = k0 + i < kin && n < N ? *reinterpret_cast<const uint4*>(w + (e * kin + k0 + i) * N + n)
+                                     : make_uint4(0, 0, 0, 0);
+        for (uint32_t u : {v[i].x, v[i].y, v[i].z, v[i].w}) top = max(top, max(u << 16 & 0x7fff0000u, u & 0x7fff0000u));
+    }
+    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+    if (tid % 64 == 0) tops[tid / 64] = top;
+    __syncthreads();
+    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    const float m = to_codes(top);
+    auto value = [&](int i, int j) {
+        const uint32_t u = j / 2 == 0 ? v[i].x : j / 2 == 1 ? v[i].y : j / 2 == 2 ? v[i].z : v[i].w;
+        return j % 2 ? bf16_hi(u) : bf16_lo(u);
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint2*>(&turn[c8 + j][tid / 16 * 8]) =
+            make_uint2(four_codes(value(0, j), value(1, j), value(2, j), value(3, j), m),
+                       four_codes(value(4, j), value(5, j), value(6, j), value(7, j), m));
+    if (tid == 0) scale[b] = (uint8_t)scale_byte(top);
+    __syncthreads();
+    // 4 tiles of 32 columns, 8 pieces, 32 columns
+    for (int i = tid; i < 4 * 256; i += 256) {
+        const int tile = i / 256, piece = i / 32 % 8, c = i % 32;
+        if (nblk * kBlk + tile * kCols >= N) continue;
+        codes[((e * (N / kCols) + nblk * 4 + tile) * kb + b) * 256 + piece * 32 + c] =
+            *reinterpret_cast<const uint4*>(&turn[tile * kCols + c][piece * 16]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// products of few rows
+// ---------------------------------------------------------------------------
+
+// Eight codes times their scale as bf16: exact (down to 2^-133).
+__device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi, float scale) {
+    union {
+        bf16x2_t two[4];
+        bf16x8_t all;
+    } r;
+    r.two[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    r.two[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    r.two[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    r.two[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return r.all;
+}
+// The row of a 32 x 32 result that a lane's register r holds; the column is lane % 32.
+__device__ __forceinline__ int result_row(int r, int lane) { return r / 4 * 8 + (lane >> 5) * 4 + r % 4; }
+
+// acc = 32 rows times NT column tiles, over blocks first, first + step, ... of the input direction.
+// A lane holds row lane % 32 and, of each 32 input values, the 16 of its half of the wave; so does it of
+// the columns, whose layout makes a wave's load one KiB in a row.  D blocks are on their way while one is
+// multiplied; past the last one they are asked for again instead of branching around the load.
+// The codes are widened to bf16: the 8-bit matrix instructions keep a sum of products to about 16 bits only
+// (measured: relative error 1.3e-5, with 32x32x64, 16x16x128 and 32x32x16 alike), which moves values of act over
+// the border between two codes; with bf16 operands it is exact to float32.  Half the rate costs nothing where
+// reading the weights is what takes the time.
+template <int NT, int D>
+__device__ __forceinline__ void multiply_thin(f32x16_t (&acc)[NT], const F8Mat& m, const size_t* tile,
+                                              const uint8_t* const* scale, const uint8_t* row, const uint8_t* row_scale,
+                                              int first, int step) {
+    const int lane = threadIdx.x & 63;
+    const int n = first < m.kb ? (m.kb - first + step - 1) / step : 0;
+    uint4 a[D][4], b[D][NT][4];
+    int sa[D], sb[D][NT];
+    const uint4* base[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        base[t] = m.codes + tile[t] * m.kb * 256;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[t][i] = 0.0f;
+    }
+    if (n == 0) return;
+    const uint8_t* half = row + (lane >> 5) * 16;
+    auto load = [&](int j, int s) {
+        const int k = first + min(s, n - 1) * step;
+        sa[j] = row_scale[k];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) a[j][p] = *reinterpret_cast<const uint4*>(half + (size_t)k * kBlk + p * 32);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            sb[j][t] = scale[t][k];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) b[j][t][p] = ld_nt(base[t] + (size_t)k * 256 + p * 64 + lane);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < D; ++j) load(j, j);
+    for (int s = 0; s < n; s += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            if (s + j < n) {
+                const float fa = __uint_as_float((uint32_t)sa[j] << 23);
+                float fb[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) fb[t] = __uint_as_float((uint32_t)sb[j][t] << 23);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const bf16x8_t a0 = widen(a[j][p].x, a[j][p].y, fa), a1 = widen(a[j][p].z, a[j][p].w, fa);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint4 c = b[j][t][p];
+                        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, widen(c.x, c.y, fb[t]), acc[t], 0, 0, 0);
+                        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, widen(c.z, c.w, fb[t]), acc[t], 0, 0, 0);
+                    }
+                }
+            }
+            load(j, s + j + D);
+        }
+    }
+}
+
+__device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// act = q(silu(x G) * (x U)) of a run's rows and 128 columns: a block of act, which the workgroup rounds
+// itself.  Four pairs of tiles, their input direction dealt out to SPLIT waves each.
+template <int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT) void fp8_thin_up_kernel(F8Mat m, F8Ws w, F8Dims d) {
+    __shared__ float part[4 * SPLIT][2][16][64];
+    const int groups = blks(d.I), r = blockIdx.x / groups, block = blockIdx.x % groups;
+    if (r >= w.nruns[0]) return;
+    const Run run = w.runs[r];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = block * 4 + wave / SPLIT, last = d.I / kCols - 1, gate = min(col, last);
+    const size_t tiles = (size_t)run.expert * (m.n / kCols), tile[2] = {tiles + gate, tiles + d.I / kCols + gate};
+    const uint8_t* scales = m.scales + (size_t)run.expert * m.nb * m.kbp;
+    const uint8_t* scale[2] = {scales + (size_t)(gate / 4) * m.kbp, scales + (size_t)((d.I / kCols + gate) / 4) * m.kbp};
+    const size_t token = w.pair[run.first + min(lane & 31, run.n - 1)] / d.K;
+    f32x16_t acc[2];
+    multiply_thin<2, 3>(acc, m, tile, scale, w.x.codes + token * w.x.pitch, w.x.scales + token * w.x.sp, wave % SPLIT,
+                        SPLIT);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) part[wave][t][r][lane] = acc[t][r];
+    __syncthreads();
+    // 16 lanes a row, eight columns each
+    for (int i = tid / 16; i < run.n; i += 16 * SPLIT) {
+        const int c8 = tid % 16 * 8, t = c8 / kCols, r = i / 8 * 4 + i % 4, l = i / 4 % 2 * 32 + c8 % kCols;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float g = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int s = 0; s < SPLIT; ++s) {
+                g += part[t * SPLIT + s][0][r][l + j];
+                u += part[t * SPLIT + s][1][r][l + j];
+            }
+            v[j] = block * kBlk + c8 < d.I ? silu_times(g, u) : 0.0f;
+        }
+        put_block(v, w.act, run.first + i, block, tid % 16);
+    }
+}
+
+// y of a run's rows; a wave takes 32 columns.
+__global__ __launch_bounds__(256) void fp8_thin_down_kernel(F8Mat m, F8Ws w, F8Dims d) {
+    const int groups = blks(d.H), r = blockIdx.x / groups;
+    if (r >= w.nruns[0]) return;
+    const Run run = w.runs[r];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = blockIdx.x % groups * 4 + wave;
+    if (col >= d.H / kCols) return;
+    const size_t tile[1] = {(size_t)run.expert * (m.n / kCols) + col};
+    const uint8_t* scale[1] = {m.scales + ((size_t)run.expert * m.nb + col / 4) * m.kbp};
+    const size_t row = run.first + min(lane & 31, run.n - 1);
+    f32x16_t acc[1];
+    multiply_thin<1, 4>(acc, m, tile, scale, w.act.codes + row * w.act.pitch, w.act.scales + row * w.act.sp, 0, 1);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int i = result_row(r, lane);
+        if (i < run.n) w.y[(size_t)(run.first + i) * d.H + col * kCols + (lane & 31)] = acc[0][r];
+    }
+}
+
+// out = sum over k of gate * y, in k order, skipping ids that name no expert.
+__global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ gates, F8Ws w, uint2* __restrict__ out,
+                                                       F8Dims d) {
+    const int h = blockIdx.y * 256 + threadIdx.x, t = blockIdx.x;
+    if (h >= d.H / 4) return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p = t * d.K; p < (t + 1) * d.K; ++p) {
+        const int row = w.dest[p];
+        if (row < 0) continue;
+        const float4 v = reinterpret_cast<const float4*>(w.y)[(size_t)row * (d.H / 4) + h];
+        const float g = gates[p];
+        s.x += g * v.x;
+        s.y += g * v.y;
+        s.z += g * v.z;
+        s.w += g * v.w;
+    }
+    out[(size_t)t * (d.H / 4) + h] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+static bool f8_size(int32_t kin, int32_t n) {
+    return kin >= kCols && kin % kCols == 0 && n >= kCols && n % kCols == 0 && kin <= 1 << 20 && n <= 1 << 21;
+}
+static size_t f8_code_bytes(int kin, int n) { return (size_t)(n / kCols) * blks(kin) * kTileBytes; }
+static int f8_scale_pitch(int kin) { return (blks(kin) + 3) / 4 * 4; }
+
+static F8Mat f8_mat(const void* codes, const void* scales, int kin, int n) {
+    return F8Mat{static_cast<const uint4*>(codes), static_cast<const uint8_t*>(scales), kin, n, blks(kin),
+                 f8_scale_pitch(kin), blks(n)};
+}
+
+static int check_f8(const moonep_dims_t* d) {
+    if (!d || check_flags(d) != MOONEP_OK) return MOONEP_EINVAL;
+    if (d->R < 1 || d->R > kMaxR || d->S < 1 || d->E < 1 || d->E > kMaxE) return MOONEP_EINVAL;
+    if (d->K < 1 || d->K > kMaxK || d->K > d->E || d->H < 8 || d->I < 8) return MOONEP_EINVAL;
+    if (d->flags & MOONEP_F32_ROWS) return MOONEP_ENOTSUP;
+    if (!f8_size(d->H, d->I) || !f8_size(d->I, d->H)) return MOONEP_ENOTSUP;
+    if ((int64_t)d->R * d->S * d->K > MOONEP_FP8_MAX_PAIRS) return MOONEP_ENOTSUP;
+    return MOONEP_OK;
+}
+
+}  // namespace moonep
+
+using namespace moonep;
+
+extern "C" size_t moonep_fp8_code_bytes(int32_t Kin, int32_t N) { return f8_size(Kin, N) ? f8_code_bytes(Kin, N) : 0; }
+
+extern "C" size_t moonep_fp8_scale_bytes(int32_t Kin, int32_t N) {
+    return f8_size(Kin, N) ? (size_t)blks(N) * f8_scale_pitch(Kin) : 0;
+}
+
+extern "C" int moonep_quantize_fp8(int32_t E, int32_t Kin, int32_t N, const void* w, void* codes, void* scales,
+                                   void* stream) {
+    if (E < 1 || E > kMaxE || Kin < 1 || N < 1) return MOONEP_EINVAL;
+    if (!f8_size(Kin, N)) return MOONEP_ENOTSUP;
+    MOONEP_CHECK_PTR(w);
+    MOONEP_CHECK_PTR(codes);
+    MOONEP_CHECK_PTR(scales);
+    const Span spans[] = {{codes, E * moonep_fp8_code_bytes(Kin, N)}, {scales, E * moonep_fp8_scale_bytes(Kin, N)},
+                          {w, (size_t)E * Kin * N * 2}};
+    if (outputs_overlap(spans, 2, 3)) return MOONEP_EINVAL;
+    const dim3 grid(f8_scale_pitch(Kin), blks(N), E);
+    hipLaunchKernelGGL(fp8_quantize_kernel, grid, dim3(256), 0, static_cast<hipStream_t>(stream),
+                       static_cast<const uint16_t*>(w), static_cast<uint4*>(codes), static_cast<uint8_t*>(scales), Kin, N,
+                       blks(Kin), f8_scale_pitch(Kin));
+    MOONEP_LAUNCH_CHECK();
+    return MOONEP_OK;
+}
+
+extern "C" size_t moonep_fp8_ffn_workspace_bytes(const moonep_dims_t* dims) {
+    if (check_f8(dims) != MOONEP_OK) return 0;
+    return f8_ws_layout(F8Dims{dims->R * dims->S, dims->K, dims->E, dims->H, dims->I}, nullptr, nullptr);
+}
+
+extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* gates, const void* x,
+                              const void* w13_codes, const void* w13_scales, const void* w2_codes,
+                              const void* w2_scales, void* ws, void* out, void* stream) {
+    const int rc = check_f8(dims);
+    if (rc != MOONEP_OK) return rc;
+    MOONEP_CHECK_PTR(topk);
+    MOONEP_CHECK_PTR(gates);
+    MOONEP_CHECK_PTR(x);
+    MOONEP_CHECK_PTR(w13_codes);
+    MOONEP_CHECK_PTR(w13_scales);
+    MOONEP_CHECK_PTR(w2_codes);
+    MOONEP_CHECK_PTR(w2_scales);
+    MOONEP_CHECK_PTR(ws);
+    MOONEP_CHECK_PTR(out);
+    const F8Dims d{dims->R * dims->S, dims->K, dims->E, dims->H, dims->I};
+    const size_t E = d.E, pairs = (size_t)d.T * d.K, rows = (size_t)d.T * d.H * 2;
+    F8Ws w;
+    const size_t ws_bytes = f8_ws_layout(d, ws, &w);
+    const Span spans[] = {{ws, ws_bytes}, {out, rows}, {topk, pairs * 4}, {gates, pairs * 4}, {x, rows},
+                          {w13_codes, E * moonep_fp8_code_bytes(d.H, 2 * d.I)},
+                          {w13_scales, E * moonep_fp8_scale_bytes(d.H, 2 * d.I)},
+                          {w2_codes, E * moonep_fp8_code_bytes(d.I, d.H)},
+                          {w2_scales, E * moonep_fp8_scale_bytes(d.I, d.H)}};
+    if (outputs_overlap(spans, 2, 9)) return MOONEP_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const F8Mat up = f8_mat(w13_codes, w13_scales, d.H, 2 * d.I), down = f8_mat(w2_codes, w2_scales, d.I, d.H);
+    SortArgs a = sort_args((int)pairs, d.E);
+    a.topk = topk, a.hist = w.hist, a.offsets = w.offsets, a.dest = w.dest, a.pair = w.pair;
+    a.run_rows = w.run_rows, a.runs = w.runs, a.nruns = w.nruns;
+    if (launch_sort(a, s) != MOONEP_OK) return MOONEP_EHIP;
+    hipLaunchKernelGGL(fp8_rows_kernel, dim3(d.T, (up.kb + 15) / 16), dim3(256), 0, s, static_cast<const uint16_t*>(x), w.x,
+                       d.H, up.kb);
+    MOONEP_LAUNCH_CHECK();
+    hipLaunchKernelGGL(fp8_thin_up_kernel<2>, dim3(blks(d.I) * w.max_runs), dim3(512), 0, s, up, w, d);
+    MOONEP_LAUNCH_CHECK();
+    hipLaunchKernelGGL(fp8_thin_down_kernel, dim3(blks(d.H) * w.max_runs), dim3(256), 0, s, down, w, d);
+    MOONEP_LAUNCH_CHECK();
+    hipLaunchKernelGGL(fp8_join_kernel, dim3(d.T, (d.H / 4 + 255) / 256), dim3(256), 0, s, gates, w,
+                       static_cast<uint2*>(out), d);
+    MOONEP_LAUNCH_CHECK();
+    return MOONEP_OK;
+}

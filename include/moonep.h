@@ -405,6 +405,43 @@ int moonep_sort(const moonep_dims_t* dims, const int32_t* topk, void* ws, int32_
 int moonep_combine_backward(const moonep_dims_t* dims, const int32_t* dest, const void* y, const float* gates,
                             const void* dout, void* dy, float* dgates, void* stream);
 
+/* 8-bit weights.  A matrix [Kin, N] (multiples of 32 both) is held as e4m3 codes (OCP FP8: no infinities) and one
+ * scale byte s, worth 2^(s - 127), for each block of 128 x 128.  Powers of two, because the matrix instruction
+ * applies those itself.  Layout, chosen so that a wave's 16-byte loads are one KiB in a row and each lane gets 16 input
+ * values of one column:
+ *   codes  [N/32][ceil(Kin/128)][8 pieces][32 columns][16 bytes along Kin]; codes past Kin are 0
+ *   scales [ceil(N/128)][ceil(Kin/128), padded to a multiple of 4]; scales past Kin are 127
+ * These give one matrix's bytes; 0 for invalid sizes. */
+size_t moonep_fp8_code_bytes(int32_t Kin, int32_t N);
+size_t moonep_fp8_scale_bytes(int32_t Kin, int32_t N);
+
+/* Quantises E matrices: the scale of a block is the smallest power of two that 448 of hold its largest
+ * magnitude, at least 2^-126; each value is divided by it and rounded to the nearest code, halfway to the even
+ * one.  A block with an infinity or a NaN gets codes that are NaN, and the scale byte 127.
+ *   w [E, Kin, N] bf16;  codes [E, moonep_fp8_code_bytes()], scales [E, moonep_fp8_scale_bytes()] out */
+int moonep_quantize_fp8(int32_t E, int32_t Kin, int32_t N, const void* w, void* codes, void* scales, void* stream);
+
+/* The experts' SwiGLU FFN with 8-bit weights, from one decoded token to whole prompts:
+ *   out[r,s] = sum over k (in k order) of gates[r,s,k] * (q(silu(q(x) G) * (q(x) U)) D)  of expert topk[r,s,k],
+ * G | U the columns of its w13, D its w2.  q rounds a row to e4m3 as the weights are, with a scale for each 128
+ * values along it; a block with an infinity or a NaN is NaN.  Products in matrix instructions with float32
+ * accumulation; the result is rounded to nearest even once, and in calls of many pairs an expert's output to bf16
+ * before it is weighted, as moonep_grouped_ffn's is.  Needs no plan: dims' R, S, K, E, H and I count, the
+ * planner's limits on E/R and B do not apply.  An output depends on its own token only, and on dims.
+ *   topk  [R, S, K] int32: an id outside [0, E) adds nothing, whatever its gate (rows of ended
+ *         sequences: all ids -1, their output is zero); an id named twice counts twice
+ *   gates [R, S, K] float32;  x [R, S, H] bf16;  out [R, S, H] bf16 out
+ *   w13_codes, w13_scales: E matrices [H, 2I];  w2_codes, w2_scales: E matrices [I, H]
+ *   ws    moonep_fp8_ffn_workspace_bytes() bytes, scratch (same rules as above)
+ * out and ws must not overlap inputs or each other (MOONEP_EINVAL).
+ * MOONEP_ENOTSUP if H or I is not a multiple of 32, with MOONEP_F32_ROWS, or if R*S*K is more than
+ * MOONEP_FP8_MAX_PAIRS. */
+#define MOONEP_FP8_MAX_PAIRS (1 << 22)
+size_t moonep_fp8_ffn_workspace_bytes(const moonep_dims_t* dims);
+int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* gates, const void* x,
+                   const void* w13_codes, const void* w13_scales, const void* w2_codes, const void* w2_scales,
+                   void* ws, void* out, void* stream);
+
 /* Static description of an error code. */
 const char* moonep_strerror(int code);
 
