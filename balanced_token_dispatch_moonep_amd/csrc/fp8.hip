@@ -6,6 +6,7 @@
 // power of two for each 128 values along it.  The matrix instruction v_mfma_scale_f32_32x32x64_f8f6f4 multiplies
 // such codes and applies both powers itself, so a product needs no arithmetic beside it; that is why the scales
 // are powers of two and not floats (which would cost a multiply-add for every accumulator and block).
+#include "dma.h"
 #include "sort.h"
 
 #include <type_traits>
@@ -43,12 +44,22 @@ struct F8Ws {
     Run* runs;
     int max_runs, run_rows;
     F8Rows x, act;                   // [T], [P]
-    float* y;                        // [P][H]
+    float* y;                        // [P][H], with few rows
+    uint16_t* y16;                   // [P][H], with many: float16 times
+    uint8_t* y16_exp;                // [P][H/64] a power of two for each 64
+    int y16_sp;
 };
 
 __host__ __device__ static constexpr int blks(int n) { return (n + kBlk - 1) / kBlk; }
 
-constexpr int kThinRows = 32;
+constexpr int kThinRows = 32;        // rows of a run, where few rows are multiplied at a time
+constexpr int kThinEach = 48;        // pairs an expert, below which that is done
+
+// Rows of a run, and of a tile: by the pairs that an expert has on average.
+static int f8_rows(const F8Dims& d) {
+    const int64_t pairs = (int64_t)d.T * d.K;
+    return pairs < (int64_t)kThinEach * d.E ? kThinRows : pairs < 192ll * d.E ? 128 : 256;
+}
 
 static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
     const size_t pairs = (size_t)d.T * d.K, experts = std::min<size_t>(pairs, d.E);
@@ -67,17 +78,23 @@ static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
         r.scales = take(n * r.sp);
         return r;
     };
-    w.run_rows = kThinRows;
+    w.run_rows = f8_rows(d);
+    // the same parts for every way of a call, so that the scratch of a larger call serves smaller ones
     w.max_runs = (int)(experts + pairs / w.run_rows);
-    w.hist = (int32_t*)take(sort_hist_bytes(sort_args((int)pairs, d.E)));
+    w.hist = (int32_t*)take(pairs > kSortOnce ? std::min<size_t>((pairs + 4095) / 4096, kSortParts) * d.E * 4 : 0);
     w.offsets = (int32_t*)take((size_t)(d.E + 1) * 4);
     w.dest = (int32_t*)take(pairs * 4);
     w.pair = (int32_t*)take(pairs * 4);
     w.nruns = (int32_t*)take(4);
-    w.runs = (Run*)take(w.max_runs * sizeof(Run));
+    w.runs = (Run*)take((experts + pairs / kThinRows) * sizeof(Run));
     w.x = rows(d.T, d.H);
     w.act = rows(pairs, d.I);
-    w.y = (float*)take(pairs * d.H * 4);
+    w.y16_sp = (d.H + 63) / 64;
+    const size_t thin = std::min<size_t>(pairs, (size_t)kThinEach * d.E) * d.H * 4, y16 = align_up(pairs * d.H * 2, 256);
+    uint8_t* y = take(std::max(thin, y16 + pairs * w.y16_sp));
+    w.y = (float*)y;
+    w.y16 = (uint16_t*)y;
+    w.y16_exp = y + y16;
     if (ws) *ws = w;
     return off;
 }
@@ -329,6 +346,280 @@ __global__ __launch_bounds__(256) void fp8_thin_down_kernel(F8Mat m, F8Ws w, F8D
     }
 }
 
+// The bits of the largest of eight lanes, in each of them.
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, true));     // pairs
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true));     // fours
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true)); // mirrored eights
+}
+
+// Eight columns of a row of y by each of eight lanes: float16 with one power of two that brings the
+// largest of the 64 to 2^14 .. 2^15, half the bytes of float32 and off by 2^-12 (bf16 would be by 2^-9, as
+// much as the output's own rounding).  The stored byte is the largest one's exponent field.
+__device__ __forceinline__ void put_y(const float (&v)[8], const F8Ws& w, const F8Dims& d, size_t row, int col,
+                                      bool valid) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7f800000u);
+    // infinities and NaN stay what they are
+    const uint32_t e = min(max(max8(top) >> 23, 15u), 254u);
+    const float m = __uint_as_float((268u - e) << 23);
+    if (!valid || col >= d.H) return;
+    union {
+        _Float16 h[8];
+        uint4 u;
+    } r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.h[i] = (_Float16)(v[i] * m);
+    *reinterpret_cast<uint4*>(w.y16 + row * d.H + col) = r.u;
+    if (col % 64 == 0) w.y16_exp[row * w.y16_sp + col / 64] = (uint8_t)e;
+}
+
+// ---------------------------------------------------------------------------
+// products of many rows
+// ---------------------------------------------------------------------------
+
+constexpr int kRing[3] = {3, 3, 2};              // stages in LDS for tiles of 64, 128 and 256 rows
+
+// Tiles of BM rows x 256 columns (UP: 128 gate and the 128 up columns that belong to them); eight waves
+// of BM / 2 x 64.  A stage is one block of 128 input values: BM rows of A, eight column tiles of B.
+template <int BM>
+struct F8Tile {
+    static constexpr int MT = BM / 64;           // 32-row blocks of a wave
+    static constexpr int NS = kRing[MT / 2];
+    static constexpr int ABYTES = BM * kBlk, BBYTES = 256 * kBlk, STAGE = ABYTES + BBYTES;
+    static constexpr int PER = MT + 4;           // copies of a wave and stage
+    static constexpr int SCALES = NS * STAGE;    // scale bytes of the rows: [2][BM][16], 16 stages each
+    static constexpr int LOOP = SCALES + 2 * BM * 16;
+    static constexpr int ACT_PITCH = kBlk + 4, Y_PITCH = 64 + 4;
+    static constexpr int UP_BYTES = BM * ACT_PITCH * 4, DOWN_BYTES = 8 * 32 * Y_PITCH * 4;
+    static constexpr int SMEM = std::max(LOOP, std::max(UP_BYTES, DOWN_BYTES));
+    static_assert(SMEM <= 160 * 1024, "one workgroup a CU");
+};
+
+__device__ __forceinline__ i32x8_t operand(uint4 a, uint4 b) {
+    return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+template <int MT>
+struct F8Frags {
+    i32x8_t a[MT], b[2];
+};
+
+template <int BM, bool UP>
+__global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dims d) {
+    using L = F8Tile<BM>;
+    constexpr int MT = L::MT, NS = L::NS, PER = L::PER;
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / 4, wn = wave % 4;
+    const F8Rows in = UP ? w.x : w.act;
+    const int ncol = m.n / kCols, NT = UP ? (d.I + 127) / 128 : (d.H + 255) / 256;
+    const int nruns = sload(w.nruns), total = nruns * NT;
+    // each XCD (blockIdx % 8) takes a contiguous range of tiles, whose neighbours share rows and weights
+    const int chunk = (total + 7) / 8, first = blockIdx.x % 8 * chunk, end = min(total, first + chunk);
+    const uint32_t lds = lds_addr(smem);
+    const uint32_t a_to = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
+    const uint32_t b_to = __builtin_amdgcn_readfirstlane(lds + L::ABYTES + wave * 4096);
+    const uint32_t s_to = __builtin_amdgcn_readfirstlane(lds + L::SCALES + wave * BM / 8 * 16);
+    // where a lane reads 16 bytes of its row of a 32-row block: piece p of the block of 128
+    const int r32 = lane & 31, half = lane >> 5;
+    int a_at[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) a_at[p] = (wm * (BM / 2) + r32) * 128 + ((2 * p + half) ^ (r32 >> 1 & 7)) * 16;
+
+    for (int t = first + blockIdx.x / 8; t < end; t += gridDim.x / 8) {
+        // tiles go expert by expert, column tile by column tile, run by run
+        const Run* runs = w.runs;
+        const int r0 = t / NT, e = sload(&runs[r0].expert), begin = sload(w.offsets + e);
+        const int mtiles = (sload(w.offsets + e + 1) - begin + BM - 1) / BM;
+        const int rb = r0 - (sload(&runs[r0].first) - begin) / BM, local = t - rb * NT;
+        const int nt = local / mtiles, mt = local % mtiles;
+        const int row0 = begin + mt * BM, rows = min(BM, sload(w.offsets + e + 1) - row0);
+        // column tiles that this wave copies and multiplies, past the last one the last one
+        int copy, cols[2];
+        if (UP) {
+            const int g = d.I / kCols;
+            copy = (wave < 4 ? 0 : g) + min(nt * 4 + wn, g - 1);
+            cols[0] = min(nt * 4 + wn, g - 1);
+            cols[1] = g + cols[0];
+        } else {
+            copy = min(nt * 8 + wave, ncol - 1);
+            cols[0] = min(nt * 8 + 2 * wn, ncol - 1);
+            cols[1] = min(nt * 8 + 2 * wn + 1, ncol - 1);
+        }
+        const int nst = m.kb;
+        const uint4* B = m.codes + ((size_t)e * ncol + copy) * nst * 256;
+        const int32_t* sb[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            sb[j] = reinterpret_cast<const int32_t*>(m.scales + ((size_t)e * m.nb + cols[j] / 4) * m.kbp);
+        // the rows that this lane copies: eight a copy, eight lanes a row, pieces swapped by row so that
+        // sixteen rows side by side meet sixteen different groups of banks when they are read
+        uint32_t ao[MT];
+        const uint8_t* A = UP ? in.codes : in.codes + (size_t)row0 * in.pitch;
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+            const int r = u * 64 + wave * 8 + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
+            const uint32_t row = r >= rows ? 0u : UP ? (uint32_t)(w.pair[row0 + r] / d.K) : (uint32_t)r;
+            ao[u] = r < rows ? row * (uint32_t)in.pitch + c * 16 : kZeroOff;
+        }
+        const uint8_t* sp;
+        {
+            const int r = row0 + min(wave * (BM / 8) + min(lane, BM / 8 - 1), rows - 1);
+            sp = in.scales + (size_t)(UP ? w.pair[r] / d.K : r) * in.sp;
+        }
+        auto copy_scales = [&](int seg) {
+            if (lane < BM / 8)
+                dma16(reinterpret_cast<const uint16_t*>(sp + seg * 16), s_to + (seg & 1) * BM * 16);
+        };
+        auto copy_part = [&](int s, int buf, int i) {    // copy i of stage s
+            const uint32_t to = buf * L::STAGE;
+            if (i < MT) dma16b(rsrc_of(A + (size_t)s * kBlk), ao[i], a_to + to + i * 8192);
+            else dma16s(reinterpret_cast<const uint16_t*>(B + (size_t)s * 256 + (i - MT) * 64), lane * 16,
+                        b_to + to + (i - MT) * 1024);
+        };
+
+        f32x16_t acc[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+        copy_scales(0);
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            if (s < nst)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) copy_part(s, s, i);
+        if (nst >= 3 && NS == 3) wait_vm<2 * PER>();
+        else if (nst >= 2) wait_vm<PER>();
+        else wait_vm<0>();
+        block_sync();
+
+        F8Frags<MT> f0, f1;
+        int sa0[MT], sa1[MT];        // scales of this stage's rows and the next one's
+        auto read_a = [&](F8Frags<MT>& f, const char* st, int kk, int i) {
+            f.a[i] = operand(*reinterpret_cast<const uint4*>(st + a_at[2 * kk] + i * 4096),
+                             *reinterpret_cast<const uint4*>(st + a_at[2 * kk + 1] + i * 4096));
+        };
+        auto read_b = [&](F8Frags<MT>& f, const char* st, int kk) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const char* p = st + L::ABYTES + (UP ? wn + 4 * j : 2 * wn + j) * 4096 + kk * 2048 + lane * 16;
+                f.b[j] = operand(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 1024));
+            }
+        };
+        auto read_sa = [&](int (&sa)[MT], int s) {
+            const char* p = smem + L::SCALES + ((s >> 4) & 1) * BM * 16 + (wm * (BM / 2) + r32) * 16 + (s & 15);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) sa[i] = *reinterpret_cast<const uint8_t*>(p + i * 512);
+        };
+        read_sa(sa0, 0);
+        read_b(f0, smem, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) read_a(f0, smem, 0, i);
+        // One stage: two slices of 64 input values.  After the first one every wave has read all of the
+        // stage and, behind the barrier, the next stage is there for all; this stage's buffer then takes
+        // stage s + NS.  A row block's operand is read where the one before has been used, so one set of
+        // registers serves.  steady: stage s + NS exists; more: stage s + 1 does.
+        int cur = 0;
+        auto stage = [&](int s, auto steady_c, auto more_c) {
+            constexpr bool steady = decltype(steady_c)::value, more = decltype(more_c)::value;
+            const char* st = smem + cur * L::STAGE;
+            const int nxt = cur + 1 == NS ? 0 : cur + 1;
+            const int w0 = sload(sb[0] + (s >> 2)) >> (8 * (s & 3)) & 255, w1 = sload(sb[1] + (s >> 2)) >> (8 * (s & 3)) & 255;
+            read_b(f1, st, 1);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.a[i], f0.b[0], acc[i][0], 0, 0, 0, sa0[i], 0, w0);
+                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.a[i], f0.b[1], acc[i][1], 0, 0, 0, sa0[i], 0, w1);
+                __builtin_amdgcn_sched_barrier(0);
+                read_a(f1, st, 1, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            wait_lgkm0();
+            if (NS == 3 && (steady || s + 2 < nst)) wait_vm<PER>();
+            else wait_vm<0>();
+            block_sync();
+            if constexpr (more) {
+                read_sa(sa1, s + 1);
+                read_b(f0, smem + nxt * L::STAGE, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.a[i], f1.b[0], acc[i][0], 0, 0, 0, sa0[i], 0, w0);
+                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.a[i], f1.b[1], acc[i][1], 0, 0, 0, sa0[i], 0, w1);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (more) read_a(f0, smem + nxt * L::STAGE, 0, i);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (steady) {
+#pragma unroll
+                    for (int p = PER * i / MT; p < PER * (i + 1) / MT; ++p) copy_part(s + NS, cur, p);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) sa0[i] = sa1[i];
+            cur = nxt;
+        };
+        int s = 0;
+        while (s + NS < nst) {       // the scales of the next 16 stages, then 16 stages: no branch among these
+            if (s + 16 < nst) copy_scales((s >> 4) + 1);
+            for (const int stop = min(nst - NS, s + 16); s < stop; ++s) stage(s, std::true_type{}, std::true_type{});
+        }
+        for (; s + 1 < nst; ++s) stage(s, std::false_type{}, std::true_type{});
+        stage(s, std::false_type{}, std::false_type{});
+
+        if constexpr (UP) {
+            // act in float32 by way of LDS, so that 16 lanes get a row's block of 128 and round it
+            float* act = reinterpret_cast<float*>(smem);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    act[(wm * (BM / 2) + i * 32 + result_row(r, lane)) * L::ACT_PITCH + wn * 32 + r32] =
+                        silu_times(acc[i][0][r], acc[i][1][r]);
+            __syncthreads();
+#pragma unroll 2
+            for (int r = tid / 16; r < rows; r += 32) {
+                const int c8 = tid % 16 * 8;
+                const float4 p = *reinterpret_cast<const float4*>(act + r * L::ACT_PITCH + c8);
+                const float4 q = *reinterpret_cast<const float4*>(act + r * L::ACT_PITCH + c8 + 4);
+                float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+                if (nt * 128 + c8 >= d.I)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                put_block(v, w.act, (size_t)row0 + r, nt, tid % 16);
+            }
+            __syncthreads();
+        } else {
+            float* ep = reinterpret_cast<float*>(smem) + wave * 32 * L::Y_PITCH;
+            const int c8 = lane % 8 * 8, col = nt * 256 + wn * 64 + c8;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) ep[result_row(r, lane) * L::Y_PITCH + j * 32 + r32] = acc[i][j][r];
+                wave_sync();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int rr = q * 8 + lane / 8, r = wm * (BM / 2) + i * 32 + rr;
+                    const float4 a = *reinterpret_cast<const float4*>(ep + rr * L::Y_PITCH + c8);
+                    const float4 b = *reinterpret_cast<const float4*>(ep + rr * L::Y_PITCH + c8 + 4);
+                    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    put_y(v, w, d, (size_t)row0 + r, col, r < rows);
+                }
+                wave_sync();
+            }
+            __syncthreads();
+        }
+    }
+}
+
 // out = sum over k of gate * y, in k order, skipping ids that name no expert.
 __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ gates, F8Ws w, uint2* __restrict__ out,
                                                        F8Dims d) {
@@ -348,9 +639,68 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__
     out[(size_t)t * (d.H / 4) + h] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
+// The same of float16 rows: a wave a token, a chunk of one row after another, as moonep_combine.
+__global__ __launch_bounds__(256) void fp8_join16_kernel(const float* __restrict__ gates, F8Ws w, uint4* __restrict__ out,
+                                                         F8Dims d) {
+    constexpr int VB = 7;
+    const int tok = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, vecs = d.H / 8;
+    if (tok >= d.T) return;
+    const int32_t* dest = w.dest + (size_t)tok * d.K;
+    for (int v0 = 0; v0 < vecs; v0 += 64 * VB) {
+        float acc[VB][8] = {};
+#pragma unroll 1
+        for (int k = 0; k < d.K; ++k) {
+            const int row = dest[k];
+            if (row < 0) continue;
+            const float g = gates[(size_t)tok * d.K + k];
+            const uint4* y = reinterpret_cast<const uint4*>(w.y16) + (size_t)row * vecs;
+            const uint8_t* ex = w.y16_exp + (size_t)row * w.y16_sp;
+#pragma unroll
+            for (int u = 0; u < VB; ++u) {
+                const int v = v0 + u * 64 + lane;
+                if (v >= vecs) continue;
+                union {
+                    uint4 u;
+                    _Float16 h[8];
+                } r;
+                r.u = ld_nt(y + v);
+                const float s = __uint_as_float((uint32_t)(ex[v / 8] - 14) << 23);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[u][i] += g * ((float)r.h[i] * s);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < VB; ++u) {
+            const int v = v0 + u * 64 + lane;
+            if (v < vecs)
+                st_nt(make_uint4(pack_bf16(acc[u][0], acc[u][1]), pack_bf16(acc[u][2], acc[u][3]),
+                                 pack_bf16(acc[u][4], acc[u][5]), pack_bf16(acc[u][6], acc[u][7])),
+                      out + (size_t)tok * vecs + v);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
+
+template <int BM, bool UP>
+static int launch_tiles(const F8Mat& m, const F8Ws& w, const F8Dims& d, hipStream_t s) {
+    const auto kernel = fp8_tile_kernel<BM, UP>;
+    constexpr int smem = F8Tile<BM>::SMEM;
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        hipSuccess)
+        return MOONEP_EHIP;
+    hipLaunchKernelGGL(kernel, dim3(256), dim3(512), smem, s, m, w, d);
+    MOONEP_LAUNCH_CHECK();
+    return MOONEP_OK;
+}
+
+template <int BM>
+static int launch_both(const F8Mat& up, const F8Mat& down, const F8Ws& w, const F8Dims& d, hipStream_t s) {
+    const int rc = launch_tiles<BM, true>(up, w, d, s);
+    return rc != MOONEP_OK ? rc : launch_tiles<BM, false>(down, w, d, s);
+}
 
 static bool f8_size(int32_t kin, int32_t n) {
     return kin >= kCols && kin % kCols == 0 && n >= kCols && n % kCols == 0 && kin <= 1 << 20 && n <= 1 << 21;
@@ -370,6 +720,8 @@ static int check_f8(const moonep_dims_t* d) {
     if (d->flags & MOONEP_F32_ROWS) return MOONEP_ENOTSUP;
     if (!f8_size(d->H, d->I) || !f8_size(d->I, d->H)) return MOONEP_ENOTSUP;
     if ((int64_t)d->R * d->S * d->K > MOONEP_FP8_MAX_PAIRS) return MOONEP_ENOTSUP;
+    // rows of x are found by 32-bit offsets
+    if ((int64_t)d->R * d->S * blks(d->H) * kBlk > 0xffff0000ll) return MOONEP_ENOTSUP;
     return MOONEP_OK;
 }
 
@@ -439,6 +791,15 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     hipLaunchKernelGGL(fp8_rows_kernel, dim3(d.T, (up.kb + 15) / 16), dim3(256), 0, s, static_cast<const uint16_t*>(x), w.x,
                        d.H, up.kb);
     MOONEP_LAUNCH_CHECK();
+    if (w.run_rows != kThinRows) {
+        const int rc2 = w.run_rows == 64 ? launch_both<64>(up, down, w, d, s)
+                        : w.run_rows == 128 ? launch_both<128>(up, down, w, d, s)
+                                            : launch_both<256>(up, down, w, d, s);
+        if (rc2 != MOONEP_OK) return rc2;
+        hipLaunchKernelGGL(fp8_join16_kernel, dim3((d.T + 3) / 4), dim3(256), 0, s, gates, w, static_cast<uint4*>(out), d);
+        MOONEP_LAUNCH_CHECK();
+        return MOONEP_OK;
+    }
     hipLaunchKernelGGL(fp8_thin_up_kernel<2>, dim3(blks(d.I) * w.max_runs), dim3(512), 0, s, up, w, d);
     MOONEP_LAUNCH_CHECK();
     hipLaunchKernelGGL(fp8_thin_down_kernel, dim3(blks(d.H) * w.max_runs), dim3(256), 0, s, down, w, d);

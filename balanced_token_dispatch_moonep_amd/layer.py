@@ -14,12 +14,13 @@ from __future__ import annotations
 
 import torch
 
-from . import (Dims, GradList, moonep_combine, moonep_dispatch, moonep_grad_clip, moonep_grad_norm,
-               moonep_grad_norm_workspace_bytes, moonep_grouped_ffn, moonep_grouped_ffn_backward,
+from . import (Dims, GradList, moonep_combine, moonep_combine_backward, moonep_dispatch, moonep_fp8_code_bytes,
+               moonep_fp8_ffn, moonep_fp8_ffn_workspace_bytes, moonep_fp8_scale_bytes, moonep_grad_clip,
+               moonep_grad_norm, moonep_grad_norm_workspace_bytes, moonep_grouped_ffn, moonep_grouped_ffn_backward,
                moonep_layer_norm, moonep_layer_norm_backward, moonep_layer_norm_workspace_bytes,
-               moonep_plan, moonep_plan_workspace_bytes, moonep_prefetch, moonep_quantize_w4,
-               moonep_reduce_grad, moonep_w4_code_bytes, moonep_w4_ffn, moonep_w4_ffn_workspace_bytes,
-               moonep_w4_scale_bytes, NSTATS)
+               moonep_plan, moonep_plan_workspace_bytes, moonep_prefetch, moonep_quantize_fp8, moonep_quantize_w4,
+               moonep_reduce_grad, moonep_route, moonep_route_backward, moonep_w4_code_bytes, moonep_w4_ffn,
+               moonep_w4_ffn_workspace_bytes, moonep_w4_scale_bytes, NSTATS, ROUTE_SOFTMAX)
 
 
 def _slot_shapes(R, B, H, I):
@@ -76,6 +77,38 @@ def stack_slot_bytes(R, B, H, I, layers, pooled, training=False) -> int:
     return per if pooled else layers * per
 
 
+class Router:
+    """Top K and gates of a router's logits, and their gradient.
+
+    ``dims``: R, S, E and K count.  ``mode``: ROUTE_SOFTMAX, ROUTE_SOFTMAX_ALL or ROUTE_SIGMOID; ``scale`` multiplies
+    the gates; ``bias`` [E] float32 or None moves the choice only (read at each call, so it may be updated in
+    place).  All buffers are static: a call replaces the outputs of the one before.
+    """
+
+    def __init__(self, dims: Dims, mode: int = ROUTE_SOFTMAX, scale: float = 1.0, bias=None, training: bool = False,
+                 dtype=torch.float32, device="cuda"):
+        dev = torch.device(device)
+        R, S, E, K = dims.R, dims.S, dims.E, dims.K
+        self.d, self.mode, self.scale, self.bias, self.training = dims, mode, scale, bias, training
+        self.topk = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+        self.gates = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+        self.dlogits = torch.empty((R, S, E), dtype=dtype, device=dev) if training else None
+        self.logits = None        # of the last forward, which its backward reads
+
+    def forward(self, logits):
+        """(topk, gates) of the logits [R, S, E], which must stay as they are until the backward."""
+        moonep_route(self.d, logits, self.bias, self.topk, self.gates, self.mode, self.scale)
+        self.logits = logits
+        return self.topk, self.gates
+
+    def backward(self, dgates):
+        """dlogits [R, S, E] from dgates [R, S, K], such as a layer's with ``gate_grad``."""
+        if not self.training or self.logits is None:
+            raise ValueError("backward needs a training router and its forward")
+        moonep_route_backward(self.d, dgates, self.logits, self.topk, self.dlogits, self.mode, self.scale)
+        return self.dlogits
+
+
 class MoonEPLayer:
     """One emulated EP layer: R ranks as R static partitions of one GPU's memory.
 
@@ -88,12 +121,17 @@ class MoonEPLayer:
     writes ``dnorm_weight`` and ``dnorm_bias``.  A router that reads the normed rows calls ``norm(x)``
     itself; ``forward`` given what that returned does not norm again, and given a copy of it does not
     with ``normed=True``.  ``backward`` goes back to the rows of the last ``norm(x)``.
+
+    With ``gate_grad``, ``backward`` also writes ``dgates`` [R, S, K], the gradient of the gates, for the
+    router's backward.
     """
 
     def __init__(self, dims: Dims, w13=None, w2=None, training: bool = False, device="cuda", pool=None,
-                 norm_weight=None, norm_bias=None, norm_eps: float = 1e-5):
+                 norm_weight=None, norm_bias=None, norm_eps: float = 1e-5, gate_grad: bool = False):
         if norm_bias is not None and norm_weight is None:
             raise ValueError("norm_bias needs norm_weight")
+        if gate_grad and not (training and dims.I > 0):
+            raise ValueError("only a training layer with experts has a gradient of the gates")
         self.d = dims
         self.training = training
         self.pool = pool
@@ -110,6 +148,7 @@ class MoonEPLayer:
         self.recv = torch.empty((M, H), dtype=rt, device=dev)
         self.out = torch.empty((R, S, H), dtype=rt, device=dev)
         self.w13, self.w2 = w13, w2
+        self.dgates = torch.empty((R, S, K), dtype=torch.float32, device=dev) if gate_grad else None
         self.norm_weight, self.norm_bias, self.norm_eps = norm_weight, norm_bias, norm_eps
         if norm_weight is not None:
             f32 = torch.float32
@@ -198,13 +237,17 @@ class MoonEPLayer:
 
     def backward(self, dout, gates):
         """Gradient of forward(): returns dx [R, S, H]; writes dw13 / dw2 (fp32; added to them
-        with MOONEP_GRAD_ACCUM), slot replicas' gradients reduced into their home experts.
+        with MOONEP_GRAD_ACCUM), slot replicas' gradients reduced into their home experts, and
+        dgates (with gate_grad).
 
         The saved gate|up activations are overwritten by their gradients."""
         assert self.training and self.d.I > 0
         if self.pool is not None and self.pool.owner is not self:
             self.prefetch()       # a later layer reused the shared slots
-        moonep_dispatch(self.d, self.dest, dout, gates, self.dy)
+        if self.dgates is not None:
+            moonep_combine_backward(self.d, self.dest, self.y, gates, dout, self.dy, self.dgates)
+        else:
+            moonep_dispatch(self.d, self.dest, dout, gates, self.dy)
         moonep_grouped_ffn_backward(self.d, self.ws, self.cu, self.recv, self.gu, self.act, self.dy,
                                     self.w13, self.w2, self.w13_slot, self.w2_slot, self.drecv,
                                     self.dw13, self.dw2, self.dw13_red, self.dw2_red)
@@ -224,11 +267,15 @@ class MoonEPLayer:
         norm = [self.dnorm_weight, self.dnorm_bias] if self.norm_weight is not None else []
         return [g for g in [self.dw13, self.dw2, *norm] if g is not None]
 
-    def decoder(self, max_tokens: int) -> "W4Experts":
-        """The same norm and experts for decoding, with 4-bit weights made from the present ones."""
+    def decoder(self, max_tokens: int, bits: int = 4) -> "W4Experts | Fp8Experts":
+        """The same norm and experts for decoding, with weights of 4 or 8 bits made from the present ones.
+        8 bits serve whole prompts too."""
         if self.d.I == 0:
             raise ValueError("a layer without experts has nothing to decode with")
-        return W4Experts(self.w13, self.w2, self.d.K, max_tokens, self.norm_weight, self.norm_bias, self.norm_eps)
+        if bits not in (4, 8):
+            raise ValueError(f"weights of 4 or 8 bits, not {bits}")
+        kind = W4Experts if bits == 4 else Fp8Experts
+        return kind(self.w13, self.w2, self.d.K, max_tokens, self.norm_weight, self.norm_bias, self.norm_eps)
 
 
 class GradClipper:
@@ -248,8 +295,8 @@ class GradClipper:
         return self.norm
 
 
-class W4Experts:
-    """A layer's experts for decoding: up to max_tokens tokens a call, weights in 4 bits.
+class _Experts:
+    """A layer's experts with quantised weights: up to max_tokens tokens a call.
 
     ``w13`` [E, H, 2I] and ``w2`` [E, I, H] bf16 are quantised here, once, and not kept.  All buffers
     are static, so a call can be captured; a call replaces the output of the one before.
@@ -262,11 +309,12 @@ class W4Experts:
         self.norm_weight, self.norm_bias, self.norm_eps = norm_weight, norm_bias, norm_eps
         self.packed = []
         for w, kin, n in ((w13, H, 2 * I), (w2, I, H)):
-            codes = torch.empty((E, moonep_w4_code_bytes(kin, n)), dtype=u8, device=dev)
-            scales = torch.empty((E, moonep_w4_scale_bytes(kin, n)), dtype=u8, device=dev)
-            moonep_quantize_w4(w, codes, scales)
+            code_bytes, scale_bytes = self._bytes(kin, n)
+            codes = torch.empty((E, code_bytes), dtype=u8, device=dev)
+            scales = torch.empty((E, scale_bytes), dtype=u8, device=dev)
+            self._quantize(w, codes, scales)
             self.packed += [codes, scales]
-        self.ws = torch.empty(moonep_w4_ffn_workspace_bytes(self._dims(max_tokens)), dtype=u8, device=dev)
+        self.ws = torch.empty(self._workspace(self._dims(max_tokens)), dtype=u8, device=dev)
         self.normed = torch.empty((max_tokens, H), dtype=torch.bfloat16, device=dev)
         self.out = torch.empty((max_tokens, H), dtype=torch.bfloat16, device=dev)
 
@@ -293,8 +341,40 @@ class W4Experts:
         if self.norm_weight is not None and not normed and not _within(x, self.normed):
             x = self.norm(x)
         d = self._dims(T)
-        ws = self.ws[:moonep_w4_ffn_workspace_bytes(d)]
+        ws = self.ws[:self._workspace(d)]
         out = self.out[:T]
-        moonep_w4_ffn(d, _aligned(topk).unsqueeze(0), _aligned(gates).unsqueeze(0), x.unsqueeze(0), *self.packed, ws,
-                      out.unsqueeze(0))
+        self._ffn(d, _aligned(topk).unsqueeze(0), _aligned(gates).unsqueeze(0), x.unsqueeze(0), *self.packed, ws,
+                  out.unsqueeze(0))
         return out
+
+
+class W4Experts(_Experts):
+    """Experts for decoding, weights in 4 bits."""
+
+    def _bytes(self, kin, n):
+        return moonep_w4_code_bytes(kin, n), moonep_w4_scale_bytes(kin, n)
+
+    def _quantize(self, w, codes, scales):
+        moonep_quantize_w4(w, codes, scales)
+
+    def _workspace(self, d):
+        return moonep_w4_ffn_workspace_bytes(d)
+
+    def _ffn(self, *args):
+        moonep_w4_ffn(*args)
+
+
+class Fp8Experts(_Experts):
+    """Experts for decoding and for prompts, weights and rows in 8 bits, a scale for each block of 128."""
+
+    def _bytes(self, kin, n):
+        return moonep_fp8_code_bytes(kin, n), moonep_fp8_scale_bytes(kin, n)
+
+    def _quantize(self, w, codes, scales):
+        moonep_quantize_fp8(w, codes, scales)
+
+    def _workspace(self, d):
+        return moonep_fp8_ffn_workspace_bytes(d)
+
+    def _ffn(self, *args):
+        moonep_fp8_ffn(*args)
