@@ -39,9 +39,16 @@ struct F8Rows {
     int pitch, sp;
 };
 
+// A tile of a product of many rows: `rows` rows from row0 on, of one expert, and column tile nt.
+struct alignas(16) Tile {
+    int32_t expert, row0, rows, nt;
+};
+
 struct F8Ws {
     int32_t *hist, *offsets, *dest, *pair, *nruns;
     Run* runs;
+    Tile *up_tiles, *down_tiles;
+    int32_t* token;                  // [P]: of each row
     int max_runs, run_rows;
     F8Rows x, act;                   // [T], [P]
     float* y;                        // [P][H], with few rows
@@ -51,6 +58,10 @@ struct F8Ws {
 };
 
 __host__ __device__ static constexpr int blks(int n) { return (n + kBlk - 1) / kBlk; }
+
+// column tiles of 128 pairs of gate and up columns, and of 256 columns
+__host__ __device__ static constexpr int up_columns(const F8Dims& d) { return (d.I + 127) / 128; }
+__host__ __device__ static constexpr int down_columns(const F8Dims& d) { return (d.H + 255) / 256; }
 
 constexpr int kThinRows = 32;        // rows of a run, where few rows are multiplied at a time
 constexpr int kThinEach = 48;        // pairs an expert, below which that is done
@@ -87,6 +98,10 @@ static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
     w.pair = (int32_t*)take(pairs * 4);
     w.nruns = (int32_t*)take(4);
     w.runs = (Run*)take((experts + pairs / kThinRows) * sizeof(Run));
+    const size_t most = experts + pairs / 128;   // runs, where there are tiles
+    w.up_tiles = (Tile*)take(most * up_columns(d) * sizeof(Tile));
+    w.down_tiles = (Tile*)take(most * down_columns(d) * sizeof(Tile));
+    w.token = (int32_t*)take(pairs * 4);
     w.x = rows(d.T, d.H);
     w.act = rows(pairs, d.I);
     w.y16_sp = (d.H + 63) / 64;
@@ -144,14 +159,36 @@ __device__ __forceinline__ void put_block(const float (&v)[8], const F8Rows& r, 
     if (lane16 == 0) r.scales[row * r.sp + block] = (uint8_t)scale_byte(top);
 }
 
-__global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ x, F8Rows r, int H, int kb) {
+// Rounds rows of x.  With tiles, workgroups past the rows list them: expert by expert, column tile by column
+// tile, run by run, so that neighbours share rows and weights; and the rows' tokens.
+__global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ x, F8Ws w, F8Dims d, int kb) {
+    if ((int)blockIdx.x >= d.T) {
+        if (blockIdx.y > 0) return;
+        int t = (blockIdx.x - d.T) * 256 + threadIdx.x;
+        if (t < w.offsets[d.E]) w.token[t] = w.pair[t] / d.K;
+        const int nruns = w.nruns[0];
+        int NT = up_columns(d);
+        Tile* tiles = w.up_tiles;
+        if (t >= nruns * NT) {
+            t -= nruns * NT;
+            NT = down_columns(d);
+            tiles = w.down_tiles;
+            if (t >= nruns * NT) return;
+        }
+        const Run run = w.runs[t / NT];
+        const int begin = w.offsets[run.expert], rows = w.offsets[run.expert + 1] - begin;
+        const int mtiles = (rows + w.run_rows - 1) / w.run_rows;
+        const int local = t - (t / NT - (run.first - begin) / w.run_rows) * NT, row0 = local % mtiles * w.run_rows;
+        tiles[t] = Tile{run.expert, begin + row0, min(w.run_rows, rows - row0), local / mtiles};
+        return;
+    }
     const int at = blockIdx.y * 16 + threadIdx.x / 16, lane16 = threadIdx.x % 16, k = at * kBlk + lane16 * 8;
     const size_t row = blockIdx.x;
     if (at >= kb) return;
-    const uint4 u = k < H ? *reinterpret_cast<const uint4*>(x + row * H + k) : make_uint4(0, 0, 0, 0);
+    const uint4 u = k < d.H ? *reinterpret_cast<const uint4*>(x + row * d.H + k) : make_uint4(0, 0, 0, 0);
     const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
                         bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
-    put_block(v, r, row, at, lane16);
+    put_block(v, w.x, row, at, lane16);
 }
 
 // A workgroup a block of 128 x 128.  A thread reads eight columns of eight rows; the codes are turned in
@@ -286,6 +323,12 @@ __device__ __forceinline__ void multiply_thin(f32x16_t (&acc)[NT], const F8Mat& 
 
 __device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// The same with the hardware's exponential and reciprocal: off by some 2^-22, far below what the 8-bit products
+// before it are off by.
+__device__ __forceinline__ float silu_fast(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
 // act = q(silu(x G) * (x U)) of a run's rows and 128 columns: a block of act, which the workgroup rounds
 // itself.  Four pairs of tiles, their input direction dealt out to SPLIT waves each.
 template <int SPLIT>
@@ -346,64 +389,120 @@ __global__ __launch_bounds__(256) void fp8_thin_down_kernel(F8Mat m, F8Ws w, F8D
     }
 }
 
-// The bits of the largest of eight lanes, in each of them.
-__device__ __forceinline__ uint32_t max8(uint32_t v) {
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, true));     // pairs
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true));     // fours
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true)); // mirrored eights
-}
-
-// Eight columns of a row of y by each of eight lanes: float16 with one power of two that brings the
-// largest of the 64 to 2^14 .. 2^15, half the bytes of float32 and off by 2^-12 (bf16 would be by 2^-9, as
-// much as the output's own rounding).  The stored byte is the largest one's exponent field.
-__device__ __forceinline__ void put_y(const float (&v)[8], const F8Ws& w, const F8Dims& d, size_t row, int col,
-                                      bool valid) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7f800000u);
-    // infinities and NaN stay what they are
-    const uint32_t e = min(max(max8(top) >> 23, 15u), 254u);
-    const float m = __uint_as_float((268u - e) << 23);
-    if (!valid || col >= d.H) return;
-    union {
-        _Float16 h[8];
-        uint4 u;
-    } r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.h[i] = (_Float16)(v[i] * m);
-    *reinterpret_cast<uint4*>(w.y16 + row * d.H + col) = r.u;
-    if (col % 64 == 0) w.y16_exp[row * w.y16_sp + col / 64] = (uint8_t)e;
-}
-
 // ---------------------------------------------------------------------------
 // products of many rows
 // ---------------------------------------------------------------------------
 
-constexpr int kRing[3] = {3, 3, 2};              // stages in LDS for tiles of 64, 128 and 256 rows
-
 // Tiles of BM rows x 256 columns (UP: 128 gate and the 128 up columns that belong to them); eight waves
-// of BM / 2 x 64.  A stage is one block of 128 input values: BM rows of A, eight column tiles of B.
+// of BM / 2 x 64.  A stage is one block of 128 input values: BM rows of A and eight column tiles of B, copied
+// straight into LDS, NS stages in turn.
 template <int BM>
 struct F8Tile {
     static constexpr int MT = BM / 64;           // 32-row blocks of a wave
-    static constexpr int NS = kRing[MT / 2];
-    static constexpr int ABYTES = BM * kBlk, BBYTES = 256 * kBlk, STAGE = ABYTES + BBYTES;
+    static constexpr int NS = BM == 256 ? 2 : 3;
+    static constexpr int ABYTES = BM * kBlk, STAGE = ABYTES + 256 * kBlk;
     static constexpr int PER = MT + 4;           // copies of a wave and stage
-    static constexpr int SCALES = NS * STAGE;    // scale bytes of the rows: [2][BM][16], 16 stages each
-    static constexpr int LOOP = SCALES + 2 * BM * 16;
-    static constexpr int ACT_PITCH = kBlk + 4, Y_PITCH = 64 + 4;
-    static constexpr int UP_BYTES = BM * ACT_PITCH * 4, DOWN_BYTES = 8 * 32 * Y_PITCH * 4;
-    static constexpr int SMEM = std::max(LOOP, std::max(UP_BYTES, DOWN_BYTES));
+    static constexpr int SCALES_AT = NS * STAGE; // scale bytes of the rows: [2][BM][16], 16 stages each
+    static constexpr int TOPS_AT = SCALES_AT + 2 * BM * 16;    // UP: largest of a row in each of four waves
+    static constexpr int SMEM = TOPS_AT + 4 * BM * 4;
     static_assert(SMEM <= 160 * 1024, "one workgroup a CU");
+    // stores of a wave for a tile without rows or columns past the end, at least
+    static constexpr int stores(bool up) { return up ? MT : 5 * MT; }
 };
 
 __device__ __forceinline__ i32x8_t operand(uint4 a, uint4 b) {
     return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
+// After it the lower half of the wave holds a of both halves, a the lower's and b the upper's; the upper half b's.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ float max_halves(float v) {
+    uint32_t a = __float_as_uint(v), b = a;
+    swap_halves(a, b);
+    return fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+
+// The 64 columns of y that a wave has of 32 rows, of which `valid` are there: float16 with one power of two that brings the largest of
+// them to 2^14 .. 2^15, half the bytes of float32 and off by 2^-12 (bf16 would be by 2^-9, as much as the
+// output's own rounding).  The stored byte is the largest one's exponent field; infinities and NaN, which
+// have none, stay what they are.  A lane has 16 columns of each tile of one row, in fours, and the lane in the
+// other half of the wave the fours between: two of them make 16 bytes.
+__device__ __forceinline__ void put_y(const f32x16_t (&v)[2], const F8Ws& w, const F8Dims& d, size_t row0, int col,
+                                      int valid) {
+    const int half = (threadIdx.x >> 5) & 1;
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(v[j][r]));
+    top = max_halves(top);
+    if (__any(top == __builtin_inff())) {
+        float fine = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) fine = fmaxf(fine, fabsf(v[j][r]) == __builtin_inff() ? 0.0f : fabsf(v[j][r]));
+        top = max_halves(fine);
+    }
+    const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
+    const float m = __uint_as_float((268u - e) << 23);
+    // piece k: columns 16 k .. + 8 in the lower half of the wave, + 8 .. + 16 in the upper one
+    uint32_t h[4][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+            f16x2_t t;
+            t.x = (_Float16)(v[j][2 * i] * m);
+            t.y = (_Float16)(v[j][2 * i + 1] * m);
+            h[j * 2 + i / 4][i % 4] = __builtin_bit_cast(uint32_t, t);
+        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        swap_halves(h[k][0], h[k][2]);
+        swap_halves(h[k][1], h[k][3]);
+    }
+    // 16 lanes of a piece change places with 16 of the next one: a store then covers 64 bytes of 16 rows, and
+    // not 32 of 32 (128 bytes of 8 rows are no faster than 64)
+    const int lane = threadIdx.x & 63, group = lane >> 4;
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto r = __builtin_amdgcn_permlane16_swap(h[k][i], h[k + 1][i], false, false);
+            h[k][i] = r[0];
+            h[k + 1][i] = r[1];
+        }
+        const int c = col + k * 16 + (group & 1) * 16 + (group >> 1) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (lane & 15) + i * 16;
+            if (r < valid && c < d.H)
+                *reinterpret_cast<uint4*>(w.y16 + (row0 + r) * d.H + c) = make_uint4(h[k + i][0], h[k + i][1], h[k + i][2], h[k + i][3]);
+        }
+    }
+    if ((lane & 31) < valid && half == 0 && col < d.H) w.y16_exp[(row0 + lane) * w.y16_sp + col / 64] = (uint8_t)e;
+}
+
 template <int MT>
 struct F8Frags {
     i32x8_t a[MT], b[2];
+};
+
+// What a tile's copies and products read.
+template <int MT>
+struct F8TileIn {
+    const uint4* B;                  // the column tile that this wave copies
+    const int32_t* sb[2];            // scales of the two that it multiplies, four stages a word
+    const uint8_t *A, *S;
+    uint32_t ao[MT];                 // the lane's pieces of A, from there
+    uint32_t so;                     // scales of the row whose scales the lane copies, from S
+    int nt, row0, rows;
 };
 
 template <int BM, bool UP>
@@ -414,71 +513,108 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / 4, wn = wave % 4;
     const F8Rows in = UP ? w.x : w.act;
-    const int ncol = m.n / kCols, NT = UP ? (d.I + 127) / 128 : (d.H + 255) / 256;
-    const int nruns = sload(w.nruns), total = nruns * NT;
+    const int ncol = m.n / kCols, nst = m.kb;
+    const int total = sload(w.nruns) * (UP ? up_columns(d) : down_columns(d));
     // each XCD (blockIdx % 8) takes a contiguous range of tiles, whose neighbours share rows and weights
     const int chunk = (total + 7) / 8, first = blockIdx.x % 8 * chunk, end = min(total, first + chunk);
     const uint32_t lds = lds_addr(smem);
     const uint32_t a_to = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
     const uint32_t b_to = __builtin_amdgcn_readfirstlane(lds + L::ABYTES + wave * 4096);
-    const uint32_t s_to = __builtin_amdgcn_readfirstlane(lds + L::SCALES + wave * BM / 8 * 16);
+    const uint32_t s_to = __builtin_amdgcn_readfirstlane(lds + L::SCALES_AT + wave * (BM / 8) * 16);
     // where a lane reads 16 bytes of its row of a 32-row block: piece p of the block of 128
     const int r32 = lane & 31, half = lane >> 5;
     int a_at[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) a_at[p] = (wm * (BM / 2) + r32) * 128 + ((2 * p + half) ^ (r32 >> 1 & 7)) * 16;
 
-    for (int t = first + blockIdx.x / 8; t < end; t += gridDim.x / 8) {
-        // tiles go expert by expert, column tile by column tile, run by run
-        const Run* runs = w.runs;
-        const int r0 = t / NT, e = sload(&runs[r0].expert), begin = sload(w.offsets + e);
-        const int mtiles = (sload(w.offsets + e + 1) - begin + BM - 1) / BM;
-        const int rb = r0 - (sload(&runs[r0].first) - begin) / BM, local = t - rb * NT;
-        const int nt = local / mtiles, mt = local % mtiles;
-        const int row0 = begin + mt * BM, rows = min(BM, sload(w.offsets + e + 1) - row0);
+    auto tile_of = [&](int t) {
+        const int32_t* p = reinterpret_cast<const int32_t*>((UP ? w.up_tiles : w.down_tiles) + t);
+        return Tile{sload(p), sload(p + 1), sload(p + 2), sload(p + 3)};
+    };
+    // the rows that this lane copies, within the tile: eight a copy, eight lanes a row; and one for its scales
+    auto copied = [&](int u) { return u < MT ? u * 64 + wave * 8 + (lane >> 3) : wave * (BM / 8) + min(lane, BM / 8 - 1); };
+    // those rows of A
+    struct Sources {
+        int row[MT + 1];
+    };
+    auto sources = [&](const Tile& c) {
+        Sources r;
+#pragma unroll
+        for (int u = 0; u <= MT; ++u) {
+            const int i = c.row0 + min(copied(u), c.rows - 1);
+            r.row[u] = UP ? w.token[i] : i;
+        }
+        return r;
+    };
+    auto tile_in = [&](const Tile& c, const Sources& from) {
+        F8TileIn<MT> q;
+        q.nt = c.nt, q.row0 = c.row0, q.rows = c.rows;
         // column tiles that this wave copies and multiplies, past the last one the last one
         int copy, cols[2];
         if (UP) {
             const int g = d.I / kCols;
-            copy = (wave < 4 ? 0 : g) + min(nt * 4 + wn, g - 1);
-            cols[0] = min(nt * 4 + wn, g - 1);
+            cols[0] = min(q.nt * 4 + wn, g - 1);
             cols[1] = g + cols[0];
+            copy = cols[wave / 4];
         } else {
-            copy = min(nt * 8 + wave, ncol - 1);
-            cols[0] = min(nt * 8 + 2 * wn, ncol - 1);
-            cols[1] = min(nt * 8 + 2 * wn + 1, ncol - 1);
+            copy = min(q.nt * 8 + wave, ncol - 1);
+            cols[0] = min(q.nt * 8 + 2 * wn, ncol - 1);
+            cols[1] = min(q.nt * 8 + 2 * wn + 1, ncol - 1);
         }
-        const int nst = m.kb;
-        const uint4* B = m.codes + ((size_t)e * ncol + copy) * nst * 256;
-        const int32_t* sb[2];
+        q.B = m.codes + ((size_t)c.expert * ncol + copy) * nst * 256;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            sb[j] = reinterpret_cast<const int32_t*>(m.scales + ((size_t)e * m.nb + cols[j] / 4) * m.kbp);
-        // the rows that this lane copies: eight a copy, eight lanes a row, pieces swapped by row so that
-        // sixteen rows side by side meet sixteen different groups of banks when they are read
-        uint32_t ao[MT];
-        const uint8_t* A = UP ? in.codes : in.codes + (size_t)row0 * in.pitch;
+            q.sb[j] = reinterpret_cast<const int32_t*>(m.scales + ((size_t)c.expert * m.nb + cols[j] / 4) * m.kbp);
+        // pieces of 16 bytes are swapped by row, so that sixteen rows side by side meet sixteen different groups of
+        // banks when they are read; act is addressed from the tile's first row
+        q.A = UP ? in.codes : in.codes + (size_t)q.row0 * in.pitch;
+        q.S = UP ? in.scales : in.scales + (size_t)q.row0 * in.sp;
+        const int base = UP ? 0 : q.row0;
 #pragma unroll
         for (int u = 0; u < MT; ++u) {
-            const int r = u * 64 + wave * 8 + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
-            const uint32_t row = r >= rows ? 0u : UP ? (uint32_t)(w.pair[row0 + r] / d.K) : (uint32_t)r;
-            ao[u] = r < rows ? row * (uint32_t)in.pitch + c * 16 : kZeroOff;
+            const int r = copied(u), p = (lane & 7) ^ (r >> 1 & 7);
+            q.ao[u] = r < q.rows ? (uint32_t)(from.row[u] - base) * (uint32_t)in.pitch + p * 16 : kZeroOff;
         }
-        const uint8_t* sp;
-        {
-            const int r = row0 + min(wave * (BM / 8) + min(lane, BM / 8 - 1), rows - 1);
-            sp = in.scales + (size_t)(UP ? w.pair[r] / d.K : r) * in.sp;
-        }
-        auto copy_scales = [&](int seg) {
-            if (lane < BM / 8)
-                dma16(reinterpret_cast<const uint16_t*>(sp + seg * 16), s_to + (seg & 1) * BM * 16);
-        };
-        auto copy_part = [&](int s, int buf, int i) {    // copy i of stage s
-            const uint32_t to = buf * L::STAGE;
-            if (i < MT) dma16b(rsrc_of(A + (size_t)s * kBlk), ao[i], a_to + to + i * 8192);
-            else dma16s(reinterpret_cast<const uint16_t*>(B + (size_t)s * 256 + (i - MT) * 64), lane * 16,
-                        b_to + to + (i - MT) * 1024);
-        };
+        q.so = (uint32_t)(from.row[MT] - base) * (uint32_t)in.sp;
+        return q;
+    };
+    auto copy_scales = [&](const F8TileIn<MT>& q, int piece) {
+        if (lane < BM / 8)
+            dma16s(reinterpret_cast<const uint16_t*>(q.S + piece * 16), q.so, s_to + (piece & 1) * BM * 16);
+    };
+    auto copy_part = [&](const F8TileIn<MT>& q, int s, int buf, int i) {     // copy i of stage s
+        const uint32_t to = buf * L::STAGE;
+        if (i < MT)
+            dma16b(rsrc_of(q.A + (size_t)s * kBlk), q.ao[i], __builtin_amdgcn_readfirstlane(a_to + to + i * 8192));
+        else
+            dma16s(reinterpret_cast<const uint16_t*>(q.B + (size_t)s * 256 + (i - MT) * 64), lane * 16,
+                   __builtin_amdgcn_readfirstlane(b_to + to + (i - MT) * 1024));
+    };
+    auto copy_stage = [&](const F8TileIn<MT>& q, int s) {
+        if (s < nst)
+#pragma unroll
+            for (int i = 0; i < PER; ++i) copy_part(q, s, s, i);
+    };
+
+    int t = first + blockIdx.x / 8;
+    if (t >= end) return;
+    Tile c = tile_of(t);
+    F8TileIn<MT> q = tile_in(c, sources(c));
+    copy_scales(q, 0);
+    copy_stage(q, 0);
+    copy_stage(q, 1);
+    bool counted = false;            // whether the stores since those copies are as many as stores() says
+    while (true) {
+        if constexpr (NS == 3) copy_stage(q, 2);
+        // stage 0 is there; newer copies and the last tile's stores may be on their way
+        constexpr int newer = L::stores(UP) + (NS - 1) * PER;
+        if (counted && nst > NS) wait_vm<newer>();
+        else wait_vm<0>();
+        block_sync();
+        // what the next tile begins with is on its way during this one
+        t += gridDim.x / 8;
+        c = tile_of(min(t, end - 1));
+        const Sources next = sources(c);
 
         f32x16_t acc[MT][2];
 #pragma unroll
@@ -487,17 +623,6 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-        copy_scales(0);
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-            if (s < nst)
-#pragma unroll
-                for (int i = 0; i < PER; ++i) copy_part(s, s, i);
-        if (nst >= 3 && NS == 3) wait_vm<2 * PER>();
-        else if (nst >= 2) wait_vm<PER>();
-        else wait_vm<0>();
-        block_sync();
 
         F8Frags<MT> f0, f1;
         int sa0[MT], sa1[MT];        // scales of this stage's rows and the next one's
@@ -513,7 +638,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
             }
         };
         auto read_sa = [&](int (&sa)[MT], int s) {
-            const char* p = smem + L::SCALES + ((s >> 4) & 1) * BM * 16 + (wm * (BM / 2) + r32) * 16 + (s & 15);
+            const char* p = smem + L::SCALES_AT + ((s >> 4) & 1) * BM * 16 + (wm * (BM / 2) + r32) * 16 + (s & 15);
 #pragma unroll
             for (int i = 0; i < MT; ++i) sa[i] = *reinterpret_cast<const uint8_t*>(p + i * 512);
         };
@@ -521,43 +646,60 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
         read_b(f0, smem, 0);
 #pragma unroll
         for (int i = 0; i < MT; ++i) read_a(f0, smem, 0, i);
+        // The products so far are asked for before what follows: they have no effect that keeps their place, and
+        // moved behind a branch they hold the operands' registers.  (No instruction reads them here.)
+        auto settle = [&] {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
+        };
         // One stage: two slices of 64 input values.  After the first one every wave has read all of the
         // stage and, behind the barrier, the next stage is there for all; this stage's buffer then takes
         // stage s + NS.  A row block's operand is read where the one before has been used, so one set of
-        // registers serves.  steady: stage s + NS exists; more: stage s + 1 does.
+        // registers serves.  STEADY: stage s + NS exists; FIRST: stage 0 of those, whose next stage was asked for
+        // before the last tile's stores; MORE: stage s + 1 exists.
+        enum { LAST, MORE, STEADY, FIRST };
         int cur = 0;
-        auto stage = [&](int s, auto steady_c, auto more_c) {
-            constexpr bool steady = decltype(steady_c)::value, more = decltype(more_c)::value;
+        auto stage = [&](int s, auto kind_c) {
+            constexpr int kind = decltype(kind_c)::value;
             const char* st = smem + cur * L::STAGE;
             const int nxt = cur + 1 == NS ? 0 : cur + 1;
-            const int w0 = sload(sb[0] + (s >> 2)) >> (8 * (s & 3)) & 255, w1 = sload(sb[1] + (s >> 2)) >> (8 * (s & 3)) & 255;
+            const int w0 = sload(q.sb[0] + (s >> 2)) >> (8 * (s & 3)) & 255, w1 = sload(q.sb[1] + (s >> 2)) >> (8 * (s & 3)) & 255;
             read_b(f1, st, 1);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.a[i], f0.b[0], acc[i][0], 0, 0, 0, sa0[i], 0, w0);
-                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.a[i], f0.b[1], acc[i][1], 0, 0, 0, sa0[i], 0, w1);
+                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.b[0], f0.a[i], acc[i][0], 0, 0, 0, w0, 0, sa0[i]);
+                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.b[1], f0.a[i], acc[i][1], 0, 0, 0, w1, 0, sa0[i]);
                 __builtin_amdgcn_sched_barrier(0);
                 read_a(f1, st, 1, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
             wait_lgkm0();
-            if (NS == 3 && (steady || s + 2 < nst)) wait_vm<PER>();
-            else wait_vm<0>();
+            if constexpr (kind == FIRST) {
+                settle();
+                if (counted) wait_vm<newer - PER>();
+                else wait_vm<0>();
+            } else if constexpr (NS == 3 && kind == STEADY) {
+                wait_vm<PER>();
+            } else {
+                wait_vm<0>();
+            }
             block_sync();
-            if constexpr (more) {
+            if constexpr (kind != LAST) {
                 read_sa(sa1, s + 1);
                 read_b(f0, smem + nxt * L::STAGE, 0);
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.a[i], f1.b[0], acc[i][0], 0, 0, 0, sa0[i], 0, w0);
-                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.a[i], f1.b[1], acc[i][1], 0, 0, 0, sa0[i], 0, w1);
+                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.b[0], f1.a[i], acc[i][0], 0, 0, 0, w0, 0, sa0[i]);
+                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.b[1], f1.a[i], acc[i][1], 0, 0, 0, w1, 0, sa0[i]);
                 __builtin_amdgcn_sched_barrier(0);
-                if constexpr (more) read_a(f0, smem + nxt * L::STAGE, 0, i);
+                if constexpr (kind != LAST) read_a(f0, smem + nxt * L::STAGE, 0, i);
                 __builtin_amdgcn_sched_barrier(0);
-                if constexpr (steady) {
+                if constexpr (kind >= STEADY) {
 #pragma unroll
-                    for (int p = PER * i / MT; p < PER * (i + 1) / MT; ++p) copy_part(s + NS, cur, p);
+                    for (int p = PER * i / MT; p < PER * (i + 1) / MT; ++p) copy_part(q, s + NS, cur, p);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -566,57 +708,76 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
             cur = nxt;
         };
         int s = 0;
-        while (s + NS < nst) {       // the scales of the next 16 stages, then 16 stages: no branch among these
-            if (s + 16 < nst) copy_scales((s >> 4) + 1);
-            for (const int stop = min(nst - NS, s + 16); s < stop; ++s) stage(s, std::true_type{}, std::true_type{});
+        if (nst > NS) {
+            if (nst > 16) copy_scales(q, 1);
+            stage(s++, std::integral_constant<int, FIRST>{});
         }
-        for (; s + 1 < nst; ++s) stage(s, std::false_type{}, std::true_type{});
-        stage(s, std::false_type{}, std::false_type{});
+        while (s + NS < nst) {       // the scales of the next 16 stages, then those stages: no branch among these
+            if ((s & 15) == 0 && s + 16 < nst) copy_scales(q, (s >> 4) + 1);
+            for (const int stop = min(nst - NS, (s & ~15) + 16); s < stop; ++s) stage(s, std::integral_constant<int, STEADY>{});
+        }
+        for (; s + 1 < nst; ++s) stage(s, std::integral_constant<int, MORE>{});
+        stage(s, std::integral_constant<int, LAST>{});
+        settle();
 
+        // the next tile's first two stages are on their way while this one's results go out
+        const int nt = q.nt, row0 = q.row0, rows = q.rows;
+        counted = rows == BM && (UP || nt * 256 + 256 <= d.H);
+        if (t < end) {
+            q = tile_in(c, next);
+            copy_scales(q, 0);
+            copy_stage(q, 0);
+            copy_stage(q, 1);
+        }
+        // A column of a result is a row of the tile: lane % 32 is its row, register r its column result_row(r).
         if constexpr (UP) {
-            // act in float32 by way of LDS, so that 16 lanes get a row's block of 128 and round it
-            float* act = reinterpret_cast<float*>(smem);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    act[(wm * (BM / 2) + i * 32 + result_row(r, lane)) * L::ACT_PITCH + wn * 32 + r32] =
-                        silu_times(acc[i][0][r], acc[i][1][r]);
-            __syncthreads();
-#pragma unroll 2
-            for (int r = tid / 16; r < rows; r += 32) {
-                const int c8 = tid % 16 * 8;
-                const float4 p = *reinterpret_cast<const float4*>(act + r * L::ACT_PITCH + c8);
-                const float4 q = *reinterpret_cast<const float4*>(act + r * L::ACT_PITCH + c8 + 4);
-                float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-                if (nt * 128 + c8 >= d.I)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-                put_block(v, w.act, (size_t)row0 + r, nt, tid % 16);
-            }
-            __syncthreads();
-        } else {
-            float* ep = reinterpret_cast<float*>(smem) + wave * 32 * L::Y_PITCH;
-            const int c8 = lane % 8 * 8, col = nt * 256 + wn * 64 + c8;
+            float* tops = reinterpret_cast<float*>(smem + L::TOPS_AT);
+            const bool real = nt * 4 + wn < d.I / kCols;     // columns past the last one are zeros
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
+                uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) ep[result_row(r, lane) * L::Y_PITCH + j * 32 + r32] = acc[i][j][r];
-                wave_sync();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int rr = q * 8 + lane / 8, r = wm * (BM / 2) + i * 32 + rr;
-                    const float4 a = *reinterpret_cast<const float4*>(ep + rr * L::Y_PITCH + c8);
-                    const float4 b = *reinterpret_cast<const float4*>(ep + rr * L::Y_PITCH + c8 + 4);
-                    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                    put_y(v, w, d, (size_t)row0 + r, col, r < rows);
+                for (int r = 0; r < 16; ++r) {
+                    const float v = real ? silu_fast(acc[i][0][r], acc[i][1][r]) : 0.0f;
+                    top = max(top, __float_as_uint(v) & 0x7fffffffu);
+                    acc[i][0][r] = v;
                 }
-                wave_sync();
+                uint32_t a = top, b = top;
+                swap_halves(a, b);
+                if (half == 0) tops[wn * BM + wm * (BM / 2) + i * 32 + r32] = __uint_as_float(max(a, b));
             }
-            __syncthreads();
+            wait_lgkm0();
+            block_sync();
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int r = wm * (BM / 2) + i * 32 + r32;
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(tops[k * BM + r]));
+                const float f = to_codes(top);
+                uint32_t c[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    c[g] = four_codes(acc[i][0][4 * g], acc[i][0][4 * g + 1], acc[i][0][4 * g + 2], acc[i][0][4 * g + 3], f);
+                swap_halves(c[0], c[2]);             // the lower half's columns 0 .. 15, the upper one's 16 .. 31
+                swap_halves(c[1], c[3]);
+                const size_t row = (size_t)row0 + r;
+                if (r < rows) {
+                    *reinterpret_cast<uint4*>(w.act.codes + row * w.act.pitch + nt * 128 + wn * 32 + half * 16) =
+                        make_uint4(c[0], c[2], c[1], c[3]);
+                    if (wn == 0 && half == 0) w.act.scales[row * w.act.sp + nt] = (uint8_t)scale_byte(top);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int r = wm * (BM / 2) + i * 32;
+                put_y(acc[i], w, d, (size_t)row0 + r, nt * 256 + wn * 64, rows - r);
+            }
         }
+        if (t >= end) break;
+        wait_lgkm0();
+        block_sync();                // the third stage's place is free
     }
 }
 
@@ -639,44 +800,44 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__
     out[(size_t)t * (d.H / 4) + h] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
-// The same of float16 rows: a wave a token, a chunk of one row after another, as moonep_combine.
+// The same of float16 rows: a wave a token and VB pieces of 512 columns, which it reads of one row after another.
+// VB: 7 where there are tokens enough for all waves (8192 of H 7168 219 us), else 1 (512 of H 7168 64 us with 7).
+template <int VB>
 __global__ __launch_bounds__(256) void fp8_join16_kernel(const float* __restrict__ gates, F8Ws w, uint4* __restrict__ out,
                                                          F8Dims d) {
-    constexpr int VB = 7;
     const int tok = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, vecs = d.H / 8;
     if (tok >= d.T) return;
     const int32_t* dest = w.dest + (size_t)tok * d.K;
-    for (int v0 = 0; v0 < vecs; v0 += 64 * VB) {
-        float acc[VB][8] = {};
+    const int v0 = blockIdx.y * 64 * VB;
+    float acc[VB][8] = {};
 #pragma unroll 1
-        for (int k = 0; k < d.K; ++k) {
-            const int row = dest[k];
-            if (row < 0) continue;
-            const float g = gates[(size_t)tok * d.K + k];
-            const uint4* y = reinterpret_cast<const uint4*>(w.y16) + (size_t)row * vecs;
-            const uint8_t* ex = w.y16_exp + (size_t)row * w.y16_sp;
-#pragma unroll
-            for (int u = 0; u < VB; ++u) {
-                const int v = v0 + u * 64 + lane;
-                if (v >= vecs) continue;
-                union {
-                    uint4 u;
-                    _Float16 h[8];
-                } r;
-                r.u = ld_nt(y + v);
-                const float s = __uint_as_float((uint32_t)(ex[v / 8] - 14) << 23);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[u][i] += g * ((float)r.h[i] * s);
-            }
-        }
+    for (int k = 0; k < d.K; ++k) {
+        const int row = dest[k];
+        if (row < 0) continue;
+        const float g = gates[(size_t)tok * d.K + k];
+        const uint4* y = reinterpret_cast<const uint4*>(w.y16) + (size_t)row * vecs;
+        const uint8_t* ex = w.y16_exp + (size_t)row * w.y16_sp;
 #pragma unroll
         for (int u = 0; u < VB; ++u) {
             const int v = v0 + u * 64 + lane;
-            if (v < vecs)
-                st_nt(make_uint4(pack_bf16(acc[u][0], acc[u][1]), pack_bf16(acc[u][2], acc[u][3]),
-                                 pack_bf16(acc[u][4], acc[u][5]), pack_bf16(acc[u][6], acc[u][7])),
-                      out + (size_t)tok * vecs + v);
+            if (v >= vecs) continue;
+            union {
+                uint4 u;
+                _Float16 h[8];
+            } r;
+            r.u = ld_nt(y + v);
+            const float s = __uint_as_float((uint32_t)(ex[v / 8] - 14) << 23);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[u][i] += g * ((float)r.h[i] * s);
         }
+    }
+#pragma unroll
+    for (int u = 0; u < VB; ++u) {
+        const int v = v0 + u * 64 + lane;
+        if (v < vecs)
+            st_nt(make_uint4(pack_bf16(acc[u][0], acc[u][1]), pack_bf16(acc[u][2], acc[u][3]),
+                             pack_bf16(acc[u][4], acc[u][5]), pack_bf16(acc[u][6], acc[u][7])),
+                  out + (size_t)tok * vecs + v);
     }
 }
 
@@ -788,15 +949,21 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     a.topk = topk, a.hist = w.hist, a.offsets = w.offsets, a.dest = w.dest, a.pair = w.pair;
     a.run_rows = w.run_rows, a.runs = w.runs, a.nruns = w.nruns;
     if (launch_sort(a, s) != MOONEP_OK) return MOONEP_EHIP;
-    hipLaunchKernelGGL(fp8_rows_kernel, dim3(d.T, (up.kb + 15) / 16), dim3(256), 0, s, static_cast<const uint16_t*>(x), w.x,
-                       d.H, up.kb);
+    const size_t listed = w.run_rows == kThinRows
+                              ? 0 : std::max(pairs, (size_t)w.max_runs * (up_columns(d) + down_columns(d)));
+    hipLaunchKernelGGL(fp8_rows_kernel, dim3(d.T + (unsigned)((listed + 255) / 256), (up.kb + 15) / 16), dim3(256), 0, s,
+                       static_cast<const uint16_t*>(x), w, d, up.kb);
     MOONEP_LAUNCH_CHECK();
     if (w.run_rows != kThinRows) {
         const int rc2 = w.run_rows == 64 ? launch_both<64>(up, down, w, d, s)
                         : w.run_rows == 128 ? launch_both<128>(up, down, w, d, s)
                                             : launch_both<256>(up, down, w, d, s);
         if (rc2 != MOONEP_OK) return rc2;
-        hipLaunchKernelGGL(fp8_join16_kernel, dim3((d.T + 3) / 4), dim3(256), 0, s, gates, w, static_cast<uint4*>(out), d);
+        uint4* o = static_cast<uint4*>(out);
+        if (d.T >= 4096)
+            hipLaunchKernelGGL(fp8_join16_kernel<7>, dim3((d.T + 3) / 4, (d.H / 8 + 447) / 448), dim3(256), 0, s, gates, w, o, d);
+        else
+            hipLaunchKernelGGL(fp8_join16_kernel<1>, dim3((d.T + 3) / 4, (d.H / 8 + 63) / 64), dim3(256), 0, s, gates, w, o, d);
         MOONEP_LAUNCH_CHECK();
         return MOONEP_OK;
     }
