@@ -234,4 +234,25 @@ __device__ __forceinline__ T wave_sum(T v) {
     return v;
 }
 
+constexpr int kFewPairs = 64;        // (token, k) pairs whose ids one wave can look at together
+
+// The wave's number, known to be the same for all its lanes: what follows from it stays in scalar registers.
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// A wave's view of all pairs: the expert of pair `lane`, -1 for none.
+__device__ __forceinline__ int pair_expert(const int32_t* topk, int pairs, int E) {
+    const int lane = threadIdx.x & 63;
+    const int id = lane < pairs ? topk[lane] : -1;
+    return (unsigned)id < (unsigned)E ? id : -1;
+}
+
+// Lane r's pair of the r-th member of `members`, r < popcount.
+__device__ __forceinline__ int member_pair(unsigned long long members) {
+    const int lane = threadIdx.x & 63;
+    const unsigned long long below = (1ull << lane) - 1;
+    const int n = __popcll(members);
+    const int to = (members >> lane) & 1 ? __popcll(members & below) : n + __popcll(~members & below);
+    return __builtin_amdgcn_ds_permute(to * 4, lane);
+}
+
 }  // namespace moonep

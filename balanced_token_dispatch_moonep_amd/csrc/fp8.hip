@@ -51,8 +51,7 @@ struct F8Ws {
     int32_t* token;                  // [P]: of each row
     int max_runs, run_rows;
     F8Rows x, act;                   // [T], [P]
-    float* y;                        // [P][H], with few rows
-    uint16_t* y16;                   // [P][H], with many: float16 times
+    uint16_t* y16;                   // [P][H]: float16 times
     uint8_t* y16_exp;                // [P][H/64] a power of two for each 64
     int y16_sp;
 };
@@ -63,13 +62,16 @@ __host__ __device__ static constexpr int blks(int n) { return (n + kBlk - 1) / k
 __host__ __device__ static constexpr int up_columns(const F8Dims& d) { return (d.I + 127) / 128; }
 __host__ __device__ static constexpr int down_columns(const F8Dims& d) { return (d.H + 255) / 256; }
 
-constexpr int kThinRows = 32;        // rows of a run, where few rows are multiplied at a time
-constexpr int kThinEach = 48;        // pairs an expert, below which that is done
+// Whether two launches for few pairs take a call: 8 tokens of up to 64 pairs, whose rounded rows fit LDS.
+constexpr int kFewRows = 8, kFewPitch = 8192;
+static bool f8_few(const F8Dims& d) {
+    return d.T <= kFewRows && d.T * d.K <= kFewPairs && blks(d.H) * kBlk <= kFewPitch;
+}
 
-// Rows of a run, and of a tile: by the pairs that an expert has on average.
+// Rows of a tile otherwise: by the pairs that an expert has on average.
 static int f8_rows(const F8Dims& d) {
     const int64_t pairs = (int64_t)d.T * d.K;
-    return pairs < (int64_t)kThinEach * d.E ? kThinRows : pairs < 192ll * d.E ? 128 : 256;
+    return pairs < 48ll * d.E ? 64 : pairs < 192ll * d.E ? 128 : 256;
 }
 
 static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
@@ -89,27 +91,26 @@ static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
         r.scales = take(n * r.sp);
         return r;
     };
-    w.run_rows = f8_rows(d);
     // the same parts for every way of a call, so that the scratch of a larger call serves smaller ones
-    w.max_runs = (int)(experts + pairs / w.run_rows);
-    w.hist = (int32_t*)take(pairs > kSortOnce ? std::min<size_t>((pairs + 4095) / 4096, kSortParts) * d.E * 4 : 0);
-    w.offsets = (int32_t*)take((size_t)(d.E + 1) * 4);
-    w.dest = (int32_t*)take(pairs * 4);
-    w.pair = (int32_t*)take(pairs * 4);
-    w.nruns = (int32_t*)take(4);
-    w.runs = (Run*)take((experts + pairs / kThinRows) * sizeof(Run));
-    const size_t most = experts + pairs / 128;   // runs, where there are tiles
-    w.up_tiles = (Tile*)take(most * up_columns(d) * sizeof(Tile));
-    w.down_tiles = (Tile*)take(most * down_columns(d) * sizeof(Tile));
-    w.token = (int32_t*)take(pairs * 4);
-    w.x = rows(d.T, d.H);
+    w.run_rows = f8_rows(d);
     w.act = rows(pairs, d.I);
-    w.y16_sp = (d.H + 63) / 64;
-    const size_t thin = std::min<size_t>(pairs, (size_t)kThinEach * d.E) * d.H * 4, y16 = align_up(pairs * d.H * 2, 256);
-    uint8_t* y = take(std::max(thin, y16 + pairs * w.y16_sp));
-    w.y = (float*)y;
-    w.y16 = (uint16_t*)y;
-    w.y16_exp = y + y16;
+    if (!f8_few(d)) {
+        const size_t most = experts + pairs / 64;        // runs
+        w.max_runs = (int)(experts + pairs / w.run_rows);
+        w.hist = (int32_t*)take(pairs > kSortOnce ? std::min<size_t>((pairs + 4095) / 4096, kSortParts) * d.E * 4 : 0);
+        w.offsets = (int32_t*)take((size_t)(d.E + 1) * 4);
+        w.dest = (int32_t*)take(pairs * 4);
+        w.pair = (int32_t*)take(pairs * 4);
+        w.token = (int32_t*)take(pairs * 4);
+        w.nruns = (int32_t*)take(4);
+        w.runs = (Run*)take(most * sizeof(Run));
+        w.up_tiles = (Tile*)take(most * up_columns(d) * sizeof(Tile));
+        w.down_tiles = (Tile*)take(most * down_columns(d) * sizeof(Tile));
+        w.x = rows(d.T, d.H);
+        w.y16_sp = (d.H + 63) / 64;
+        w.y16 = (uint16_t*)take(pairs * d.H * 2);
+        w.y16_exp = take(pairs * w.y16_sp);
+    }
     if (ws) *ws = w;
     return off;
 }
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t* __res
 }
 
 // ---------------------------------------------------------------------------
-// products of few rows
+// few pairs
 // ---------------------------------------------------------------------------
 
 // Eight codes times their scale as bf16: exact (down to 2^-133).
@@ -255,21 +256,24 @@ __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi, float scale)
     r.two[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
     return r.all;
 }
+__device__ __forceinline__ float scale_of(int byte) { return __uint_as_float((uint32_t)byte << 23); }
 // The row of a 32 x 32 result that a lane's register r holds; the column is lane % 32.
 __device__ __forceinline__ int result_row(int r, int lane) { return r / 4 * 8 + (lane >> 5) * 4 + r % 4; }
 
 // acc = 32 rows times NT column tiles, over blocks first, first + step, ... of the input direction.
 // A lane holds row lane % 32 and, of each 32 input values, the 16 of its half of the wave; so does it of
-// the columns, whose layout makes a wave's load one KiB in a row.  D blocks are on their way while one is
-// multiplied; past the last one they are asked for again instead of branching around the load.
+// the columns, whose layout makes a wave's load one KiB in a row.  D blocks of weights are on their way while one is
+// multiplied; past the last one they are asked for again instead of branching around the load.  start() runs
+// after the first of them have been asked for; rows(k, p) and row_scale(k) give piece p and the scale of block k,
+// from LDS or, with AHEAD, from memory, when they are asked for with the weights: loads return in order.
 // The codes are widened to bf16: the 8-bit matrix instructions keep a sum of products to about 16 bits only
 // (measured: relative error 1.3e-5, with 32x32x64, 16x16x128 and 32x32x16 alike), which moves values of act over
 // the border between two codes; with bf16 operands it is exact to float32.  Half the rate costs nothing where
 // reading the weights is what takes the time.
-template <int NT, int D>
-__device__ __forceinline__ void multiply_thin(f32x16_t (&acc)[NT], const F8Mat& m, const size_t* tile,
-                                              const uint8_t* const* scale, const uint8_t* row, const uint8_t* row_scale,
-                                              int first, int step) {
+template <int NT, int D, bool AHEAD, class Start, class Rows, class Scale>
+__device__ __forceinline__ void multiply_few(f32x16_t (&acc)[NT], const F8Mat& m, const size_t* tile,
+                                             const uint8_t* const* scale, int first, int step, Start start, Rows rows,
+                                             Scale row_scale) {
     const int lane = threadIdx.x & 63;
     const int n = first < m.kb ? (m.kb - first + step - 1) / step : 0;
     uint4 a[D][4], b[D][NT][4];
@@ -281,13 +285,14 @@ __device__ __forceinline__ void multiply_thin(f32x16_t (&acc)[NT], const F8Mat& 
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][i] = 0.0f;
     }
-    if (n == 0) return;
-    const uint8_t* half = row + (lane >> 5) * 16;
+    auto block = [&](int s) { return first + max(min(s, n - 1), 0) * step; };
     auto load = [&](int j, int s) {
-        const int k = first + min(s, n - 1) * step;
-        sa[j] = row_scale[k];
+        const int k = min(block(s), m.kb - 1);
+        if constexpr (AHEAD) {
+            sa[j] = row_scale(k);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) a[j][p] = *reinterpret_cast<const uint4*>(half + (size_t)k * kBlk + p * 32);
+            for (int p = 0; p < 4; ++p) a[j][p] = rows(k, p);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             sb[j][t] = scale[t][k];
@@ -297,17 +302,20 @@ __device__ __forceinline__ void multiply_thin(f32x16_t (&acc)[NT], const F8Mat& 
     };
 #pragma unroll
     for (int j = 0; j < D; ++j) load(j, j);
+    start();
     for (int s = 0; s < n; s += D) {
 #pragma unroll
         for (int j = 0; j < D; ++j) {
             if (s + j < n) {
-                const float fa = __uint_as_float((uint32_t)sa[j] << 23);
+                const int k = block(s + j);
+                const float fa = scale_of(AHEAD ? sa[j] : row_scale(k));
                 float fb[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) fb[t] = __uint_as_float((uint32_t)sb[j][t] << 23);
+                for (int t = 0; t < NT; ++t) fb[t] = scale_of(sb[j][t]);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const bf16x8_t a0 = widen(a[j][p].x, a[j][p].y, fa), a1 = widen(a[j][p].z, a[j][p].w, fa);
+                    const uint4 r = AHEAD ? a[j][p] : rows(k, p);
+                    const bf16x8_t a0 = widen(r.x, r.y, fa), a1 = widen(r.z, r.w, fa);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const uint4 c = b[j][t][p];
@@ -323,70 +331,129 @@ __device__ __forceinline__ void multiply_thin(f32x16_t (&acc)[NT], const F8Mat& 
 
 __device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// act = q(silu(q(x) G) * (q(x) U)) of one expert's pairs and 128 columns: a block of act, which the workgroup rounds
+// itself.  Four pairs of tiles, their input direction dealt out to SPLIT waves each, which join their sums in order.
+// blockIdx.y: a pair, that leads its expert's group if it is the first of it, or an expert where there are
+// fewer experts than pairs.  The workgroup rounds the rows of x itself, while the first weights arrive.
+template <int SPLIT, int D>
+__global__ __launch_bounds__(256 * SPLIT) void fp8_few_up_kernel(const int32_t* __restrict__ topk,
+                                                                 const uint16_t* __restrict__ x, F8Mat m, F8Rows act,
+                                                                 F8Dims d) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int pairs = d.T * d.K, tid = threadIdx.x, lane = tid & 63, wave = wave_of();
+    const int id = pair_expert(topk, pairs, d.E);
+    const int e = pairs <= d.E ? __builtin_amdgcn_readlane(id, blockIdx.y) : blockIdx.y;
+    const unsigned long long members = __ballot(id == e);
+    if (e < 0 || members == 0) return;
+    if (pairs <= d.E && __ffsll(members) - 1 != (int)blockIdx.y) return;
+    const int n = __popcll(members), pair = member_pair(members), block = blockIdx.x;
+    const int gate = min(block * 4 + wave / SPLIT, d.I / kCols - 1), up = d.I / kCols + gate;
+    const size_t tiles = (size_t)e * (m.n / kCols), tile[2] = {tiles + gate, tiles + up};
+    const uint8_t* scales = m.scales + (size_t)e * m.nb * m.kbp;
+    const uint8_t* scale[2] = {scales + (size_t)(gate / 4) * m.kbp, scales + (size_t)(up / 4) * m.kbp};
+    // rows of x in LDS, 16 bytes apart from multiples of 128 so that eight rows meet eight groups of banks;
+    // the waves' sums take their place
+    const int pitch = m.kb * kBlk + 16;
+    uint8_t* rows = reinterpret_cast<uint8_t*>(smem);
+    uint8_t* row_scales = rows + kFewRows * pitch;
+    float(*part)[2][4][64] = reinterpret_cast<float(*)[2][4][64]>(smem);
+    for (int r0 = 0; r0 < n; r0 += kFewRows) {
+        const int count = min(kFewRows, n - r0), mine = min(lane & 31, count - 1);
+        __syncthreads();
+        f32x16_t acc[2];
+        multiply_few<2, D, false>(
+            acc, m, tile, scale, wave % SPLIT, SPLIT,
+            [&] {
+                // 16 lanes a block
+                for (int i0 = 0; i0 < count * m.kb; i0 += 16 * SPLIT) {
+                    const int i = i0 + tid / 16, r = min(i / m.kb, count - 1), b = i % m.kb, k = b * kBlk + tid % 16 * 8;
+                    const size_t token = __shfl(pair, r0 + r, 64) / d.K;
+                    if (i >= count * m.kb) continue;
+                    const uint4 u = k < d.H ? *reinterpret_cast<const uint4*>(x + token * d.H + k) : make_uint4(0, 0, 0, 0);
+                    const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
+                                        bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+                    put_block(v, F8Rows{rows, row_scales, pitch, m.kb}, r, b, tid % 16);
+                }
+                wait_lgkm0();
+                block_sync();
+            },
+            [&](int k, int p) {
+                return *reinterpret_cast<const uint4*>(rows + mine * pitch + k * kBlk + p * 32 + (lane >> 5) * 16);
+            },
+            [&](int k) { return (int)row_scales[mine * m.kb + k]; });
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) part[wave][t][r][lane] = acc[t][r];      // rows 0 .. 7
+        __syncthreads();
+        // 16 lanes a row, eight columns each
+        const int i = tid / 16;
+        const size_t to = __shfl(pair, min(r0 + i, n - 1), 64);
+        if (i < count) {
+            const int c8 = tid % 16 * 8, t = c8 / kCols, l = i / 4 * 32 + c8 % kCols;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float g = 0.0f, u = 0.0f;
+#pragma unroll
+                for (int s = 0; s < SPLIT; ++s) {
+                    g += part[t * SPLIT + s][0][i % 4][l + j];
+                    u += part[t * SPLIT + s][1][i % 4][l + j];
+                }
+                v[j] = block * kBlk + c8 < d.I ? silu_times(g, u) : 0.0f;
+            }
+            put_block(v, act, to, block, tid % 16);
+        }
+    }
+}
+
+// out for 32 columns and all tokens: the waves take the experts in turn, and a token's pairs are joined in k order.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void fp8_few_down_kernel(const int32_t* __restrict__ topk,
+                                                                  const float* __restrict__ gates, F8Mat m, F8Rows act,
+                                                                  uint16_t* __restrict__ out, F8Dims d) {
+    __shared__ float y[kFewPairs][kCols];
+    const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), col = blockIdx.x;
+    const int id = pair_expert(topk, pairs, d.E);
+    unsigned long long left = __ballot(id >= 0);
+    for (int turn = 0; left; ++turn) {
+        const int e = __builtin_amdgcn_readlane(id, __ffsll(left) - 1);
+        const unsigned long long members = __ballot(id == e);
+        left &= ~members;
+        if (turn % WAVES != wave) continue;
+        const int n = __popcll(members), pair = member_pair(members);
+        const size_t tile[1] = {(size_t)e * (m.n / kCols) + col};
+        const uint8_t* scale[1] = {m.scales + ((size_t)e * m.nb + col / 4) * m.kbp};
+        for (int r0 = 0; r0 < n; r0 += 32) {
+            const size_t row = __shfl(pair, min(r0 + (lane & 31), n - 1), 64);
+            const uint8_t *codes = act.codes + row * act.pitch + (lane >> 5) * 16, *scales = act.scales + row * act.sp;
+            f32x16_t acc[1];
+            multiply_few<1, 4, true>(
+                acc, m, tile, scale, 0, 1, [] {},
+                [&](int k, int p) { return *reinterpret_cast<const uint4*>(codes + (size_t)k * kBlk + p * 32); },
+                [&](int k) { return (int)scales[k]; });
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int i = r0 + result_row(r, lane), p = __shfl(pair, min(i, n - 1), 64);
+                if (i < n) y[p][lane & 31] = acc[0][r];
+            }
+        }
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < d.T * kCols; v += 64 * WAVES) {
+        const int t = v / kCols, c = v % kCols;
+        float s = 0.0f;
+        for (int p = t * d.K; p < (t + 1) * d.K; ++p)
+            if ((unsigned)topk[p] < (unsigned)d.E) s += gates[p] * y[p][c];
+        out[(size_t)t * d.H + col * kCols + c] = (uint16_t)pack_bf16(s, 0.0f);
+    }
+}
+
 // The same with the hardware's exponential and reciprocal: off by some 2^-22, far below what the 8-bit products
 // before it are off by.
 __device__ __forceinline__ float silu_fast(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
-// act = q(silu(x G) * (x U)) of a run's rows and 128 columns: a block of act, which the workgroup rounds
-// itself.  Four pairs of tiles, their input direction dealt out to SPLIT waves each.
-template <int SPLIT>
-__global__ __launch_bounds__(256 * SPLIT) void fp8_thin_up_kernel(F8Mat m, F8Ws w, F8Dims d) {
-    __shared__ float part[4 * SPLIT][2][16][64];
-    const int groups = blks(d.I), r = blockIdx.x / groups, block = blockIdx.x % groups;
-    if (r >= w.nruns[0]) return;
-    const Run run = w.runs[r];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = block * 4 + wave / SPLIT, last = d.I / kCols - 1, gate = min(col, last);
-    const size_t tiles = (size_t)run.expert * (m.n / kCols), tile[2] = {tiles + gate, tiles + d.I / kCols + gate};
-    const uint8_t* scales = m.scales + (size_t)run.expert * m.nb * m.kbp;
-    const uint8_t* scale[2] = {scales + (size_t)(gate / 4) * m.kbp, scales + (size_t)((d.I / kCols + gate) / 4) * m.kbp};
-    const size_t token = w.pair[run.first + min(lane & 31, run.n - 1)] / d.K;
-    f32x16_t acc[2];
-    multiply_thin<2, 3>(acc, m, tile, scale, w.x.codes + token * w.x.pitch, w.x.scales + token * w.x.sp, wave % SPLIT,
-                        SPLIT);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) part[wave][t][r][lane] = acc[t][r];
-    __syncthreads();
-    // 16 lanes a row, eight columns each
-    for (int i = tid / 16; i < run.n; i += 16 * SPLIT) {
-        const int c8 = tid % 16 * 8, t = c8 / kCols, r = i / 8 * 4 + i % 4, l = i / 4 % 2 * 32 + c8 % kCols;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float g = 0.0f, u = 0.0f;
-#pragma unroll
-            for (int s = 0; s < SPLIT; ++s) {
-                g += part[t * SPLIT + s][0][r][l + j];
-                u += part[t * SPLIT + s][1][r][l + j];
-            }
-            v[j] = block * kBlk + c8 < d.I ? silu_times(g, u) : 0.0f;
-        }
-        put_block(v, w.act, run.first + i, block, tid % 16);
-    }
-}
-
-// y of a run's rows; a wave takes 32 columns.
-__global__ __launch_bounds__(256) void fp8_thin_down_kernel(F8Mat m, F8Ws w, F8Dims d) {
-    const int groups = blks(d.H), r = blockIdx.x / groups;
-    if (r >= w.nruns[0]) return;
-    const Run run = w.runs[r];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = blockIdx.x % groups * 4 + wave;
-    if (col >= d.H / kCols) return;
-    const size_t tile[1] = {(size_t)run.expert * (m.n / kCols) + col};
-    const uint8_t* scale[1] = {m.scales + ((size_t)run.expert * m.nb + col / 4) * m.kbp};
-    const size_t row = run.first + min(lane & 31, run.n - 1);
-    f32x16_t acc[1];
-    multiply_thin<1, 4>(acc, m, tile, scale, w.act.codes + row * w.act.pitch, w.act.scales + row * w.act.sp, 0, 1);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int i = result_row(r, lane);
-        if (i < run.n) w.y[(size_t)(run.first + i) * d.H + col * kCols + (lane & 31)] = acc[0][r];
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -427,8 +494,8 @@ __device__ __forceinline__ float max_halves(float v) {
 }
 
 // The 64 columns of y that a wave has of 32 rows, of which `valid` are there: float16 with one power of two that brings the largest of
-// them to 2^14 .. 2^15, half the bytes of float32 and off by 2^-12 (bf16 would be by 2^-9, as much as the
-// output's own rounding).  The stored byte is the largest one's exponent field; infinities and NaN, which
+// them to 2^14 .. 2^15, half the bytes of float32 and off by at most 2^-11 (bf16 would be by 2^-8, as much as
+// the output's own rounding).  The stored byte is the largest one's exponent field; infinities and NaN, which
 // have none, stay what they are.  A lane has 16 columns of each tile of one row, in fours, and the lane in the
 // other half of the wave the fours between: two of them make 16 bytes.
 __device__ __forceinline__ void put_y(const f32x16_t (&v)[2], const F8Ws& w, const F8Dims& d, size_t row0, int col,
@@ -648,6 +715,18 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
         for (int i = 0; i < MT; ++i) read_a(f0, smem, 0, i);
         // The products so far are asked for before what follows: they have no effect that keeps their place, and
         // moved behind a branch they hold the operands' registers.  (No instruction reads them here.)
+        // acc += rows times one column tile, one slice.  Tiles of 64 rows, which few rows an expert fill, take the time that
+        // reading their weights takes, and widen their operands as multiply_few does.
+        auto product = [&](f32x16_t& sum, const i32x8_t& a, const i32x8_t& b, int sa, int sb) {
+            if constexpr (BM == 64) {
+#pragma unroll
+                for (int h = 0; h < 8; h += 2)
+                    sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b[h], b[h + 1], scale_of(sb)),
+                                                                  widen(a[h], a[h + 1], scale_of(sa)), sum, 0, 0, 0);
+            } else {
+                sum = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, sum, 0, 0, 0, sb, 0, sa);
+            }
+        };
         auto settle = [&] {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
@@ -669,8 +748,8 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
             read_b(f1, st, 1);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.b[0], f0.a[i], acc[i][0], 0, 0, 0, w0, 0, sa0[i]);
-                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0.b[1], f0.a[i], acc[i][1], 0, 0, 0, w1, 0, sa0[i]);
+                product(acc[i][0], f0.a[i], f0.b[0], sa0[i], w0);
+                product(acc[i][1], f0.a[i], f0.b[1], sa0[i], w1);
                 __builtin_amdgcn_sched_barrier(0);
                 read_a(f1, st, 1, i);
                 __builtin_amdgcn_sched_barrier(0);
@@ -692,8 +771,8 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                acc[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.b[0], f1.a[i], acc[i][0], 0, 0, 0, w0, 0, sa0[i]);
-                acc[i][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1.b[1], f1.a[i], acc[i][1], 0, 0, 0, w1, 0, sa0[i]);
+                product(acc[i][0], f1.a[i], f1.b[0], sa0[i], w0);
+                product(acc[i][1], f1.a[i], f1.b[1], sa0[i], w1);
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (kind != LAST) read_a(f0, smem + nxt * L::STAGE, 0, i);
                 __builtin_amdgcn_sched_barrier(0);
@@ -738,7 +817,8 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
                 uint32_t top = 0;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const float v = real ? silu_fast(acc[i][0][r], acc[i][1][r]) : 0.0f;
+                    const float g = acc[i][0][r], u = acc[i][1][r];
+                    const float v = !real ? 0.0f : BM == 64 ? silu_times(g, u) : silu_fast(g, u);
                     top = max(top, __float_as_uint(v) & 0x7fffffffu);
                     acc[i][0][r] = v;
                 }
@@ -781,29 +861,10 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
     }
 }
 
-// out = sum over k of gate * y, in k order, skipping ids that name no expert.
-__global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ gates, F8Ws w, uint2* __restrict__ out,
-                                                       F8Dims d) {
-    const int h = blockIdx.y * 256 + threadIdx.x, t = blockIdx.x;
-    if (h >= d.H / 4) return;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int p = t * d.K; p < (t + 1) * d.K; ++p) {
-        const int row = w.dest[p];
-        if (row < 0) continue;
-        const float4 v = reinterpret_cast<const float4*>(w.y)[(size_t)row * (d.H / 4) + h];
-        const float g = gates[p];
-        s.x += g * v.x;
-        s.y += g * v.y;
-        s.z += g * v.z;
-        s.w += g * v.w;
-    }
-    out[(size_t)t * (d.H / 4) + h] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-}
-
-// The same of float16 rows: a wave a token and VB pieces of 512 columns, which it reads of one row after another.
+// out = sum over k of gate * y, in k order, skipping pairs without a row; a wave a token and VB pieces of 512 columns, which it reads of one row after another.
 // VB: 7 where there are tokens enough for all waves (8192 of H 7168 219 us), else 1 (512 of H 7168 64 us with 7).
 template <int VB>
-__global__ __launch_bounds__(256) void fp8_join16_kernel(const float* __restrict__ gates, F8Ws w, uint4* __restrict__ out,
+__global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ gates, F8Ws w, uint4* __restrict__ out,
                                                          F8Dims d) {
     const int tok = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, vecs = d.H / 8;
     if (tok >= d.T) return;
@@ -945,34 +1006,38 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     if (outputs_overlap(spans, 2, 9)) return MOONEP_EINVAL;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const F8Mat up = f8_mat(w13_codes, w13_scales, d.H, 2 * d.I), down = f8_mat(w2_codes, w2_scales, d.I, d.H);
+    if (f8_few(d)) {
+        constexpr int split = 2;
+        const int smem = std::max(kFewRows * (up.kb * kBlk + 16 + up.kb), 4 * split * 2 * 4 * 64 * 4);
+        const auto kernel = fp8_few_up_kernel<split, 3>;
+        if (hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            hipSuccess)
+            return MOONEP_EHIP;
+        hipLaunchKernelGGL(kernel, dim3(blks(d.I), std::min(d.T * d.K, d.E)), dim3(256 * split), smem, s, topk,
+                           static_cast<const uint16_t*>(x), up, w.act, d);
+        MOONEP_LAUNCH_CHECK();
+        hipLaunchKernelGGL(fp8_few_down_kernel<8>, dim3(d.H / kCols), dim3(512), 0, s, topk, gates, down, w.act,
+                           static_cast<uint16_t*>(out), d);
+        MOONEP_LAUNCH_CHECK();
+        return MOONEP_OK;
+    }
     SortArgs a = sort_args((int)pairs, d.E);
     a.topk = topk, a.hist = w.hist, a.offsets = w.offsets, a.dest = w.dest, a.pair = w.pair;
     a.run_rows = w.run_rows, a.runs = w.runs, a.nruns = w.nruns;
     if (launch_sort(a, s) != MOONEP_OK) return MOONEP_EHIP;
-    const size_t listed = w.run_rows == kThinRows
-                              ? 0 : std::max(pairs, (size_t)w.max_runs * (up_columns(d) + down_columns(d)));
+    const size_t listed = std::max(pairs, (size_t)w.max_runs * (up_columns(d) + down_columns(d)));
     hipLaunchKernelGGL(fp8_rows_kernel, dim3(d.T + (unsigned)((listed + 255) / 256), (up.kb + 15) / 16), dim3(256), 0, s,
                        static_cast<const uint16_t*>(x), w, d, up.kb);
     MOONEP_LAUNCH_CHECK();
-    if (w.run_rows != kThinRows) {
-        const int rc2 = w.run_rows == 64 ? launch_both<64>(up, down, w, d, s)
-                        : w.run_rows == 128 ? launch_both<128>(up, down, w, d, s)
-                                            : launch_both<256>(up, down, w, d, s);
-        if (rc2 != MOONEP_OK) return rc2;
-        uint4* o = static_cast<uint4*>(out);
-        if (d.T >= 4096)
-            hipLaunchKernelGGL(fp8_join16_kernel<7>, dim3((d.T + 3) / 4, (d.H / 8 + 447) / 448), dim3(256), 0, s, gates, w, o, d);
-        else
-            hipLaunchKernelGGL(fp8_join16_kernel<1>, dim3((d.T + 3) / 4, (d.H / 8 + 63) / 64), dim3(256), 0, s, gates, w, o, d);
-        MOONEP_LAUNCH_CHECK();
-        return MOONEP_OK;
-    }
-    hipLaunchKernelGGL(fp8_thin_up_kernel<2>, dim3(blks(d.I) * w.max_runs), dim3(512), 0, s, up, w, d);
-    MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(fp8_thin_down_kernel, dim3(blks(d.H) * w.max_runs), dim3(256), 0, s, down, w, d);
-    MOONEP_LAUNCH_CHECK();
-    hipLaunchKernelGGL(fp8_join_kernel, dim3(d.T, (d.H / 4 + 255) / 256), dim3(256), 0, s, gates, w,
-                       static_cast<uint2*>(out), d);
+    const int rc2 = w.run_rows == 64 ? launch_both<64>(up, down, w, d, s)
+                    : w.run_rows == 128 ? launch_both<128>(up, down, w, d, s)
+                                        : launch_both<256>(up, down, w, d, s);
+    if (rc2 != MOONEP_OK) return rc2;
+    uint4* o = static_cast<uint4*>(out);
+    if (d.T >= 4096)
+        hipLaunchKernelGGL(fp8_join_kernel<7>, dim3((d.T + 3) / 4, (d.H / 8 + 447) / 448), dim3(256), 0, s, gates, w, o, d);
+    else
+        hipLaunchKernelGGL(fp8_join_kernel<1>, dim3((d.T + 3) / 4, (d.H / 8 + 63) / 64), dim3(256), 0, s, gates, w, o, d);
     MOONEP_LAUNCH_CHECK();
     return MOONEP_OK;
 }

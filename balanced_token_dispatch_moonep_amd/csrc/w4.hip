@@ -46,7 +46,6 @@ constexpr int kGroup = 32;           // values a scale
 constexpr int kBlock = 128;          // input values of one wave's load
 constexpr int kFour = 4 * kBlock;    // input values of four blocks, whose scales come in one load
 constexpr int kTile = 16;            // rows a matrix instruction takes, columns of a tile
-constexpr int kFewPairs = 64;        // one wave can look at all their ids
 constexpr int kCUs = 256;
 
 struct W4Dims {
@@ -131,9 +130,6 @@ static size_t w4_ws_layout(const W4Dims& d, void* base, W4Ws* ws) {
     return off;
 }
 
-// The wave's number, known to be the same for all its lanes: what follows from it stays in scalar registers.
-__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
-
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
@@ -211,22 +207,6 @@ __device__ __forceinline__ void two_terms(float a, uint16_t& lead, uint16_t& res
 // ---------------------------------------------------------------------------
 // few pairs
 // ---------------------------------------------------------------------------
-
-// A wave's view of all pairs: the expert of pair `lane`, -1 for none.
-__device__ __forceinline__ int pair_expert(const int32_t* topk, int pairs, int E) {
-    const int lane = threadIdx.x & 63;
-    const int id = lane < pairs ? topk[lane] : -1;
-    return (unsigned)id < (unsigned)E ? id : -1;
-}
-
-// Lane r's pair of the r-th member of `members`, r < popcount.
-__device__ __forceinline__ int member_pair(unsigned long long members) {
-    const int lane = threadIdx.x & 63;
-    const unsigned long long below = (1ull << lane) - 1;
-    const int n = __popcll(members);
-    const int to = (members >> lane) & 1 ? __popcll(members & below) : n + __popcll(~members & below);
-    return __builtin_amdgcn_ds_permute(to * 4, lane);
-}
 
 // acc = up to eight rows times NT column tiles, over fours first, first + step, ...  The wave keeps
 // RN rows of four blocks in `lds` (RN KiB of its own), 16-byte pieces swapped by row so that equal

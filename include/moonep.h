@@ -425,8 +425,8 @@ int moonep_quantize_fp8(int32_t E, int32_t Kin, int32_t N, const void* w, void* 
  *   out[r,s] = sum over k (in k order) of gates[r,s,k] * (q(silu(q(x) G) * (q(x) U)) D)  of expert topk[r,s,k],
  * G | U the columns of its w13, D its w2.  q rounds a row to e4m3 as the weights are, with a scale for each 128
  * values along it; a block with an infinity or a NaN is NaN.  Products in matrix instructions with float32
- * accumulation; the result is rounded to nearest even once, and in calls of many pairs an expert's output to bf16
- * before it is weighted, as moonep_grouped_ffn's is.  Needs no plan: dims' R, S, K, E, H and I count, the
+ * accumulation; the result is rounded to nearest even once, and in calls of more than a few pairs an expert's output to float16,
+ * with a power of two for each 64 columns, before it is weighted.  Needs no plan: dims' R, S, K, E, H and I count, the
  * planner's limits on E/R and B do not apply.  An output depends on its own token only, and on dims.
  *   topk  [R, S, K] int32: an id outside [0, E) adds nothing, whatever its gate (rows of ended
  *         sequences: all ids -1, their output is zero); an id named twice counts twice

@@ -243,7 +243,8 @@ def fp8_ffn(x, topk, gates, w13, w2, unit=U, keep=0.0):
             q, dq = (r[0] for r in round_rows(a[None], da[None]))
             y = q @ w2[e]
             dy = dq @ np.abs(w2[e]) + span(I) * ((np.abs(q) + dq) @ np.abs(w2[e]))
-            dy += keep * (np.abs(y) + dy) + (2.0 ** -26 * (np.abs(y) + dy).max() if keep else 0)
+            # float16 with one power of two for 64: steps of 2^-24 where the largest is 2^14
+            dy += keep * (np.abs(y) + dy) + (2.0 ** -38 * (np.abs(y) + dy).max() if keep else 0)
             out[t] += gates[t, k] * y
             off[t] += np.abs(gates[t, k]) * dy
             mass[t] += np.abs(gates[t, k]) * (np.abs(y) + dy)

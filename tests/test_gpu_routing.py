@@ -4,9 +4,10 @@ their float64 definitions.
 Tolerances.  u = 2^-24 is half a step of float32; an output rounded to bf16 is off by at most 2^-8 of its value
 more.  The bounds of gates and gradients come with the definitions, which count the roundings of a float32
 evaluation.  The 8-bit experts round their activation to codes, where a value next to a border may take
-either: the definition bounds that too.  With few rows the products are exact to float32 sums; the tiles' 8-bit
-matrix instruction keeps a sum of 64 products to 2^-16 of their magnitudes (measured 2^-15.8 at most over sums
-of one instruction, 2^-16 and less over longer ones): 2^-15 here.  Stored outputs of an expert are float16, 2^-12.
+either: the definition bounds that too.  Few pairs, and tiles of 64 rows, widen codes to bf16 and add in float32;
+the 8-bit matrix instruction of larger tiles keeps a sum of 64 products to 2^-16 of their magnitudes (measured 2^-15.8 at
+most over sums of one instruction, 2^-16 and less over longer ones): 2^-15 here.  Tiles store an expert's outputs in
+float16: 11 significant bits, so half a step is at most 2^-11 of the value.
 """
 import numpy as np
 import pytest
@@ -452,26 +453,37 @@ def _run_ffn(topk, gates, x, p13, p2, E, H, I, R=1):
     return out.reshape(T, H)
 
 
+def _way(T, K, E, H):
+    """(which kernels take a call, what its bound counts)."""
+    if T <= 8 and T * K <= 64 and H <= 8192:
+        return "few", {}
+    if T * K < 48 * E:
+        return "tiles of 64", dict(keep=2.0 ** -11)
+    return f"tiles of {128 if T * K < 192 * E else 256}", dict(unit=2.0 ** -15, keep=2.0 ** -11)
+
+
 def _check_ffn(T, K, E, H, I, seed=0, R=1, **kw):
-    tiles = T * K >= 48 * E
-    say("ffn", T, K, E, H, I, seed, R, kw, "tiles" if tiles else "")
+    way, more = _way(T, K, E, H)
+    say("ffn", T, K, E, H, I, seed, R, kw, way)
     topk, gates, x, w13, w2 = _ffn_case(T, K, E, H, I, seed, **kw)
     out = _run_ffn(topk, gates, x, _quantized(w13), _quantized(w2), E, H, I, R)
     torch.cuda.synchronize()
-    more = dict(unit=2.0 ** -15, keep=2.0 ** -12) if tiles else {}
     ref, off = G.fp8_ffn(W.bf16_to_f32(x), topk, gates, _values(w13), _values(w2), **more)
     _near(f64_of(out), ref, off + 2.0 ** -8 * (np.abs(ref) + off), "out")
     for t in kw.get("masked", ()):
         assert not out[t].any()
 
 
-# one token and many; experts with no, few, 31, 32, 33 and more rows; sizes that end inside a block of 128, in
-# one block and in several, and more than 16 blocks
+# few pairs: one token to eight, fewer and more pairs than experts, one block of input values and several, on
+# both sides of the longest rows; tiles of 64: experts with no, few, 31, 32, 33, 64, 65 and more rows; sizes
+# that end inside a block of 128, in one block and in several, and more than 16 blocks
 @pytest.mark.parametrize("T,K,E,H,I", [
-    (1, 1, 1, 32, 32), (1, 2, 4, 64, 96), (2, 2, 4, 128, 64), (3, 1, 2, 160, 32), (8, 1, 1, 96, 64), (31, 1, 1, 128, 128),
-    (32, 1, 1, 160, 96), (33, 1, 1, 192, 64), (47, 1, 1, 64, 32), (90, 2, 4, 96, 96), (5, 2, 16, 320, 192),
-    (24, 4, 8, 288, 224), (7, 8, 8, 544, 160), (1, 8, 32, 1056, 544), (200, 16, 128, 32, 32), (3, 1, 2, 2208, 32),
-    (2, 2, 2, 64, 2080),
+    (1, 1, 1, 32, 32), (1, 2, 4, 64, 96), (2, 2, 4, 128, 64), (3, 1, 2, 160, 32), (8, 1, 1, 96, 64), (8, 8, 40, 256, 160),
+    (8, 8, 16, 288, 128), (4, 16, 16, 416, 64), (5, 2, 16, 320, 192), (7, 8, 8, 544, 160), (1, 8, 32, 1056, 544),
+    (3, 1, 2, 2208, 32), (2, 2, 2, 64, 2080), (2, 1, 2, 8192, 32), (2, 1, 2, 8224, 32), (1, 1, 1, 64, 4128),
+    (9, 1, 1, 96, 64), (8, 9, 9, 96, 64), (31, 1, 1, 128, 128), (32, 1, 1, 160, 96), (33, 1, 1, 192, 64),
+    (47, 1, 1, 64, 32), (64, 1, 2, 2208, 32), (90, 2, 4, 96, 96), (24, 4, 8, 288, 224), (200, 16, 128, 32, 32),
+    (65, 1, 2, 96, 2080), (12, 2, 3, 256, 1056),
 ])
 def test_ffn_few_rows(T, K, E, H, I):
     _check_ffn(T, K, E, H, I, seed=T + H)
@@ -490,7 +502,7 @@ def test_ffn_tiles(T, K, E, H, I):
     _check_ffn(T, K, E, H, I, seed=T + H)
 
 
-@pytest.mark.parametrize("T", [8, 120, 480])
+@pytest.mark.parametrize("T", [8, 40, 120, 480])
 def test_ffn_ranks_and_ids(T):
     for R in (2, 4):
         _check_ffn(T, 2, 4, 128, 64, seed=1, R=R)
@@ -500,24 +512,25 @@ def test_ffn_ranks_and_ids(T):
     _check_ffn(T, 2, 4, 96, 32, seed=5, outside=True)
 
 
-@pytest.mark.parametrize("T", [9, 300, 800])
-def test_ffn_uneven_and_repeated(T):
-    """All pairs to one of many experts, and an expert that a token names twice."""
-    E, K, H, I = 6, 2, 96, 160
+@pytest.mark.parametrize("T,K", [(8, 5), (9, 2), (100, 2), (300, 2), (800, 2)])
+def test_ffn_uneven_and_repeated(T, K):
+    """All pairs to one of many experts, which each token names twice or more."""
+    E, H, I = 6, 96, 160
     topk, gates, x, w13, w2 = _ffn_case(T, K, E, H, I, 6)
     topk[:] = 4
-    topk[T // 3] = [1, 4]
+    topk[T // 3, 0] = 1
     p = _quantized(w13), _quantized(w2)
     out = _run_ffn(topk, gates, x, *p, E, H, I)
-    more = dict(unit=2.0 ** -15, keep=2.0 ** -12) if T * K >= 48 * E else {}
+    _, more = _way(T, K, E, H)
     ref, off = G.fp8_ffn(W.bf16_to_f32(x), topk, gates, _values(w13), _values(w2), **more)
     _near(f64_of(out), ref, off + 2.0 ** -8 * (np.abs(ref) + off), "out")
 
 
 # what is computed where, exactly: one value a row, large gates (silu(g) = g), one value a column of w2, each
 # block of 128 of its own size, so that every sum has one term and every rounding is exact
-@pytest.mark.parametrize("T,E,H,I", [(20, 5, 416, 224), (40, 3, 2208, 544), (300, 3, 416, 224), (150, 2, 2208, 544),
-                                     (1100, 3, 416, 544), (500, 1, 2208, 352), (260, 1, 4256, 32)])
+@pytest.mark.parametrize("T,E,H,I", [(8, 3, 416, 224), (6, 5, 2208, 544), (20, 5, 416, 224), (40, 3, 2208, 544),
+                                     (300, 3, 416, 224), (150, 2, 2208, 544), (1100, 3, 416, 544), (500, 1, 2208, 352),
+                                     (260, 1, 4256, 32)])
 def test_ffn_exact(T, E, H, I):
     say("exact", T, E, H, I)
     rng = np.random.default_rng(T + H)
@@ -543,7 +556,7 @@ def test_ffn_exact(T, E, H, I):
     np.testing.assert_array_equal(f64_of(out), W.bf16_to_f32(_bits(want)))
 
 
-@pytest.mark.parametrize("T", [12, 300, 700])
+@pytest.mark.parametrize("T", [8, 12, 300, 700])
 def test_ffn_rows_do_not_mix(T):
     """A token with NaN or infinities changes no other; NaN gates count only where an expert is named."""
     E, K, H, I = 3, 2, 160, 64
@@ -565,7 +578,7 @@ def test_ffn_rows_do_not_mix(T):
 def test_ffn_broken_weights():
     """A block of weights with a NaN reaches the outputs of its expert only."""
     E, K, H, I = 3, 1, 256, 160
-    for T in (9, 200, 600):
+    for T in (7, 9, 200, 600):
         topk, gates, x, w13, w2 = _ffn_case(T, K, E, H, I, 8)
         want = _run_ffn(topk, gates, x, _quantized(w13), _quantized(w2), E, H, I)
         w2[1, 130, 200] = 0x7F80
@@ -576,14 +589,17 @@ def test_ffn_broken_weights():
 
 
 def test_ffn_batch_does_not_matter_within_a_way():
-    """A token's bits: alone and in a batch of few rows an expert; in tiles of 128 and of 256 rows."""
+    """A token's bits: in calls of few pairs, in tiles of 64 rows, and in those of 128 and 256."""
     E, K, H, I = 4, 2, 416, 160
     topk, gates, x, w13, w2 = _ffn_case(900, K, E, H, I, 12)
     p = _quantized(w13), _quantized(w2)
     run = lambda lo, hi: _run_ffn(topk[lo:hi], gates[lo:hi], x[lo:hi], *p, E, H, I)
-    few = run(0, 95)
-    for lo, hi in ((0, 1), (7, 40), (94, 95)):
+    few = run(0, 8)
+    for lo, hi in ((0, 1), (2, 7), (7, 8)):
         assert torch.equal(run(lo, hi), few[lo:hi])
+    some = run(0, 95)
+    for lo, hi in ((0, 9), (7, 40), (80, 95)):
+        assert torch.equal(run(lo, hi), some[lo:hi])
     many = run(0, 900)
     for lo, hi in ((0, 100), (100, 450), (300, 899)):
         assert torch.equal(run(lo, hi), many[lo:hi])
@@ -591,7 +607,7 @@ def test_ffn_batch_does_not_matter_within_a_way():
 
 def test_ffn_deterministic_and_streams():
     E, K, H, I = 4, 3, 256, 128
-    for T in (30, 150, 400):
+    for T in (7, 30, 150, 400):
         topk, gates, x, w13, w2 = _ffn_case(T, K, E, H, I, 7)
         p = _quantized(w13), _quantized(w2)
         first = _run_ffn(topk, gates, x, *p, E, H, I)
@@ -623,10 +639,9 @@ def test_ffn_past_32_bits(T):
     gates, x = rng.random((T, K)).astype(np.float32), _bits(rng.standard_normal((T, H)))
     out = _run_ffn(topk, gates, x, packed[:2], packed[2:], E, H, I)
     few = [p[[0, E - 1]].contiguous() for p in packed]
-    n = min(T, 40) if T < 7000 else T                        # the same way: few rows, or tiles
-    alone = _run_ffn(np.minimum(topk, 1)[:n], gates[:n], x[:n], few[:2], few[2:], 2, H, I)
+    alone = _run_ffn(np.minimum(topk, 1), gates, x, few[:2], few[2:], 2, H, I)   # the same way by T, K and E
     assert torch.isfinite(out).all() and bool(out.any())
-    assert torch.equal(out[:n], alone)
+    assert torch.equal(out, alone)
 
 
 def test_ffn_rows_past_32_bits():

@@ -167,10 +167,10 @@ def test_ffn_refuses():
 
 
 def test_ffn_workspace_serves_smaller_calls():
-    """Whatever way a call takes: few rows, tiles of 128 or 256 rows, one workgroup's sort or several."""
+    """Whatever way a call takes: few pairs, tiles of 64, 128 or 256 rows, one workgroup's sort or several."""
     for E, K, H, I in ((4, 2, 64, 32), (32, 8, 1024, 512), (256, 8, 7168, 2048), (1, 1, 96, 2048)):
         last = 0
-        for T in (1, 2, 5, 20, 47, 48, 90, 100, 191, 192, 193, 300, 700, 1023, 1024, 1025, 1600, 6000, 6200, 30000, 131072,
+        for T in (1, 2, 5, 8, 9, 20, 47, 48, 90, 100, 191, 192, 193, 300, 700, 1023, 1024, 1025, 1600, 6000, 6200, 30000, 131072,
                   131200, 140000):
             n = M.moonep_fp8_ffn_workspace_bytes(_dims(S=T, E=E, K=K, H=H, I=I))
             assert n >= last
