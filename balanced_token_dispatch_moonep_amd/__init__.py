@@ -208,8 +208,8 @@ def _torch():
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else int(stream.cuda_stream)
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _ptr(t, name, dtype=None, shape=None, numel=None, optional=False):
@@ -217,17 +217,18 @@ def _ptr(t, name, dtype=None, shape=None, numel=None, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    torch = _torch()
+    torch = _TORCH or _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
-    if t.get_device() != torch._C._cuda_getDevice():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}; the library runs on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")

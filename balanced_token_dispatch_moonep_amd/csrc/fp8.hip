@@ -97,7 +97,7 @@ static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
     if (!f8_few(d)) {
         const size_t most = experts + pairs / 64;        // runs
         w.max_runs = (int)(experts + pairs / w.run_rows);
-        w.hist = (int32_t*)take(pairs > kSortOnce ? std::min<size_t>((pairs + 4095) / 4096, kSortParts) * d.E * 4 : 0);
+        w.hist = (int32_t*)take(sort_hist_most(pairs, d.E));
         w.offsets = (int32_t*)take((size_t)(d.E + 1) * 4);
         w.dest = (int32_t*)take(pairs * 4);
         w.pair = (int32_t*)take(pairs * 4);
@@ -1010,8 +1010,8 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
         constexpr int split = 2;
         const int smem = std::max(kFewRows * (up.kb * kBlk + 16 + up.kb), 4 * split * 2 * 4 * 64 * 4);
         const auto kernel = fp8_few_up_kernel<split, 3>;
-        if (hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            hipSuccess)
+        if (smem > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, smem) != hipSuccess)
             return MOONEP_EHIP;
         hipLaunchKernelGGL(kernel, dim3(blks(d.I), std::min(d.T * d.K, d.E)), dim3(256 * split), smem, s, topk,
                            static_cast<const uint16_t*>(x), up, w.act, d);

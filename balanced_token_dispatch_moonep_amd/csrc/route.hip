@@ -9,17 +9,18 @@
 // A sum of sigmoids that underflows is no division by zero this way: s_k / sum s = softmax(log s)_k.
 //
 // Sixteen lanes share a row, so that four rows go through a wave and every step across lanes is a rotation
-// inside 16 lanes, an operand modifier instead of an instruction through LDS.  A lane's elements are
-// groups of VEC side by side, the lanes' groups next to each other, so that a load of the 16 lanes is one
-// piece of the row.
+// inside 16 lanes, an operand modifier instead of an instruction through LDS.  Where rows are too few to fill the
+// chip, all 64 lanes share one: a quarter of the elements to rank for two more steps (one token over 256 experts,
+// with a bias: 10.5 us, with 64 lanes 7.6, which is what the host needs for a call).  A lane's elements are groups of
+// VEC side by side, the lanes' groups next to each other, so that a load of the lanes is one piece of the row.
 #include <type_traits>
 
 #include "common.h"
 
 namespace moonep {
 
-constexpr int kRowLanes = 16;
-constexpr int kRowsABlock = 16;      // of 256 threads
+constexpr int kRouteThreads = 256;
+constexpr int kWideRows = 4096;      // up to here a row gets 64 lanes
 
 struct RouteArgs {
     const void* logits;              // [T, E]
@@ -46,33 +47,61 @@ __device__ __forceinline__ uint64_t turned(uint64_t v) {
     return (uint64_t)turned<N>((uint32_t)(v >> 32)) << 32 | turned<N>((uint32_t)v);
 }
 
-// f over the 16 lanes of a row, in each of them; f is commutative, and the tree the same for all lanes
-// only if f does not round (max, min): sums are taken from lane 0's.
+// a of the lanes of a row with a's lane STEP places away (16 and 32 lanes: halves and quarters of the wave change places)
 template <class T, class F>
+__device__ __forceinline__ T with_quarters(T v, F f) {
+    union {
+        T t;
+        uint32_t u[sizeof(T) / 4];
+    } a, b;
+    a.t = b.t = v;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 4; ++i) {
+        const auto r = __builtin_amdgcn_permlane16_swap(a.u[i], b.u[i], false, false);
+        a.u[i] = r[0];
+        b.u[i] = r[1];
+    }
+    v = f(a.t, b.t);
+    a.t = b.t = v;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 4; ++i) {
+        const auto r = __builtin_amdgcn_permlane32_swap(a.u[i], b.u[i], false, false);
+        a.u[i] = r[0];
+        b.u[i] = r[1];
+    }
+    return f(a.t, b.t);
+}
+
+// f over the lanes of a row, in each of them.  Each step joins the same pairs in every lane, and f is
+// commutative, so that all lanes agree where f rounds, too.
+template <int LANES, class T, class F>
 __device__ __forceinline__ T over_row(T v, F f) {
     v = f(v, turned<8>(v));
     v = f(v, turned<4>(v));
     v = f(v, turned<2>(v));
-    return f(v, turned<1>(v));
+    v = f(v, turned<1>(v));
+    if constexpr (LANES == 64) v = with_quarters(v, f);
+    return v;
 }
-// Rotations by 8, 4, 2, 1 add the same pairs in every lane (addition commutes), so all lanes agree.
+template <int LANES>
 __device__ __forceinline__ float row_sum(float v) {
-    return over_row(v, [](float a, float b) { return a + b; });
+    return over_row<LANES>(v, [](float a, float b) { return a + b; });
 }
+template <int LANES>
 __device__ __forceinline__ float row_max(float v) {
-    return over_row(v, [](float a, float b) { return fmaxf(a, b); });
+    return over_row<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 __device__ __forceinline__ float element(const float* p) { return *p; }
 __device__ __forceinline__ float element(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
-// A lane's elements of a row: element VEC * v + i is number (v * 16 + lane) * VEC + i of the row;
+// A lane's elements of a row: element VEC * v + i is number (v * LANES + lane) * VEC + i of the row;
 // -inf past its end.
-template <int NE, int VEC, class T>
+template <int LANES, int NE, int VEC, class T>
 __device__ __forceinline__ void load_row(float (&x)[NE], const T* row, int E, int lane) {
 #pragma unroll
     for (int v = 0; v < NE / VEC; ++v) {
-        const int e = (v * kRowLanes + lane) * VEC;
+        const int e = (v * LANES + lane) * VEC;
         if constexpr (VEC == 4 && sizeof(T) == 4) {
             const float inf = -__builtin_inff();
             const float4 f = e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(inf, inf, inf, inf);
@@ -85,9 +114,9 @@ __device__ __forceinline__ void load_row(float (&x)[NE], const T* row, int E, in
         }
     }
 }
-template <int VEC>
+template <int LANES, int VEC>
 __device__ __forceinline__ int index_of(int i, int lane) {
-    return (i / VEC * kRowLanes + lane) * VEC + i % VEC;
+    return (i / VEC * LANES + lane) * VEC + i % VEC;
 }
 
 // Order-preserving keys: larger for larger values, largest for NaN of either sign, 0 for -inf (no expert).
@@ -110,40 +139,41 @@ __device__ __forceinline__ float log_sigmoid(float v) { return fminf(v, 0.0f) - 
 
 // p of a row's picks, lane k that of pick k (0 where `here` is false); w is the picked logit or what stands
 // for it.  `top` and `total` are over the whole row in SOFTMAX_ALL.
+template <int LANES>
 __device__ __forceinline__ float picked_share(float w, bool here, bool all, float top, float total) {
     if (!all) {
-        top = row_max(here ? w : -__builtin_inff());
-        total = row_sum(here ? expf(w - top) : 0.0f);
+        top = row_max<LANES>(here ? w : -__builtin_inff());
+        total = row_sum<LANES>(here ? expf(w - top) : 0.0f);
     }
     return here ? expf(w - top) / total : 0.0f;
 }
 
 // Row maximum and sum of exp(x - maximum) over all of the row's elements.
-template <int NE>
+template <int LANES, int NE>
 __device__ __forceinline__ void row_softmax(const float (&x)[NE], float& top, float& total) {
     top = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < NE; ++i) top = fmaxf(top, x[i]);
-    top = row_max(top);
+    top = row_max<LANES>(top);
     total = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) total += x[i] == -__builtin_inff() ? 0.0f : expf(x[i] - top);
-    total = row_sum(total);
+    total = row_sum<LANES>(total);
 }
 
-template <class T, int NE, int VEC, bool BIAS>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+template <class T, int LANES, int NE, int VEC, bool BIAS>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     using Key = std::conditional_t<BIAS, uint64_t, uint32_t>;
-    const int lane = threadIdx.x % kRowLanes, row = blockIdx.x * kRowsABlock + threadIdx.x / kRowLanes;
+    const int lane = threadIdx.x % LANES, row = blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
     if (row >= a.T) return;
     const T* logits = static_cast<const T*>(a.logits) + (size_t)row * a.E;
     float x[NE];
-    load_row<NE, VEC>(x, logits, a.E, lane);
+    load_row<LANES, NE, VEC>(x, logits, a.E, lane);
     Key key[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         if constexpr (BIAS) {
-            const int e = index_of<VEC>(i, lane);
+            const int e = index_of<LANES, VEC>(i, lane);
             const double b = e < a.E ? a.bias[e] : 0.0f;
             const double v = a.mode == MOONEP_ROUTE_SIGMOID ? 1.0 / (1.0 + exp(-(double)x[i])) : (double)x[i];
             key[i] = x[i] == -__builtin_inff() ? 0 : key_of(v + b);
@@ -153,36 +183,34 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     }
     int mine = -1;                   // the expert of pick `lane`
     for (int k = 0; k < a.K; ++k) {
-        Key best = 0;
-        int at = 0x7fffffff;
+        Key best = 0;                // first the largest key, then the lowest of the ids that have it
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = index_of<VEC>(i, lane);
-            }
-        const Key top = over_row(best, [](Key p, Key q) { return p > q ? p : q; });
-        const uint32_t id = over_row(best == top ? (uint32_t)at : 0x7fffffffu,
-                                     [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+        for (int i = 0; i < NE; ++i) best = key[i] > best ? key[i] : best;
+        const Key top = over_row<LANES>(best, [](Key p, Key q) { return p > q ? p : q; });
+        uint32_t at = 0x7fffffffu;
+#pragma unroll
+        for (int i = NE - 1; i >= 0; --i)
+            if (key[i] == top) at = index_of<LANES, VEC>(i, lane);
+        const uint32_t id = over_row<LANES>(at, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
         if (lane == k && top != 0) mine = (int)id;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (index_of<VEC>(i, lane) == (int)id) key[i] = 0;
+            if (index_of<LANES, VEC>(i, lane) == (int)id) key[i] = 0;
     }
     const bool here = mine >= 0, all = a.mode == MOONEP_ROUTE_SOFTMAX_ALL;
     float w = here ? element(logits + mine) : 0.0f, top = 0.0f, total = 0.0f;
     if (a.mode == MOONEP_ROUTE_SIGMOID) w = log_sigmoid(w);
-    if (all) row_softmax(x, top, total);
-    const float p = picked_share(w, here, all, top, total);
+    if (all) row_softmax<LANES>(x, top, total);
+    const float p = picked_share<LANES>(w, here, all, top, total);
     if (lane < a.K) {
         a.topk[(size_t)row * a.K + lane] = mine;
         a.gates[(size_t)row * a.K + lane] = here ? a.scale * p : 0.0f;
     }
 }
 
-template <class T, int NE, int VEC>
-__global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs a) {
-    const int lane = threadIdx.x % kRowLanes, row = blockIdx.x * kRowsABlock + threadIdx.x / kRowLanes;
+template <class T, int LANES, int NE, int VEC>
+__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
+    const int lane = threadIdx.x % LANES, row = blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
     if (row >= a.T) return;
     const T* logits = static_cast<const T*>(a.logits) + (size_t)row * a.E;
     const bool all = a.mode == MOONEP_ROUTE_SOFTMAX_ALL;
@@ -197,31 +225,31 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs a) {
     const float l = here ? element(logits + id) : 0.0f;
     float x[NE], top = 0.0f, total = 0.0f;
     if (all) {
-        load_row<NE, VEC>(x, logits, a.E, lane);
-        row_softmax(x, top, total);
+        load_row<LANES, NE, VEC>(x, logits, a.E, lane);
+        row_softmax<LANES>(x, top, total);
     }
-    const float p = picked_share(a.mode == MOONEP_ROUTE_SIGMOID ? log_sigmoid(l) : l, here, all, top, total);
-    const float dot = row_sum(here ? p * dg : 0.0f);
+    const float p = picked_share<LANES>(a.mode == MOONEP_ROUTE_SIGMOID ? log_sigmoid(l) : l, here, all, top, total);
+    const float dot = row_sum<LANES>(here ? p * dg : 0.0f);
     // the picks' own part
     float d = all ? p * dg : p * (dg - dot);
     if (a.mode == MOONEP_ROUTE_SIGMOID) d *= 1.0f / (1.0f + expf(l));
     if (!here) d = 0.0f;
-    const bool any = row_max(here ? 1.0f : 0.0f) > 0.0f;
+    const bool any = row_max<LANES>(here ? 1.0f : 0.0f) > 0.0f;
     float g[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i)
         g[i] = all && any && x[i] != -__builtin_inff() ? -(expf(x[i] - top) / total) * dot : 0.0f;
     for (int k = 0; k < a.K; ++k) {  // an id that is named twice gets both, in this order
-        const int to = __shfl(id, k, kRowLanes);
-        const float v = __shfl(d, k, kRowLanes);
+        const int to = __shfl(id, k, LANES);
+        const float v = __shfl(d, k, LANES);
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (index_of<VEC>(i, lane) == to) g[i] += v;
+            if (index_of<LANES, VEC>(i, lane) == to) g[i] += v;
     }
     T* out = static_cast<T*>(a.dlogits) + (size_t)row * a.E;
 #pragma unroll
     for (int v = 0; v < NE / VEC; ++v) {
-        const int e = (v * kRowLanes + lane) * VEC;
+        const int e = (v * LANES + lane) * VEC;
         if (e >= a.E) continue;
         if constexpr (VEC == 4 && sizeof(T) == 4) {
             *reinterpret_cast<float4*>(out + e) =
@@ -249,24 +277,31 @@ static int check_route(const moonep_dims_t* d, uint32_t mode, float scale) {
     return MOONEP_OK;
 }
 
-template <class T, int NE, int VEC, bool BACK>
+template <class T, int LANES, int NE, int VEC, bool BACK>
 static void launch_route(const RouteArgs& a, hipStream_t s) {
-    const dim3 grid((a.T + kRowsABlock - 1) / kRowsABlock);
+    constexpr int rows = kRouteThreads / LANES;
+    const dim3 grid((a.T + rows - 1) / rows);
     if constexpr (BACK)
-        hipLaunchKernelGGL((route_backward_kernel<T, NE, VEC>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((route_backward_kernel<T, LANES, NE, VEC>), grid, dim3(kRouteThreads), 0, s, a);
     else if (a.bias)
-        hipLaunchKernelGGL((route_kernel<T, NE, VEC, true>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((route_kernel<T, LANES, NE, VEC, true>), grid, dim3(kRouteThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((route_kernel<T, NE, VEC, false>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((route_kernel<T, LANES, NE, VEC, false>), grid, dim3(kRouteThreads), 0, s, a);
 }
 
 template <class T, int VEC, bool BACK>
 static void route_sizes(const RouteArgs& a, hipStream_t s) {
-    if (a.E <= 4 * kRowLanes) launch_route<T, 4, VEC, BACK>(a, s);
-    else if (a.E <= 8 * kRowLanes) launch_route<T, 8, VEC, BACK>(a, s);
-    else if (a.E <= 16 * kRowLanes) launch_route<T, 16, VEC, BACK>(a, s);
-    else if (a.E <= 32 * kRowLanes) launch_route<T, 32, VEC, BACK>(a, s);
-    else launch_route<T, 64, VEC, BACK>(a, s);
+    if (a.T <= kWideRows) {
+        if (a.E <= 4 * 64) launch_route<T, 64, 4, VEC, BACK>(a, s);
+        else if (a.E <= 8 * 64) launch_route<T, 64, 8, VEC, BACK>(a, s);
+        else launch_route<T, 64, 16, VEC, BACK>(a, s);
+    } else {
+        if (a.E <= 4 * 16) launch_route<T, 16, 4, VEC, BACK>(a, s);
+        else if (a.E <= 8 * 16) launch_route<T, 16, 8, VEC, BACK>(a, s);
+        else if (a.E <= 16 * 16) launch_route<T, 16, 16, VEC, BACK>(a, s);
+        else if (a.E <= 32 * 16) launch_route<T, 16, 32, VEC, BACK>(a, s);
+        else launch_route<T, 16, 64, VEC, BACK>(a, s);
+    }
 }
 
 // Rows of a multiple of four logits start where a load of four does.

@@ -10,6 +10,8 @@
 
 namespace moonep {
 
+constexpr int kKept = 4;             // rounds of 64 pairs: a wave's share of kSortPart
+
 // Lanes of the wave with this lane's id; ids below 2^bits.
 __device__ __forceinline__ unsigned long long same_id(int id, bool valid, int bits) {
     unsigned long long m = __ballot(valid);
@@ -30,7 +32,8 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_count_kernel(SortArgs a)
         if ((unsigned)id < (unsigned)a.E) atomicAdd(&count[id], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 64 * kSortWaves) a.hist[(size_t)blockIdx.x * a.E + e] = count[e];
+    const int even = (a.E + 1) & ~1;
+    for (int e = threadIdx.x; e < even; e += 64 * kSortWaves) a.hist[(size_t)blockIdx.x * even + e] = e < a.E ? count[e] : 0;
 }
 
 // Exclusive prefix sums over the experts of up to two counts each, for threads that hold two experts in a row.
@@ -65,7 +68,17 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs a)
     const int begin = blockIdx.x * a.part, n = min(a.P - begin, a.part);
     const int rounds = (n + NT - 1) / NT;        // of 64 pairs a wave
     const int first = begin + wave * rounds * 64, last = min(begin + n, first + rounds * 64);
-    for (int p = first + lane; p < last; p += 64) {
+    // the first kKept rounds' ids stay in registers for the second time that they are needed
+    int kept[kKept];
+#pragma unroll
+    for (int r = 0; r < kKept; ++r) {
+        const int p = first + r * 64 + lane;
+        kept[r] = p < last ? a.topk[p] : -1;
+    }
+#pragma unroll
+    for (int r = 0; r < kKept; ++r)
+        if ((unsigned)kept[r] < (unsigned)a.E) atomicAdd(&at[wave][kept[r]], 1);
+    for (int p = first + kKept * 64 + lane; p < last; p += 64) {
         const int id = a.topk[p];
         if ((unsigned)id < (unsigned)a.E) atomicAdd(&at[wave][id], 1);
     }
@@ -82,14 +95,33 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs a)
         if constexpr (ONCE) total[i] = mine[i];
     }
     if constexpr (!ONCE) {
-#pragma unroll 4
-        for (int b = 0; b < a.parts; ++b)
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = tid * PER + i;
-                const int c = e < a.E ? a.hist[(size_t)b * a.E + e] : 0;
-                total[i] += c;
-                before[i] += b < (int)blockIdx.x ? c : 0;
+        // two experts a thread; where that is not all threads, several groups of them share the parts
+        __shared__ int2 sums_of[2][NT];
+        const int pairs = (a.E + 1) / 2, groups = min(NT / pairs, 16), g = tid / pairs;
+        int2 all = make_int2(0, 0), earlier = make_int2(0, 0);
+        if (g < groups) {
+            const int2* h = reinterpret_cast<const int2*>(a.hist) + tid % pairs;
+#pragma unroll 8
+            for (int b = g; b < a.parts; b += groups) {
+                const int2 c = h[(size_t)b * pairs];
+                const bool before_this = b < (int)blockIdx.x;
+                all.x += c.x;
+                all.y += c.y;
+                earlier.x += before_this ? c.x : 0;
+                earlier.y += before_this ? c.y : 0;
+            }
+        }
+        sums_of[0][tid] = all;
+        sums_of[1][tid] = earlier;
+        __syncthreads();
+        static_assert(PER == 2, "a thread's experts are one pair");
+        if (tid < pairs)
+            for (int i = 0; i < groups; ++i) {
+                const int2 c = sums_of[0][i * pairs + tid], b = sums_of[1][i * pairs + tid];
+                total[0] += c.x;
+                total[1] += c.y;
+                before[0] += b.x;
+                before[1] += b.y;
             }
     }
     int sum = 0;
@@ -126,11 +158,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs a)
     }
     __syncthreads();
     const int bits = 32 - __clz(a.E);
-    for (int p0 = first; p0 < last; p0 += 64) {
-        const int p = p0 + lane;
-        const int id = p < last ? a.topk[p] : -1;
-        const bool valid = (unsigned)id < (unsigned)a.E;
-        const unsigned long long same = same_id(id, valid, bits);
+    auto place = [&](int p, int id, bool valid, unsigned long long same) {
         int row = -1;
         if (valid) {
             row = at[wave][id] + __popcll(same & ((1ull << lane) - 1));
@@ -142,6 +170,17 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs a)
         if (valid && lane == 63 - __clzll(same)) at[wave][id] = row + 1;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
+    };
+    unsigned long long same[kKept];
+#pragma unroll
+    for (int r = 0; r < kKept; ++r) same[r] = same_id(kept[r], (unsigned)kept[r] < (unsigned)a.E, bits);
+#pragma unroll
+    for (int r = 0; r < kKept; ++r) place(first + r * 64 + lane, kept[r], (unsigned)kept[r] < (unsigned)a.E, same[r]);
+    for (int p0 = first + kKept * 64; p0 < last; p0 += 64) {
+        const int p = p0 + lane;
+        const int id = p < last ? a.topk[p] : -1;
+        const bool valid = (unsigned)id < (unsigned)a.E;
+        place(p, id, valid, same_id(id, valid, bits));
     }
 }
 

@@ -77,6 +77,29 @@ def test_route(mode, dtype, bias):
         _near(gates.double().cpu().numpy(), ref, tol, "gates")
 
 
+# more rows than get a wave each: 16 lanes a row, which hold 4 to 64 elements each
+@pytest.mark.parametrize("E,K", [(5, 3), (64, 8), (65, 2), (128, 16), (250, 8), (256, 8), (400, 5), (1000, 4), (1023, 16)])
+def test_route_many_rows(E, K):
+    T = 4100
+    rows = [0, 1, 2, 3, 1000, 4095, 4096, 4097, 4099]
+    for mode in MODES:
+        for bias in (False, True):
+            dtype = BF if bias else F32
+            z = _logits(T, E, dtype, E, masked=(1,))
+            b = np.random.default_rng(E).standard_normal(E).astype(np.float32) if bias else None
+            ids, gates = _route(z, f32(b) if bias else None, K, mode, 0.5)
+            zs, got = z[rows].double().cpu().numpy(), ids.cpu().numpy()
+            want, ref, tol = G.route(zs, b, K, mode, 0.5)
+            np.testing.assert_array_equal(got[rows], want)
+            _near(gates[rows].double().cpu().numpy(), ref, tol, "gates")
+            dg = torch.randn(T, K, generator=torch.Generator().manual_seed(E)).to(DEV)
+            dz = _route_backward(dg, z, ids, mode, 0.5)
+            ref, tol = G.route_backward(dg[rows].cpu().numpy(), zs, got[rows], mode, 0.5)
+            if dtype == BF:
+                tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+            _near(dz[rows].double().cpu().numpy(), ref, tol, "dlogits")
+
+
 def test_route_ties_go_to_the_lower_id():
     rng = np.random.default_rng(1)
     for E, K in ((5, 3), (64, 16), (200, 8), (1001, 16)):
@@ -84,8 +107,11 @@ def test_route_ties_go_to_the_lower_id():
         z[z == 0] = np.where(rng.random((z == 0).sum()) < 0.5, 0.0, -0.0)    # zeros of both signs are one value
         for bias in (None, rng.integers(0, 2, E).astype(np.float32)):
             for dtype in (F32, BF):
-                ids, _ = _route(torch.from_numpy(z).to(dtype).to(DEV), None if bias is None else f32(bias), K, "softmax")
-                np.testing.assert_array_equal(ids.cpu().numpy(), G.route(z, bias, K, "softmax")[0])
+                want = G.route(z, bias, K, "softmax")[0]
+                for copies in (1, 110):                      # 64 lanes a row, and 16
+                    ids, _ = _route(torch.from_numpy(z).to(dtype).to(DEV).repeat(copies, 1), None if bias is None else f32(bias),
+                                    K, "softmax")
+                    np.testing.assert_array_equal(ids.cpu().numpy(), np.tile(want, (copies, 1)))
 
 
 def test_route_bias_next_to_a_border():
@@ -231,7 +257,7 @@ def _check_sort(topk, E, **kw):
         assert (got[n:] == -7).all()                         # behind the last row: left as they were
 
 
-# one workgroup's rounds and waves, its limit of 8192 pairs, several parts, the last of them short
+# one workgroup's rounds and waves, its limit of 8192 pairs, several parts of 2048, the last of them short
 @pytest.mark.parametrize("T,K,E", [(1, 1, 1), (1, 8, 256), (63, 1, 5), (64, 1, 5), (65, 1, 5), (128, 8, 256), (511, 1, 3),
                                    (513, 1, 3), (1024, 8, 1024), (8193, 1, 7), (4097, 2, 1), (1250, 10, 33), (20011, 15, 1024),
                                    (262144, 4, 256), (70000, 16, 1000)])
@@ -257,7 +283,7 @@ def test_sort_without_rows_and_ranks():
 
 
 def test_sort_past_a_million_pairs():
-    """Parts of more than 4096 pairs."""
+    """Parts of more than 2048 pairs."""
     topk = np.random.default_rng(3).integers(-1, 300, (600011, 2)).astype(np.int32)
     _check_sort(topk, 300)
 
