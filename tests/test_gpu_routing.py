@@ -313,7 +313,7 @@ def _check_combine_backward(T, K, H, dtype, seed, weights=True, dy=True, dgates=
         _near(dg[0].double().cpu().numpy(), ref, tol, "dgates")
 
 
-# rows that a wave keeps in 2, 8 and 14 vectors a lane, and longer ones; on both sides of each
+# rows of 4 and 14 vectors a lane at a time, on both sides of each, and longer ones
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 @pytest.mark.parametrize("H", [8, 72, 512, 520, 1024, 1032, 2048, 3584, 3592, 4096, 4104, 7168, 7176, 16384])
 def test_combine_backward(H, dtype):
