@@ -160,36 +160,63 @@ __device__ __forceinline__ void put_block(const float (&v)[8], const F8Rows& r, 
     if (lane16 == 0) r.scales[row * r.sp + block] = (uint8_t)scale_byte(top);
 }
 
-// Rounds rows of x.  With tiles, workgroups past the rows list them: expert by expert, column tile by column
-// tile, run by run, so that neighbours share rows and weights; and the rows' tokens.
-__global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ x, F8Ws w, F8Dims d, int kb) {
-    if ((int)blockIdx.x >= d.T) {
-        if (blockIdx.y > 0) return;
-        int t = (blockIdx.x - d.T) * 256 + threadIdx.x;
-        if (t < w.offsets[d.E]) w.token[t] = w.pair[t] / d.K;
-        const int nruns = w.nruns[0];
-        int NT = up_columns(d);
-        Tile* tiles = w.up_tiles;
-        if (t >= nruns * NT) {
-            t -= nruns * NT;
-            NT = down_columns(d);
-            tiles = w.down_tiles;
-            if (t >= nruns * NT) return;
-        }
-        const Run run = w.runs[t / NT];
-        const int begin = w.offsets[run.expert], rows = w.offsets[run.expert + 1] - begin;
-        const int mtiles = (rows + w.run_rows - 1) / w.run_rows;
-        const int local = t - (t / NT - (run.first - begin) / w.run_rows) * NT, row0 = local % mtiles * w.run_rows;
-        tiles[t] = Tile{run.expert, begin + row0, min(w.run_rows, rows - row0), local / mtiles};
-        return;
+// Tile t of the list: expert by expert, column tile by column tile, run by run, so that neighbours share rows and
+// weights; the tiles of the first product, then those of the second.
+__device__ __forceinline__ void list_tile(const F8Ws& w, const F8Dims& d, int nruns, int t) {
+    int NT = up_columns(d);
+    Tile* tiles = w.up_tiles;
+    if (t >= nruns * NT) {
+        t -= nruns * NT;
+        NT = down_columns(d);
+        tiles = w.down_tiles;
+        if (t >= nruns * NT) return;
     }
-    const int at = blockIdx.y * 16 + threadIdx.x / 16, lane16 = threadIdx.x % 16, k = at * kBlk + lane16 * 8;
-    const size_t row = blockIdx.x;
-    if (at >= kb) return;
+    const Run run = w.runs[t / NT];
+    const int begin = w.offsets[run.expert], rows = w.offsets[run.expert + 1] - begin;
+    const int mtiles = (rows + w.run_rows - 1) / w.run_rows;
+    const int local = t - (t / NT - (run.first - begin) / w.run_rows) * NT, row0 = local % mtiles * w.run_rows;
+    tiles[t] = Tile{run.expert, begin + row0, min(w.run_rows, rows - row0), local / mtiles};
+}
+
+// Rounds blocks of a row of x, 16 lanes each.
+__device__ __forceinline__ void round_row(const uint16_t* x, const F8Ws& w, const F8Dims& d, size_t row, int block) {
+    const int lane16 = threadIdx.x % 16, k = block * kBlk + lane16 * 8;
+    if (block >= blks(d.H)) return;
     const uint4 u = k < d.H ? *reinterpret_cast<const uint4*>(x + row * d.H + k) : make_uint4(0, 0, 0, 0);
     const float v[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
                         bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
-    put_block(v, w.x, row, at, lane16);
+    put_block(v, w.x, row, block, lane16);
+}
+
+// All that comes before the products, where one workgroup sorts and lists in the time that a second launch would
+// take: it does, and the others round x.
+constexpr int kBeginPairs = 2048;
+static_assert(kBeginPairs <= kSortOnce, "one workgroup sorts");
+__global__ __launch_bounds__(64 * kSortWaves) void fp8_begin_kernel(const uint16_t* __restrict__ x, SortArgs a, F8Ws w,
+                                                                    F8Dims d) {
+    constexpr int NT = 64 * kSortWaves;
+    if (blockIdx.x > 0) {
+        round_row(x, w, d, blockIdx.x - 1, blockIdx.y * (NT / 16) + threadIdx.x / 16);
+        return;
+    }
+    if (blockIdx.y > 0) return;
+    sort_place<true>(a, 0);
+    __syncthreads();
+    const int nruns = w.nruns[0], rows = w.offsets[d.E];
+    for (int i = threadIdx.x; i < rows; i += NT) w.token[i] = w.pair[i] / d.K;
+    for (int t = threadIdx.x; t < nruns * (up_columns(d) + down_columns(d)); t += NT) list_tile(w, d, nruns, t);
+}
+
+// The same after a sort: the workgroups past the rows of x list tiles and tokens.
+__global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* __restrict__ x, F8Ws w, F8Dims d) {
+    if ((int)blockIdx.x < d.T) {
+        round_row(x, w, d, blockIdx.x, blockIdx.y * 16 + threadIdx.x / 16);
+        return;
+    }
+    if (blockIdx.y > 0) return;
+    const int t = (blockIdx.x - d.T) * 256 + threadIdx.x;
+    if (t < w.offsets[d.E]) w.token[t] = w.pair[t] / d.K;
+    list_tile(w, d, w.nruns[0], t);
 }
 
 // A workgroup a block of 128 x 128.  A thread reads eight columns of eight rows; the codes are turned in
@@ -429,7 +456,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_down_kernel(const int32_t*
             const size_t row = __shfl(pair, min(r0 + (lane & 31), n - 1), 64);
             const uint8_t *codes = act.codes + row * act.pitch + (lane >> 5) * 16, *scales = act.scales + row * act.sp;
             f32x16_t acc[1];
-            multiply_few<1, 4, true>(
+            multiply_few<1, 2, true>(
                 acc, m, tile, scale, 0, 1, [] {},
                 [&](int k, int p) { return *reinterpret_cast<const uint4*>(codes + (size_t)k * kBlk + p * 32); },
                 [&](int k) { return (int)scales[k]; });
@@ -1007,9 +1034,9 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     hipStream_t s = static_cast<hipStream_t>(stream);
     const F8Mat up = f8_mat(w13_codes, w13_scales, d.H, 2 * d.I), down = f8_mat(w2_codes, w2_scales, d.I, d.H);
     if (f8_few(d)) {
-        constexpr int split = 2;
+        constexpr int split = 1;
         const int smem = std::max(kFewRows * (up.kb * kBlk + 16 + up.kb), 4 * split * 2 * 4 * 64 * 4);
-        const auto kernel = fp8_few_up_kernel<split, 3>;
+        const auto kernel = fp8_few_up_kernel<split, 4>;
         if (smem > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, smem) != hipSuccess)
             return MOONEP_EHIP;
@@ -1024,10 +1051,15 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     SortArgs a = sort_args((int)pairs, d.E);
     a.topk = topk, a.hist = w.hist, a.offsets = w.offsets, a.dest = w.dest, a.pair = w.pair;
     a.run_rows = w.run_rows, a.runs = w.runs, a.nruns = w.nruns;
-    if (launch_sort(a, s) != MOONEP_OK) return MOONEP_EHIP;
-    const size_t listed = std::max(pairs, (size_t)w.max_runs * (up_columns(d) + down_columns(d)));
-    hipLaunchKernelGGL(fp8_rows_kernel, dim3(d.T + (unsigned)((listed + 255) / 256), (up.kb + 15) / 16), dim3(256), 0, s,
-                       static_cast<const uint16_t*>(x), w, d, up.kb);
+    if (pairs <= kBeginPairs) {
+        hipLaunchKernelGGL(fp8_begin_kernel, dim3(d.T + 1, (up.kb + 31) / 32), dim3(64 * kSortWaves), 0, s,
+                           static_cast<const uint16_t*>(x), a, w, d);
+    } else {
+        if (launch_sort(a, s) != MOONEP_OK) return MOONEP_EHIP;
+        const size_t listed = std::max(pairs, (size_t)w.max_runs * (up_columns(d) + down_columns(d)));
+        hipLaunchKernelGGL(fp8_rows_kernel, dim3(d.T + (unsigned)((listed + 255) / 256), (up.kb + 15) / 16), dim3(256), 0,
+                           s, static_cast<const uint16_t*>(x), w, d);
+    }
     MOONEP_LAUNCH_CHECK();
     const int rc2 = w.run_rows == 64 ? launch_both<64>(up, down, w, d, s)
                     : w.run_rows == 128 ? launch_both<128>(up, down, w, d, s)

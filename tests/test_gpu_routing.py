@@ -257,9 +257,9 @@ def _check_sort(topk, E, **kw):
         assert (got[n:] == -7).all()                         # behind the last row: left as they were
 
 
-# one workgroup's rounds and waves, its limit of 8192 pairs, several parts of 2048, the last of them short
+# one workgroup's rounds and waves, its limit of 4096 pairs, several parts of 2048, the last of them short
 @pytest.mark.parametrize("T,K,E", [(1, 1, 1), (1, 8, 256), (63, 1, 5), (64, 1, 5), (65, 1, 5), (128, 8, 256), (511, 1, 3),
-                                   (513, 1, 3), (1024, 8, 1024), (8193, 1, 7), (4097, 2, 1), (1250, 10, 33), (20011, 15, 1024),
+                                   (513, 1, 3), (512, 8, 1024), (4096, 1, 2), (4097, 1, 500), (1024, 8, 1024), (8193, 1, 7), (4097, 2, 1), (1250, 10, 33), (20011, 15, 1024),
                                    (262144, 4, 256), (70000, 16, 1000)])
 def test_sort(T, K, E):
     say("sort", T, K, E)
@@ -515,14 +515,14 @@ def test_ffn_few_rows(T, K, E, H, I):
     _check_ffn(T, K, E, H, I, seed=T + H)
 
 
-# tiles of 128 rows (48 to 191 pairs an expert) and of 256: one in part and several, experts without rows;
+# tiles of 128 rows (48 to 191 pairs an expert) and of 256, sorted with the rounding and in launches of their own: one in part and several, experts without rows;
 # one, two, three and more stages of 128 input values, 16 and 17 and more than 32 of them; columns that end
 # inside a tile of 256 and inside a block of 128
 @pytest.mark.parametrize("T,K,E,H,I", [
     (48, 1, 1, 32, 32), (64, 2, 2, 128, 64), (127, 1, 1, 160, 96), (128, 1, 1, 288, 128), (129, 1, 1, 384, 160),
     (191, 1, 1, 512, 320), (192, 1, 1, 96, 64), (255, 1, 1, 128, 128), (256, 1, 1, 160, 288), (257, 1, 1, 288, 32),
     (600, 2, 3, 320, 96), (100, 3, 5, 416, 192), (70, 2, 2, 2048, 32), (70, 2, 2, 2080, 32), (200, 1, 1, 2208, 64),
-    (60, 1, 1, 4256, 32), (200, 1, 1, 64, 2112), (64, 1, 1, 96, 4128), (700, 1, 2, 544, 32),
+    (60, 1, 1, 4256, 32), (200, 1, 1, 64, 2112), (64, 1, 1, 96, 4128), (700, 1, 2, 544, 32), (1100, 2, 20, 64, 32), (2100, 2, 3, 64, 32),
 ])
 def test_ffn_tiles(T, K, E, H, I):
     _check_ffn(T, K, E, H, I, seed=T + H)
