@@ -449,6 +449,7 @@ extern "C" int moonep_combine_backward(const moonep_dims_t* dims, const int32_t*
                                        const float* gates, const void* dout, void* dy, float* dgates, void* stream) {
     const int rc = check_row_dims(dims);
     if (rc != MOONEP_OK) return rc;
+    if ((int64_t)dims->R * dims->S > 1 << 25) return MOONEP_ENOTSUP;        // a wave a token: fewer than 2^32 lanes in a launch
     if (!dy && !dgates) return MOONEP_EINVAL;
     MOONEP_CHECK_PTR(dest);
     MOONEP_CHECK_PTR(dout);

@@ -8,19 +8,24 @@
 //   over the whole row: dlogit_e = scale * ([e picked] p_e dg_e - p_e sum_i p_i dg_i).
 // A sum of sigmoids that underflows is no division by zero this way: s_k / sum s = softmax(log s)_k.
 //
+// What bounds it is ranking.  Without a bias each lane sorts its best K and the K heads are compared across lanes:
+// 32768 rows of 256 float32 take 11.4 us for K 8 and 15.6 for K 16 in a graph, of which reading them is 6; K times a
+// maximum over all elements took 17.1 and 25.5.  With a bias keys are doubles and are ranked that way, and a sigmoid in
+// float64 comes before it: 37.5 us.
+//
 // Sixteen lanes share a row, so that four rows go through a wave and every step across lanes is a rotation
 // inside 16 lanes, an operand modifier instead of an instruction through LDS.  Where rows are too few to fill the
 // chip, all 64 lanes share one: a quarter of the elements to rank for two more steps (one token over 256 experts,
 // with a bias: 10.5 us, with 64 lanes 7.6, which is what the host needs for a call).  A lane's elements are groups of
 // VEC side by side, the lanes' groups next to each other, so that a load of the lanes is one piece of the row.
-#include <type_traits>
-
 #include "common.h"
 
 namespace moonep {
 
 constexpr int kRouteThreads = 256;
-constexpr int kWideRows = 4096;      // up to here a row gets 64 lanes
+// Up to so many rows get 64 lanes each (16 lanes / 64, us, E 256, K 8): 1024 rows 3.4 / 3.3 and 2048 3.4 / 3.8; with a
+// bias 1024 rows 10.3 / 5.5 and 4096 11.5 / 10.0, backward 4.0 / 3.3 and 4.9 / 4.9.
+constexpr int kWideRows = 1024, kWideSlowRows = 4096;
 
 struct RouteArgs {
     const void* logits;              // [T, E]
@@ -45,6 +50,10 @@ __device__ __forceinline__ float turned(float v) {
 template <int N>
 __device__ __forceinline__ uint64_t turned(uint64_t v) {
     return (uint64_t)turned<N>((uint32_t)(v >> 32)) << 32 | turned<N>((uint32_t)v);
+}
+template <int N>
+__device__ __forceinline__ double turned(double v) {
+    return __longlong_as_double(turned<N>((uint64_t)__double_as_longlong(v)));
 }
 
 // a of the lanes of a row with a's lane STEP places away (16 and 32 lanes: halves and quarters of the wave change places)
@@ -119,21 +128,6 @@ __device__ __forceinline__ int index_of(int i, int lane) {
     return (i / VEC * LANES + lane) * VEC + i % VEC;
 }
 
-// Order-preserving keys: larger for larger values, largest for NaN of either sign, 0 for -inf (no expert).
-// Zeros of both signs are one value.
-__device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v + 0.0f);
-    if (v != v) return 0xffffffffu;
-    if (v == -__builtin_inff()) return 0;
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ uint64_t key_of(double v) {
-    const uint64_t u = __double_as_longlong(v + 0.0);
-    if (v != v) return ~0ull;
-    if (v == -__builtin_inf()) return 0;
-    return u >> 63 ? ~u : u | 1ull << 63;
-}
-
 // log(sigmoid(v)): no underflow for v far below zero
 __device__ __forceinline__ float log_sigmoid(float v) { return fminf(v, 0.0f) - log1pf(expf(-fabsf(v))); }
 
@@ -161,41 +155,150 @@ __device__ __forceinline__ void row_softmax(const float (&x)[NE], float& top, fl
     total = row_sum<LANES>(total);
 }
 
-template <class T, int LANES, int NE, int VEC, bool BIAS>
+// Without a bias a logit and its id make one number, so that one comparison ranks both: a double from 1 up to 2
+// with the logit's 32 bits in order and then kMaxE - 1 - id in the 52 bits of its fraction, which the maximum of two doubles
+// orders as it does integers.  (Doubles because one instruction takes the larger of two, and none does of 64-bit
+// integers.)
+constexpr double kNoPick = 1.0, kNoKey = -0x1p200;
+static_assert(kMaxE == 1 << 10, "32 bits of a logit and 10 of its id");
+__device__ __forceinline__ double ranked(float v, int id) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    const uint32_t key = v != v ? 0xffffffffu : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    const uint32_t hi = __builtin_amdgcn_alignbit(0x3ffu, key, 12), lo = (key << 20) + (kMaxE - 1 - id);
+    return __longlong_as_double((uint64_t)hi << 32 | lo);
+}
+// -1 for what is no pick: -inf and less
+__device__ __forceinline__ int ranked_id(double v) {
+    const uint64_t u = __double_as_longlong(v);
+    return (u >> 43 & 0x1ff) != 0 ? kMaxE - 1 - (int)(u & (kMaxE - 1)) : -1;
+}
+// No operand is NaN.  (fmax and fmin quiet NaN in an instruction of their own, for most operands here.)
+__device__ __forceinline__ double larger(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double smaller(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+// The same for results that move to other lanes: two wait states before that.
+__device__ __forceinline__ double larger_to_move(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2\n\ts_nop 1" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ void larger_first(double& a, double& b) {
+    const double m = larger(a, b);
+    b = smaller(a, b);
+    a = m;
+}
+
+// Comparisons that sort N values (Batcher's odd-even merges).
+template <int N>
+struct Network {
+    int n = 0, a[N * 4] = {}, b[N * 4] = {};
+    constexpr Network() {
+        for (int p = 1; p < N; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < N; j += 2 * k)
+                    for (int i = 0; i < k && i + j + k < N; ++i)
+                        if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            a[n] = i + j;
+                            b[n++] = i + j + k;
+                        }
+    }
+};
+
+// The D best of a lane's NE elements, best first: D at a time sorted, and joined with the best so far, of which
+// the element-wise larger ones against the others backwards are the D best, in an order that log D steps sort.
+template <int LANES, int NE, int VEC, int D>
+__device__ __forceinline__ void lane_best(double (&best)[D], const float (&x)[NE], int lane) {
+    constexpr Network<D> net;
+#pragma unroll
+    for (int c = 0; c < NE; c += D) {
+        double v[D];
+#pragma unroll
+        for (int i = 0; i < D; ++i) v[i] = ranked(x[c + i], index_of<LANES, VEC>(c + i, lane));
+#pragma unroll
+        for (int i = 0; i < net.n; ++i) larger_first(v[net.a[i]], v[net.b[i]]);
+        if (c == 0) {
+#pragma unroll
+            for (int i = 0; i < D; ++i) best[i] = v[i];
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < D; ++i) best[i] = larger(best[i], v[D - 1 - i]);
+#pragma unroll
+        for (int step = D / 2; step > 0; step /= 2)
+#pragma unroll
+            for (int i = 0; i < D; ++i)
+                if ((i & step) == 0) larger_first(best[i], best[i + step]);
+    }
+}
+
+// Pick k, and the MOVES first of the lane's others if it was its own.
+template <int LANES, int MOVES, int D>
+__device__ __forceinline__ void next_pick(double (&best)[D], double& pick, int k, int lane) {
+    const double top = over_row<LANES>(best[0], larger_to_move);
+    if (lane == k) pick = top;
+    const bool own = best[0] == top;
+#pragma unroll
+    for (int i = 0; i < MOVES; ++i)
+        best[i] = own ? i + 1 < D ? best[i + 1] : kNoPick : best[i];
+}
+// Picks k .. K of up to KM, each moving what later ones can need.
+template <int LANES, int KM, int k, int D>
+__device__ __forceinline__ void next_picks(double (&best)[D], double& pick, int K, int lane) {
+    if (k >= K) return;
+    next_pick<LANES, KM - 1 - k < D ? KM - 1 - k : D>(best, pick, k, lane);
+    if constexpr (k + 1 < KM) next_picks<LANES, KM, k + 1>(best, pick, K, lane);
+}
+
+// KM: without a bias, K at most; 0 with one.
+template <class T, int LANES, int NE, int VEC, int KM>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
-    using Key = std::conditional_t<BIAS, uint64_t, uint32_t>;
     const int lane = threadIdx.x % LANES, row = blockIdx.x * (kRouteThreads / LANES) + threadIdx.x / LANES;
     if (row >= a.T) return;
     const T* logits = static_cast<const T*>(a.logits) + (size_t)row * a.E;
     float x[NE];
     load_row<LANES, NE, VEC>(x, logits, a.E, lane);
-    Key key[NE];
+    int mine = -1;                   // the expert of pick `lane`
+    if constexpr (KM > 0) {
+        constexpr int D = NE < KM ? NE : KM;
+        double best[D];
+        lane_best<LANES, NE, VEC, D>(best, x, lane);
+        asm("s_nop 1" : "+v"(best[0]));
+        double pick = kNoPick;
+        next_picks<LANES, KM, 0>(best, pick, a.K, lane);
+        mine = ranked_id(pick);
+    } else {
+        // finite keys are below 2^130: infinity and NaN are larger ones, so that all are numbers
+        double key[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        if constexpr (BIAS) {
+        for (int i = 0; i < NE; ++i) {
             const int e = index_of<LANES, VEC>(i, lane);
             const double b = e < a.E ? a.bias[e] : 0.0f;
-            const double v = a.mode == MOONEP_ROUTE_SIGMOID ? 1.0 / (1.0 + exp(-(double)x[i])) : (double)x[i];
-            key[i] = x[i] == -__builtin_inff() ? 0 : key_of(v + b);
-        } else {
-            key[i] = key_of(x[i]);
+            const double v = b + (a.mode == MOONEP_ROUTE_SIGMOID ? 1.0 / (1.0 + exp(-(double)x[i])) : (double)x[i]);
+            key[i] = x[i] == -__builtin_inff() ? kNoKey : v != v ? 0x1p201 : fmin(fmax(v, kNoKey), 0x1p200);
         }
-    }
-    int mine = -1;                   // the expert of pick `lane`
-    for (int k = 0; k < a.K; ++k) {
-        Key best = 0;                // first the largest key, then the lowest of the ids that have it
+        for (int k = 0; k < a.K; ++k) {      // first the largest key, then the lowest of the ids that have it
+            double best = key[0];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) best = key[i] > best ? key[i] : best;
-        const Key top = over_row<LANES>(best, [](Key p, Key q) { return p > q ? p : q; });
-        uint32_t at = 0x7fffffffu;
+            for (int i = 1; i < NE; ++i) best = larger(best, key[i]);
+            asm("s_nop 1" : "+v"(best));
+            const double top = over_row<LANES>(best, larger_to_move);
+            uint32_t at = 0x7fffffffu;
 #pragma unroll
-        for (int i = NE - 1; i >= 0; --i)
-            if (key[i] == top) at = index_of<LANES, VEC>(i, lane);
-        const uint32_t id = over_row<LANES>(at, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
-        if (lane == k && top != 0) mine = (int)id;
+            for (int i = NE - 1; i >= 0; --i)
+                if (key[i] == top) at = index_of<LANES, VEC>(i, lane);
+            const uint32_t id = over_row<LANES>(at, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+            if (lane == k && top != kNoKey) mine = (int)id;
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (index_of<LANES, VEC>(i, lane) == (int)id) key[i] = 0;
+            for (int i = 0; i < NE; ++i)
+                if (index_of<LANES, VEC>(i, lane) == (int)id) key[i] = kNoKey;
+        }
     }
     const bool here = mine >= 0, all = a.mode == MOONEP_ROUTE_SOFTMAX_ALL;
     float w = here ? element(logits + mine) : 0.0f, top = 0.0f, total = 0.0f;
@@ -273,6 +376,7 @@ static int check_route(const moonep_dims_t* d, uint32_t mode, float scale) {
     if (d->R < 1 || d->R > kMaxR || d->S < 1 || d->E < 1 || d->E > kMaxE) return MOONEP_EINVAL;
     if (d->K < 1 || d->K > kMaxK || d->K > d->E) return MOONEP_EINVAL;
     if ((int64_t)d->R * d->S * d->K > (int64_t)1 << 30) return MOONEP_EINVAL;
+    if ((int64_t)d->R * d->S > 1 << 27) return MOONEP_ENOTSUP;      // 16 lanes a row: fewer than 2^32 in a launch
     if (!(scale > -__builtin_inff() && scale < __builtin_inff())) return MOONEP_EINVAL;
     return MOONEP_OK;
 }
@@ -284,14 +388,16 @@ static void launch_route(const RouteArgs& a, hipStream_t s) {
     if constexpr (BACK)
         hipLaunchKernelGGL((route_backward_kernel<T, LANES, NE, VEC>), grid, dim3(kRouteThreads), 0, s, a);
     else if (a.bias)
-        hipLaunchKernelGGL((route_kernel<T, LANES, NE, VEC, true>), grid, dim3(kRouteThreads), 0, s, a);
+        hipLaunchKernelGGL((route_kernel<T, LANES, NE, VEC, 0>), grid, dim3(kRouteThreads), 0, s, a);
+    else if (a.K <= 8)
+        hipLaunchKernelGGL((route_kernel<T, LANES, NE, VEC, 8>), grid, dim3(kRouteThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((route_kernel<T, LANES, NE, VEC, false>), grid, dim3(kRouteThreads), 0, s, a);
+        hipLaunchKernelGGL((route_kernel<T, LANES, NE, VEC, 16>), grid, dim3(kRouteThreads), 0, s, a);
 }
 
 template <class T, int VEC, bool BACK>
 static void route_sizes(const RouteArgs& a, hipStream_t s) {
-    if (a.T <= kWideRows) {
+    if (a.T <= (BACK || a.bias ? kWideSlowRows : kWideRows)) {
         if (a.E <= 4 * 64) launch_route<T, 64, 4, VEC, BACK>(a, s);
         else if (a.E <= 8 * 64) launch_route<T, 64, 8, VEC, BACK>(a, s);
         else launch_route<T, 64, 16, VEC, BACK>(a, s);

@@ -359,7 +359,7 @@ int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* g
  * picked; where fewer than K are left the id is -1 and the gate 0 (moonep_sort and the decoders take
  * such ids, moonep_plan does not).  A NaN key ranks above all others, and a NaN or +inf among the logits
  * that gates are made of makes the token's gates NaN.  Gates in float32, times scale (finite).
- * Only R, S, K and E of dims matter (E to 1024, K to min(E, 16)).
+ * Only R, S, K and E of dims matter (E to 1024, K to min(E, 16); MOONEP_ENOTSUP over 2^27 tokens).
  *   logits [R, S, E] float32 or bf16;  bias [E] float32 or NULL
  *   topk   [R, S, K] int32 out;  gates [R, S, K] float32 out
  * Outputs must not overlap inputs or each other (MOONEP_EINVAL). */
@@ -395,7 +395,7 @@ int moonep_sort(const moonep_dims_t* dims, const int32_t* topk, void* ws, int32_
 /* Backward of moonep_combine, for rows and gates in one pass:
  *   dy[dest[p]] = gates[p] * dout[token(p)]  (the same bits as moonep_dispatch with gates as row_scale)
  *   dgates[p]   = sum over the row of dout[token(p)] * y[dest[p]]  (float32; 0 where dest is -1)
- * Only R, S, K, H and the row type of dims matter.
+ * Only R, S, K, H and the row type of dims matter (MOONEP_ENOTSUP over 2^25 tokens).
  *   y      [R*S*K, H] as for moonep_combine; NULL where dgates is
  *   gates  [R, S, K] float32 or NULL (ones)
  *   dout   [R, S, H] type of the rows
@@ -425,9 +425,10 @@ int moonep_quantize_fp8(int32_t E, int32_t Kin, int32_t N, const void* w, void* 
  *   out[r,s] = sum over k (in k order) of gates[r,s,k] * (q(silu(q(x) G) * (q(x) U)) D)  of expert topk[r,s,k],
  * G | U the columns of its w13, D its w2.  q rounds a row to e4m3 as the weights are, with a scale for each 128
  * values along it; a block with an infinity or a NaN is NaN.  Products in matrix instructions with float32
- * accumulation; the result is rounded to nearest even once, and in calls of more than a few pairs an expert's output to float16,
- * with a power of two for each 64 columns, before it is weighted.  Needs no plan: dims' R, S, K, E, H and I count, the
- * planner's limits on E/R and B do not apply.  An output depends on its own token only, and on dims.
+ * accumulation; the result is rounded to nearest even once.  In calls of more than a few pairs an expert's output is
+ * rounded to float16 too, with a power of two for each 64 columns, before it is weighted.  Needs no plan: dims' R, S,
+ * K, E, H and I count, the planner's limits on E/R and B do not apply.  An output depends on its own token only, and
+ * on dims.
  *   topk  [R, S, K] int32: an id outside [0, E) adds nothing, whatever its gate (rows of ended
  *         sequences: all ids -1, their output is zero); an id named twice counts twice
  *   gates [R, S, K] float32;  x [R, S, H] bf16;  out [R, S, H] bf16 out

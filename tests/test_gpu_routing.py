@@ -78,7 +78,8 @@ def test_route(mode, dtype, bias):
 
 
 # more rows than get a wave each: 16 lanes a row, which hold 4 to 64 elements each
-@pytest.mark.parametrize("E,K", [(5, 3), (64, 8), (65, 2), (128, 16), (250, 8), (256, 8), (400, 5), (1000, 4), (1023, 16)])
+@pytest.mark.parametrize("E,K", [(5, 3), (64, 8), (65, 2), (128, 16), (250, 8), (256, 8), (256, 9), (400, 5), (512, 16), (1000, 4),
+                                 (1023, 16)])
 def test_route_many_rows(E, K):
     T = 4100
     rows = [0, 1, 2, 3, 1000, 4095, 4096, 4097, 4099]
@@ -123,6 +124,28 @@ def test_route_bias_next_to_a_border():
     z = np.array([[18.0, 18.5, 19.0]], np.float32)
     ids, _ = _route(f32(z), f32([0.0, 0.0, 0.0]), 3, "sigmoid")
     assert ids.tolist() == [[2, 1, 0]]
+
+
+@pytest.mark.parametrize("K", [1, 8, 16])
+@pytest.mark.parametrize("E", [64, 256, 1000])
+def test_route_order_of_all_values(E, K):
+    """Values of every kind, many of them in one lane: NaN of either sign first, then infinity, down to the smallest
+    numbers of either sign; 64 lanes a row, and 16."""
+    bits = np.array([0x7fc00000, 0xffc00001, 0x7f800000, 0x7f7fffff, 0x3f800001, 0x3f800000, 0x00800000, 0x00000002, 0x00000001,
+                     0, 0x80000000, 0x80000001, 0x80800000, 0xbf800000, 0xff7fffff, 0xff800000], np.uint32)
+    rng = np.random.default_rng(E + K)
+    z = np.full((30, E), -np.inf, np.float32)
+    for t in range(30):
+        n = rng.integers(0, 24)
+        at = rng.permutation(E)[:n] if t % 2 else rng.permutation(min(E, 256))[:n] // 4 * 4       # of one lane or two
+        z[t, at] = rng.choice(bits, len(at)).view(np.float32)
+    key = np.where(np.isnan(z), 4e38, np.where(z == np.inf, 3.9e38, z.astype(np.float64)))
+    order = np.argsort(-key, axis=1, kind="stable")[:, :K]
+    want = np.where(np.take_along_axis(z, order, 1) == -np.inf, -1, order)
+    for copies in (1, 140):
+        for bias in (None, np.zeros(E, np.float32)):
+            ids, _ = _route(f32(np.tile(z, (copies, 1))), None if bias is None else f32(bias), K, "softmax")
+            np.testing.assert_array_equal(ids.cpu().numpy(), np.tile(want, (copies, 1)))
 
 
 @pytest.mark.parametrize("mode", MODES)

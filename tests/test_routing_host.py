@@ -70,6 +70,14 @@ def test_route_refuses(call):
     assert call(_dims(H=0, I=-3, B=1000, R=3, E=1024), topk=FAR * 50 + 4) == EALIGN
 
 
+def test_more_rows_than_a_launch_has_lanes():
+    for call in (route, route_backward):
+        assert call(_dims(S=(1 << 27) + 1, K=1)) == ENOTSUP
+        assert call(_dims(S=1 << 27, K=1), topk=FAR * 50 + 4) == EALIGN
+    assert combine_backward(_dims(S=(1 << 25) + 1, K=1)) == ENOTSUP
+    assert combine_backward(_dims(S=1 << 25, K=1), dest=FAR * 50 + 4) == EALIGN
+
+
 def test_route_refuses_overlap():
     d = _dims(S=64)                                          # picks: 2048 bytes; logits: 8192
     assert route(d, topk=FAR + 8192 - 16) == EINVAL          # the logits' end
