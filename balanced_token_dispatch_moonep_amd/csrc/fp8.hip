@@ -188,10 +188,8 @@ __device__ __forceinline__ void round_row(const uint16_t* x, const F8Ws& w, cons
     put_block(v, w.x, row, block, lane16);
 }
 
-// All that comes before the products, where one workgroup sorts and lists in the time that a second launch would
-// take: it does, and the others round x.
-constexpr int kBeginPairs = 2048;
-static_assert(kBeginPairs <= kSortOnce, "one workgroup sorts");
+// All that comes before the products, up to kSortOnce pairs: one workgroup sorts and lists, and the others round x
+// meanwhile (512 pairs 9.7 us; 4096 pairs 20, as three launches take).
 __global__ __launch_bounds__(64 * kSortWaves) void fp8_begin_kernel(const uint16_t* __restrict__ x, SortArgs a, F8Ws w,
                                                                     F8Dims d) {
     constexpr int NT = 64 * kSortWaves;
@@ -888,35 +886,53 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
     }
 }
 
-// out = sum over k of gate * y, in k order, skipping pairs without a row; a wave a token and VB pieces of 512 columns, which it reads of one row after another.
-// VB: 7 where there are tokens enough for all waves (8192 of H 7168 219 us), else 1 (512 of H 7168 64 us with 7).
-template <int VB>
+// out = sum over k of gate * y, in k order, skipping pairs without a row; a wave a token and VB pieces of 512 columns, KU
+// of its rows read together.  Bound by memory: 8192 tokens of 8 rows of 7168 (1.06 GB) take 221 us with 7 pieces,
+// 4.8 TB/s.  Fewer tokens need more waves, a piece each, and loads in flight (1 / 4 / 8 rows): 64 tokens 10.2 / 8.3 / 8.8
+// us, 512 tokens 16.6 / 15.2 / 19.2, with 7 pieces a wave 64.
+template <int VB, int KU>
 __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ gates, F8Ws w, uint4* __restrict__ out,
-                                                         F8Dims d) {
+                                                       F8Dims d) {
     const int tok = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, vecs = d.H / 8;
     if (tok >= d.T) return;
     const int32_t* dest = w.dest + (size_t)tok * d.K;
     const int v0 = blockIdx.y * 64 * VB;
     float acc[VB][8] = {};
 #pragma unroll 1
-    for (int k = 0; k < d.K; ++k) {
-        const int row = dest[k];
-        if (row < 0) continue;
-        const float g = gates[(size_t)tok * d.K + k];
-        const uint4* y = reinterpret_cast<const uint4*>(w.y16) + (size_t)row * vecs;
-        const uint8_t* ex = w.y16_exp + (size_t)row * w.y16_sp;
+    for (int k0 = 0; k0 < d.K; k0 += KU) {
+        int row[KU];
+        float g[KU];
+        uint4 y[KU][VB];
+        int ex[KU][VB];
 #pragma unroll
-        for (int u = 0; u < VB; ++u) {
-            const int v = v0 + u * 64 + lane;
-            if (v >= vecs) continue;
-            union {
-                uint4 u;
-                _Float16 h[8];
-            } r;
-            r.u = ld_nt(y + v);
-            const float s = __uint_as_float((uint32_t)(ex[v / 8] - 14) << 23);
+        for (int j = 0; j < KU; ++j) {
+            const bool there = k0 + j < d.K;
+            row[j] = there ? dest[k0 + j] : -1;
+            g[j] = there ? gates[(size_t)tok * d.K + k0 + j] : 0.0f;
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[u][i] += g * ((float)r.h[i] * s);
+        for (int j = 0; j < KU; ++j)
+#pragma unroll
+            for (int u = 0; u < VB; ++u) {
+                const int v = v0 + u * 64 + lane;
+                const bool there = row[j] >= 0 && v < vecs;
+                y[j][u] = there ? ld_nt(reinterpret_cast<const uint4*>(w.y16) + (size_t)row[j] * vecs + v) : make_uint4(0, 0, 0, 0);
+                ex[j][u] = there ? w.y16_exp[(size_t)row[j] * w.y16_sp + v / 8] : 15;
+            }
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+            if (row[j] < 0) continue;
+#pragma unroll
+            for (int u = 0; u < VB; ++u) {
+                union {
+                    uint4 u;
+                    _Float16 h[8];
+                } r;
+                r.u = y[j][u];
+                const float s = __uint_as_float((uint32_t)(ex[j][u] - 14) << 23);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[u][i] += g[j] * ((float)r.h[i] * s);
+            }
         }
     }
 #pragma unroll
@@ -1051,7 +1067,7 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     SortArgs a = sort_args((int)pairs, d.E);
     a.topk = topk, a.hist = w.hist, a.offsets = w.offsets, a.dest = w.dest, a.pair = w.pair;
     a.run_rows = w.run_rows, a.runs = w.runs, a.nruns = w.nruns;
-    if (pairs <= kBeginPairs) {
+    if (pairs <= kSortOnce) {
         hipLaunchKernelGGL(fp8_begin_kernel, dim3(d.T + 1, (up.kb + 31) / 32), dim3(64 * kSortWaves), 0, s,
                            static_cast<const uint16_t*>(x), a, w, d);
     } else {
@@ -1067,9 +1083,9 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     if (rc2 != MOONEP_OK) return rc2;
     uint4* o = static_cast<uint4*>(out);
     if (d.T >= 4096)
-        hipLaunchKernelGGL(fp8_join_kernel<7>, dim3((d.T + 3) / 4, (d.H / 8 + 447) / 448), dim3(256), 0, s, gates, w, o, d);
+        hipLaunchKernelGGL((fp8_join_kernel<7, 1>), dim3((d.T + 3) / 4, (d.H / 8 + 447) / 448), dim3(256), 0, s, gates, w, o, d);
     else
-        hipLaunchKernelGGL(fp8_join_kernel<1>, dim3((d.T + 3) / 4, (d.H / 8 + 63) / 64), dim3(256), 0, s, gates, w, o, d);
+        hipLaunchKernelGGL((fp8_join_kernel<1, 4>), dim3((d.T + 3) / 4, (d.H / 8 + 63) / 64), dim3(256), 0, s, gates, w, o, d);
     MOONEP_LAUNCH_CHECK();
     return MOONEP_OK;
 }

@@ -12,7 +12,7 @@
 namespace moonep {
 
 constexpr int kSortWaves = 8;
-constexpr int kSortOnce = 4096;      // pairs that one workgroup sorts in one launch (8.8 us; two launches 8.0, 8192 pairs 8.3 and 16.5)
+constexpr int kSortOnce = 2048;      // pairs that one workgroup sorts in one launch (5.0 us; 4096 pairs 8.8, in two launches 7.8)
 constexpr int kSortParts = 256;      // workgroups of a larger sort, at most
 constexpr int kSortPart = 2048;      // pairs of one of them, at least
 
@@ -96,7 +96,6 @@ __device__ __forceinline__ void sort_place(const SortArgs& a, int part) {
     for (int e = tid; e < a.E; e += NT)
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) at[w][e] = 0;
-    __syncthreads();
     const int begin = part * a.part, n = min(a.P - begin, a.part);
     const int rounds = (n + NT - 1) / NT;        // of 64 pairs a wave
     const int first = begin + wave * rounds * 64, last = min(begin + n, first + rounds * 64);
@@ -107,6 +106,28 @@ __device__ __forceinline__ void sort_place(const SortArgs& a, int part) {
         const int p = first + r * 64 + lane;
         kept[r] = p < last ? a.topk[p] : -1;
     }
+    // the other parts' counts, on their way with the ids: two experts a thread; where that is not all threads, several
+    // groups of them share the parts
+    __shared__ int2 sums_of[2][ONCE ? 1 : NT];
+    const int pairs = (a.E + 1) / 2, groups = min(NT / pairs, 16);
+    if constexpr (!ONCE) {
+        int2 all = make_int2(0, 0), earlier = make_int2(0, 0);
+        if (tid / pairs < groups) {
+            const int2* h = reinterpret_cast<const int2*>(a.hist) + tid % pairs;
+#pragma unroll 8
+            for (int b = tid / pairs; b < a.parts; b += groups) {
+                const int2 c = h[(size_t)b * pairs];
+                const bool before_this = b < part;
+                all.x += c.x;
+                all.y += c.y;
+                earlier.x += before_this ? c.x : 0;
+                earlier.y += before_this ? c.y : 0;
+            }
+        }
+        sums_of[0][tid] = all;
+        sums_of[1][tid] = earlier;
+    }
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < kKept; ++r)
         if ((unsigned)kept[r] < (unsigned)a.E) atomicAdd(&at[wave][kept[r]], 1);
@@ -127,25 +148,6 @@ __device__ __forceinline__ void sort_place(const SortArgs& a, int part) {
         if constexpr (ONCE) total[i] = mine[i];
     }
     if constexpr (!ONCE) {
-        // two experts a thread; where that is not all threads, several groups of them share the parts
-        __shared__ int2 sums_of[2][NT];
-        const int pairs = (a.E + 1) / 2, groups = min(NT / pairs, 16), g = tid / pairs;
-        int2 all = make_int2(0, 0), earlier = make_int2(0, 0);
-        if (g < groups) {
-            const int2* h = reinterpret_cast<const int2*>(a.hist) + tid % pairs;
-#pragma unroll 8
-            for (int b = g; b < a.parts; b += groups) {
-                const int2 c = h[(size_t)b * pairs];
-                const bool before_this = b < part;
-                all.x += c.x;
-                all.y += c.y;
-                earlier.x += before_this ? c.x : 0;
-                earlier.y += before_this ? c.y : 0;
-            }
-        }
-        sums_of[0][tid] = all;
-        sums_of[1][tid] = earlier;
-        __syncthreads();
         static_assert(PER == 2, "a thread's experts are one pair");
         if (tid < pairs)
             for (int i = 0; i < groups; ++i) {

@@ -103,7 +103,7 @@ def test_sort_refuses():
 
 def test_sort_workspace():
     size = lambda **kw: M.moonep_sort_workspace_bytes(_dims(**kw))
-    assert size() == size(S=512) == 256                      # one workgroup keeps all of it
+    assert size() == size(S=256) == 256                      # one workgroup keeps all of it
     assert size(S=1025) == 768 and 5 * 32 * 4 == 640         # five parts of 2048 pairs, in whole 256 bytes
     assert size(S=1025, E=31) == 768                         # an even number of experts
     assert size(S=1 << 26, K=16, E=1024) == 256 * 1024 * 4   # the most parts
