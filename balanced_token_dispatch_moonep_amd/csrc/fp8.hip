@@ -6,6 +6,14 @@
 // power of two for each 128 values along it.  The matrix instruction v_mfma_scale_f32_32x32x64_f8f6f4 multiplies
 // such codes and applies both powers itself, so a product needs no arithmetic beside it; that is why the scales
 // are powers of two and not floats (which would cost a multiply-add for every accumulator and block).
+//
+// What bounds it (32 experts of H 7168 and I 2048, 8 a token; a call, inputs changing):
+//   1 token       70 us   reading 352 MB of weights, 5.0 TB/s: the first product has 128 workgroups
+//   64 tokens    266 us   reading 1409 MB, 5.5 TB/s in the products; 18 us to sort, round and join
+//   512 tokens   350 us   the same weights, in whole rounds of tiles (3.1 of the first product): 4.2 TB/s
+//   8192 tokens 2770 us   matrix instructions: 2.1 PFLOP/s in all, 2.3 to 2.5 in the first product, where the matrix
+//                         cores are busy 67 to 71 % of the time at the 1.8 GHz that power leaves; the second stores its
+//                         results for 180 us of its 1000, as the registers that hold them are those of the next tile
 #include "dma.h"
 #include "sort.h"
 
@@ -62,13 +70,18 @@ __host__ __device__ static constexpr int blks(int n) { return (n + kBlk - 1) / k
 __host__ __device__ static constexpr int up_columns(const F8Dims& d) { return (d.I + 127) / 128; }
 __host__ __device__ static constexpr int down_columns(const F8Dims& d) { return (d.H + 255) / 256; }
 
-// Whether two launches for few pairs take a call: 8 tokens of up to 64 pairs, whose rounded rows fit LDS.
+// Whether two launches for few pairs take a call: 8 tokens of up to 64 pairs, whose rounded rows fit LDS.  Against tiles
+// of 64 rows (us, experts as above): 1 token 71 / 90, 2 tokens 101 / 126, 4 tokens 170 / 207, 8 tokens 210 / 241; 256
+// such experts, 8 tokens 408 / 454.
 constexpr int kFewRows = 8, kFewPitch = 8192;
 static bool f8_few(const F8Dims& d) {
     return d.T <= kFewRows && d.T * d.K <= kFewPairs && blks(d.H) * kBlk <= kFewPitch;
 }
 
-// Rows of a tile otherwise: by the pairs that an expert has on average.
+// Rows of a tile otherwise: by the pairs that an expert has on average, with which more rows that are not there meet
+// fewer reads of a weight.  Tiles of 64 / 128 / 256 rows (us, experts as above): 16 pairs an expert 259 / 266 / 315, 64 309
+// / 286 / 335, 128 414 / 360 / 381, 192 530 / 483 / 470, 512 1158 / 913 / 839; 8 experts of H 4096 and I 1024: 128 51
+// / 55 / 74, 512 121 / 115 / 108.
 static int f8_rows(const F8Dims& d) {
     const int64_t pairs = (int64_t)d.T * d.K;
     return pairs < 48ll * d.E ? 64 : pairs < 192ll * d.E ? 128 : 256;
@@ -285,7 +298,7 @@ __device__ __forceinline__ float scale_of(int byte) { return __uint_as_float((ui
 // The row of a 32 x 32 result that a lane's register r holds; the column is lane % 32.
 __device__ __forceinline__ int result_row(int r, int lane) { return r / 4 * 8 + (lane >> 5) * 4 + r % 4; }
 
-// acc = 32 rows times NT column tiles, over blocks first, first + step, ... of the input direction.
+// acc = 32 rows times NT column tiles, over all blocks of the input direction.
 // A lane holds row lane % 32 and, of each 32 input values, the 16 of its half of the wave; so does it of
 // the columns, whose layout makes a wave's load one KiB in a row.  D blocks of weights are on their way while one is
 // multiplied; past the last one they are asked for again instead of branching around the load.  start() runs
@@ -297,10 +310,8 @@ __device__ __forceinline__ int result_row(int r, int lane) { return r / 4 * 8 + 
 // reading the weights is what takes the time.
 template <int NT, int D, bool AHEAD, class Start, class Rows, class Scale>
 __device__ __forceinline__ void multiply_few(f32x16_t (&acc)[NT], const F8Mat& m, const size_t* tile,
-                                             const uint8_t* const* scale, int first, int step, Start start, Rows rows,
-                                             Scale row_scale) {
-    const int lane = threadIdx.x & 63;
-    const int n = first < m.kb ? (m.kb - first + step - 1) / step : 0;
+                                             const uint8_t* const* scale, Start start, Rows rows, Scale row_scale) {
+    const int lane = threadIdx.x & 63, n = m.kb;
     uint4 a[D][4], b[D][NT][4];
     int sa[D], sb[D][NT];
     const uint4* base[NT];
@@ -310,9 +321,8 @@ __device__ __forceinline__ void multiply_few(f32x16_t (&acc)[NT], const F8Mat& m
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][i] = 0.0f;
     }
-    auto block = [&](int s) { return first + max(min(s, n - 1), 0) * step; };
     auto load = [&](int j, int s) {
-        const int k = min(block(s), m.kb - 1);
+        const int k = min(s, n - 1);
         if constexpr (AHEAD) {
             sa[j] = row_scale(k);
 #pragma unroll
@@ -332,7 +342,7 @@ __device__ __forceinline__ void multiply_few(f32x16_t (&acc)[NT], const F8Mat& m
 #pragma unroll
         for (int j = 0; j < D; ++j) {
             if (s + j < n) {
-                const int k = block(s + j);
+                const int k = s + j;
                 const float fa = scale_of(AHEAD ? sa[j] : row_scale(k));
                 float fb[NT];
 #pragma unroll
@@ -357,13 +367,12 @@ __device__ __forceinline__ void multiply_few(f32x16_t (&acc)[NT], const F8Mat& m
 __device__ __forceinline__ float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // act = q(silu(q(x) G) * (q(x) U)) of one expert's pairs and 128 columns: a block of act, which the workgroup rounds
-// itself.  Four pairs of tiles, their input direction dealt out to SPLIT waves each, which join their sums in order.
+// itself.  A wave has a pair of gate and up tiles and all of the input direction: with two or four waves a pair, which then
+// join their sums, the kernel took 47 .. 55 us for one token of H 7168 instead of 46.5.
 // blockIdx.y: a pair, that leads its expert's group if it is the first of it, or an expert where there are
 // fewer experts than pairs.  The workgroup rounds the rows of x itself, while the first weights arrive.
-template <int SPLIT, int D>
-__global__ __launch_bounds__(256 * SPLIT) void fp8_few_up_kernel(const int32_t* __restrict__ topk,
-                                                                 const uint16_t* __restrict__ x, F8Mat m, F8Rows act,
-                                                                 F8Dims d) {
+__global__ __launch_bounds__(256) void fp8_few_up_kernel(const int32_t* __restrict__ topk,
+                                                         const uint16_t* __restrict__ x, F8Mat m, F8Rows act, F8Dims d) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int pairs = d.T * d.K, tid = threadIdx.x, lane = tid & 63, wave = wave_of();
     const int id = pair_expert(topk, pairs, d.E);
@@ -372,7 +381,7 @@ __global__ __launch_bounds__(256 * SPLIT) void fp8_few_up_kernel(const int32_t* 
     if (e < 0 || members == 0) return;
     if (pairs <= d.E && __ffsll(members) - 1 != (int)blockIdx.y) return;
     const int n = __popcll(members), pair = member_pair(members), block = blockIdx.x;
-    const int gate = min(block * 4 + wave / SPLIT, d.I / kCols - 1), up = d.I / kCols + gate;
+    const int gate = min(block * 4 + wave, d.I / kCols - 1), up = d.I / kCols + gate;
     const size_t tiles = (size_t)e * (m.n / kCols), tile[2] = {tiles + gate, tiles + up};
     const uint8_t* scales = m.scales + (size_t)e * m.nb * m.kbp;
     const uint8_t* scale[2] = {scales + (size_t)(gate / 4) * m.kbp, scales + (size_t)(up / 4) * m.kbp};
@@ -386,11 +395,11 @@ __global__ __launch_bounds__(256 * SPLIT) void fp8_few_up_kernel(const int32_t* 
         const int count = min(kFewRows, n - r0), mine = min(lane & 31, count - 1);
         __syncthreads();
         f32x16_t acc[2];
-        multiply_few<2, D, false>(
-            acc, m, tile, scale, wave % SPLIT, SPLIT,
+        multiply_few<2, 4, false>(
+            acc, m, tile, scale,
             [&] {
                 // 16 lanes a block
-                for (int i0 = 0; i0 < count * m.kb; i0 += 16 * SPLIT) {
+                for (int i0 = 0; i0 < count * m.kb; i0 += 16) {
                     const int i = i0 + tid / 16, r = min(i / m.kb, count - 1), b = i % m.kb, k = b * kBlk + tid % 16 * 8;
                     const size_t token = __shfl(pair, r0 + r, 64) / d.K;
                     if (i >= count * m.kb) continue;
@@ -420,12 +429,7 @@ __global__ __launch_bounds__(256 * SPLIT) void fp8_few_up_kernel(const int32_t* 
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float g = 0.0f, u = 0.0f;
-#pragma unroll
-                for (int s = 0; s < SPLIT; ++s) {
-                    g += part[t * SPLIT + s][0][i % 4][l + j];
-                    u += part[t * SPLIT + s][1][i % 4][l + j];
-                }
+                const float g = part[t][0][i % 4][l + j], u = part[t][1][i % 4][l + j];
                 v[j] = block * kBlk + c8 < d.I ? silu_times(g, u) : 0.0f;
             }
             put_block(v, act, to, block, tid % 16);
@@ -434,10 +438,11 @@ __global__ __launch_bounds__(256 * SPLIT) void fp8_few_up_kernel(const int32_t* 
 }
 
 // out for 32 columns and all tokens: the waves take the experts in turn, and a token's pairs are joined in k order.
-template <int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void fp8_few_down_kernel(const int32_t* __restrict__ topk,
-                                                                  const float* __restrict__ gates, F8Mat m, F8Rows act,
-                                                                  uint16_t* __restrict__ out, F8Dims d) {
+constexpr int kDownWaves = 8;
+__global__ __launch_bounds__(64 * kDownWaves) void fp8_few_down_kernel(const int32_t* __restrict__ topk,
+                                                                       const float* __restrict__ gates, F8Mat m,
+                                                                       F8Rows act, uint16_t* __restrict__ out,
+                                                                       F8Dims d) {
     __shared__ float y[kFewPairs][kCols];
     const int pairs = d.T * d.K, lane = threadIdx.x & 63, wave = wave_of(), col = blockIdx.x;
     const int id = pair_expert(topk, pairs, d.E);
@@ -446,7 +451,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_down_kernel(const int32_t*
         const int e = __builtin_amdgcn_readlane(id, __ffsll(left) - 1);
         const unsigned long long members = __ballot(id == e);
         left &= ~members;
-        if (turn % WAVES != wave) continue;
+        if (turn % kDownWaves != wave) continue;
         const int n = __popcll(members), pair = member_pair(members);
         const size_t tile[1] = {(size_t)e * (m.n / kCols) + col};
         const uint8_t* scale[1] = {m.scales + ((size_t)e * m.nb + col / 4) * m.kbp};
@@ -455,7 +460,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_down_kernel(const int32_t*
             const uint8_t *codes = act.codes + row * act.pitch + (lane >> 5) * 16, *scales = act.scales + row * act.sp;
             f32x16_t acc[1];
             multiply_few<1, 2, true>(
-                acc, m, tile, scale, 0, 1, [] {},
+                acc, m, tile, scale, [] {},
                 [&](int k, int p) { return *reinterpret_cast<const uint4*>(codes + (size_t)k * kBlk + p * 32); },
                 [&](int k) { return (int)scales[k]; });
 #pragma unroll
@@ -466,7 +471,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_few_down_kernel(const int32_t*
         }
     }
     __syncthreads();
-    for (int v = threadIdx.x; v < d.T * kCols; v += 64 * WAVES) {
+    for (int v = threadIdx.x; v < d.T * kCols; v += 64 * kDownWaves) {
         const int t = v / kCols, c = v % kCols;
         float s = 0.0f;
         for (int p = t * d.K; p < (t + 1) * d.K; ++p)
@@ -486,8 +491,11 @@ __device__ __forceinline__ float silu_fast(float g, float u) {
 // ---------------------------------------------------------------------------
 
 // Tiles of BM rows x 256 columns (UP: 128 gate and the 128 up columns that belong to them); eight waves
-// of BM / 2 x 64.  A stage is one block of 128 input values: BM rows of A and eight column tiles of B, copied
-// straight into LDS, NS stages in turn.
+// of BM / 2 x 64, two on a SIMD, whose results take half of its registers.  A stage is one block of 128 input values:
+// BM rows of A and eight column tiles of B, copied straight into LDS, NS stages in turn, as many as fit.
+// 8192 tokens, first product / second (us; 1570 / 1000 as it is): A in more and smaller units that are asked for earlier
+// 1716 / 1160, B straight to registers 1807 / 1228; operands read a row block earlier, or waves that start staggered,
+// no faster.  Without copies the matrix cores are busy 79 % of the time, without barriers too 82 %.
 template <int BM>
 struct F8Tile {
     static constexpr int MT = BM / 64;           // 32-row blocks of a wave
@@ -518,9 +526,9 @@ __device__ __forceinline__ float max_halves(float v) {
     return fmaxf(__uint_as_float(a), __uint_as_float(b));
 }
 
-// The 64 columns of y that a wave has of 32 rows, of which `valid` are there: float16 with one power of two that brings the largest of
-// them to 2^14 .. 2^15, half the bytes of float32 and off by at most 2^-11 (bf16 would be by 2^-8, as much as
-// the output's own rounding).  The stored byte is the largest one's exponent field; infinities and NaN, which
+// The 64 columns of y that a wave has of 32 rows, of which `valid` are there: float16 with one power of two that brings
+// the largest of them to 2^14 .. 2^15, half the bytes of float32 and off by at most 2^-11 of a value, or 2^-39 of the
+// largest (bf16 would be by 2^-8, as much as the output's own rounding).  The stored byte is the largest one's exponent field; infinities and NaN, which
 // have none, stay what they are.  A lane has 16 columns of each tile of one row, in fours, and the lane in the
 // other half of the wave the fours between: two of them make 16 bytes.
 __device__ __forceinline__ void put_y(const f32x16_t (&v)[2], const F8Ws& w, const F8Dims& d, size_t row0, int col,
@@ -575,7 +583,8 @@ __device__ __forceinline__ void put_y(const f32x16_t (&v)[2], const F8Ws& w, con
         for (int i = 0; i < 2; ++i) {
             const int r = (lane & 15) + i * 16;
             if (r < valid && c < d.H)
-                *reinterpret_cast<uint4*>(w.y16 + (row0 + r) * d.H + c) = make_uint4(h[k + i][0], h[k + i][1], h[k + i][2], h[k + i][3]);
+                *reinterpret_cast<uint4*>(w.y16 + (row0 + r) * d.H + c) =
+                    make_uint4(h[k + i][0], h[k + i][1], h[k + i][2], h[k + i][3]);
         }
     }
     if ((lane & 31) < valid && half == 0 && col < d.H) w.y16_exp[(row0 + lane) * w.y16_sp + col / 64] = (uint8_t)e;
@@ -769,7 +778,8 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
             constexpr int kind = decltype(kind_c)::value;
             const char* st = smem + cur * L::STAGE;
             const int nxt = cur + 1 == NS ? 0 : cur + 1;
-            const int w0 = sload(q.sb[0] + (s >> 2)) >> (8 * (s & 3)) & 255, w1 = sload(q.sb[1] + (s >> 2)) >> (8 * (s & 3)) & 255;
+            const int shift = 8 * (s & 3);
+            const int w0 = sload(q.sb[0] + (s >> 2)) >> shift & 255, w1 = sload(q.sb[1] + (s >> 2)) >> shift & 255;
             read_b(f1, st, 1);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -818,7 +828,8 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
         }
         while (s + NS < nst) {       // the scales of the next 16 stages, then those stages: no branch among these
             if ((s & 15) == 0 && s + 16 < nst) copy_scales(q, (s >> 4) + 1);
-            for (const int stop = min(nst - NS, (s & ~15) + 16); s < stop; ++s) stage(s, std::integral_constant<int, STEADY>{});
+            const int stop = min(nst - NS, (s & ~15) + 16);
+            for (; s < stop; ++s) stage(s, std::integral_constant<int, STEADY>{});
         }
         for (; s + 1 < nst; ++s) stage(s, std::integral_constant<int, MORE>{});
         stage(s, std::integral_constant<int, LAST>{});
@@ -896,6 +907,7 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__
     const int tok = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, vecs = d.H / 8;
     if (tok >= d.T) return;
     const int32_t* dest = w.dest + (size_t)tok * d.K;
+    const uint4* y16 = reinterpret_cast<const uint4*>(w.y16);
     const int v0 = blockIdx.y * 64 * VB;
     float acc[VB][8] = {};
 #pragma unroll 1
@@ -916,7 +928,7 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__
             for (int u = 0; u < VB; ++u) {
                 const int v = v0 + u * 64 + lane;
                 const bool there = row[j] >= 0 && v < vecs;
-                y[j][u] = there ? ld_nt(reinterpret_cast<const uint4*>(w.y16) + (size_t)row[j] * vecs + v) : make_uint4(0, 0, 0, 0);
+                y[j][u] = there ? ld_nt(y16 + (size_t)row[j] * vecs + v) : make_uint4(0, 0, 0, 0);
                 ex[j][u] = there ? w.y16_exp[(size_t)row[j] * w.y16_sp + v / 8] : 15;
             }
 #pragma unroll
@@ -1050,16 +1062,14 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
     hipStream_t s = static_cast<hipStream_t>(stream);
     const F8Mat up = f8_mat(w13_codes, w13_scales, d.H, 2 * d.I), down = f8_mat(w2_codes, w2_scales, d.I, d.H);
     if (f8_few(d)) {
-        constexpr int split = 1;
-        const int smem = std::max(kFewRows * (up.kb * kBlk + 16 + up.kb), 4 * split * 2 * 4 * 64 * 4);
-        const auto kernel = fp8_few_up_kernel<split, 4>;
-        if (smem > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+        const int smem = std::max(kFewRows * (up.kb * kBlk + 16 + up.kb), 4 * 2 * 4 * 64 * 4);
+        if (smem > 64 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(fp8_few_up_kernel),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, smem) != hipSuccess)
             return MOONEP_EHIP;
-        hipLaunchKernelGGL(kernel, dim3(blks(d.I), std::min(d.T * d.K, d.E)), dim3(256 * split), smem, s, topk,
+        hipLaunchKernelGGL(fp8_few_up_kernel, dim3(blks(d.I), std::min(d.T * d.K, d.E)), dim3(256), smem, s, topk,
                            static_cast<const uint16_t*>(x), up, w.act, d);
         MOONEP_LAUNCH_CHECK();
-        hipLaunchKernelGGL(fp8_few_down_kernel<8>, dim3(d.H / kCols), dim3(512), 0, s, topk, gates, down, w.act,
+        hipLaunchKernelGGL(fp8_few_down_kernel, dim3(d.H / kCols), dim3(64 * kDownWaves), 0, s, topk, gates, down, w.act,
                            static_cast<uint16_t*>(out), d);
         MOONEP_LAUNCH_CHECK();
         return MOONEP_OK;
@@ -1082,10 +1092,11 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
                                         : launch_both<256>(up, down, w, d, s);
     if (rc2 != MOONEP_OK) return rc2;
     uint4* o = static_cast<uint4*>(out);
+    const int quads = (d.T + 3) / 4, vecs = d.H / 8;
     if (d.T >= 4096)
-        hipLaunchKernelGGL((fp8_join_kernel<7, 1>), dim3((d.T + 3) / 4, (d.H / 8 + 447) / 448), dim3(256), 0, s, gates, w, o, d);
+        hipLaunchKernelGGL((fp8_join_kernel<7, 1>), dim3(quads, (vecs + 447) / 448), dim3(256), 0, s, gates, w, o, d);
     else
-        hipLaunchKernelGGL((fp8_join_kernel<1, 4>), dim3((d.T + 3) / 4, (d.H / 8 + 63) / 64), dim3(256), 0, s, gates, w, o, d);
+        hipLaunchKernelGGL((fp8_join_kernel<1, 4>), dim3(quads, (vecs + 63) / 64), dim3(256), 0, s, gates, w, o, d);
     MOONEP_LAUNCH_CHECK();
     return MOONEP_OK;
 }

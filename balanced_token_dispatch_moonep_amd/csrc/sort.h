@@ -12,7 +12,7 @@
 namespace moonep {
 
 constexpr int kSortWaves = 8;
-constexpr int kSortOnce = 2048;      // pairs that one workgroup sorts in one launch (5.0 us; 4096 pairs 8.8, in two launches 7.8)
+constexpr int kSortOnce = 2048;      // pairs that one workgroup sorts in one launch (5.0 us; 4096 8.8, two launches 7.8)
 constexpr int kSortParts = 256;      // workgroups of a larger sort, at most
 constexpr int kSortPart = 2048;      // pairs of one of them, at least
 
