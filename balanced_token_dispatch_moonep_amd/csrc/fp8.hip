@@ -494,8 +494,8 @@ __device__ __forceinline__ float silu_fast(float g, float u) {
 // of BM / 2 x 64, two on a SIMD, whose results take half of its registers.  A stage is one block of 128 input values:
 // BM rows of A and eight column tiles of B, copied straight into LDS, NS stages in turn, as many as fit.
 // 8192 tokens, first product / second (us; 1570 / 1000 as it is): A in more and smaller units that are asked for earlier
-// 1716 / 1160, B straight to registers 1807 / 1228; operands read a row block earlier, or waves that start staggered,
-// no faster.  Without copies the matrix cores are busy 79 % of the time, without barriers too 82 %.
+// 1716 / 1160, B straight to registers 1807 / 1228; four waves of 128 x 128, operands read a row block earlier, or waves
+// that start staggered, no faster: what waits less runs at a lower clock (all codes zero: 1370 / 920).
 template <int BM>
 struct F8Tile {
     static constexpr int MT = BM / 64;           // 32-row blocks of a wave

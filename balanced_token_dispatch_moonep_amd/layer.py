@@ -82,7 +82,8 @@ class Router:
 
     ``dims``: R, S, E and K count.  ``mode``: ROUTE_SOFTMAX, ROUTE_SOFTMAX_ALL or ROUTE_SIGMOID; ``scale`` multiplies
     the gates; ``bias`` [E] float32 or None moves the choice only (read at each call, so it may be updated in
-    place).  All buffers are static: a call replaces the outputs of the one before.
+    place).  A token with fewer than K logits above -inf gets ids of -1 with gates of 0, which the decoders pass over and
+    a layer's planner reports as out of range.  All buffers are static: a call replaces the outputs of the one before.
     """
 
     def __init__(self, dims: Dims, mode: int = ROUTE_SOFTMAX, scale: float = 1.0, bias=None, training: bool = False,
