@@ -601,7 +601,7 @@ def _sources_digest(call):
     """Digest of the code (comments excluded) of the call's kernel sources."""
     import hashlib
     csrc = os.path.join(ROOT, "balanced_token_dispatch_moonep_amd", "csrc")
-    files = KERNEL_SOURCES.get(call, ("gemm.hip",)) + ("common.h",)
+    files = KERNEL_SOURCES.get(call, ("gemm.hip", "dma.h")) + ("common.h",)
     h = hashlib.sha256()
     for f in files:
         with open(os.path.join(csrc, f), encoding="utf-8") as fh:
