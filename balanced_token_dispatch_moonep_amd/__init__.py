@@ -193,39 +193,37 @@ def moonep_version() -> str:
 # marshalling helpers
 # ----------------------------------------------------------------------------
 
-_TORCH = None
+_TORCH = _TENSOR = _DEVICE = None     # torch, its Tensor, and what tells the current device
 
 
 def _torch():
     """torch, imported with the first call that needs it."""
-    global _TORCH
+    global _TORCH, _TENSOR, _DEVICE
     if _TORCH is None:
         import torch
-        _TORCH = torch
+        _TENSOR, _DEVICE, _TORCH = torch.Tensor, torch._C._cuda_getDevice, torch
     return _TORCH
 
 
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else int(stream.cuda_stream)
-    c = _torch()._C
-    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return _torch()._C._cuda_getCurrentRawStream(_DEVICE())
 
 
 def _ptr(t, name, dtype=None, shape=None, numel=None, optional=False):
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is required")
-    torch = _TORCH or _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    if type(t) is not _TENSOR:
+        if t is None:
+            if optional:
+                return None
+            raise ValueError(f"{name} is required")
+        if not isinstance(t, _torch().Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
     device = t.get_device()
     if device < 0:
         raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
-    if device != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}; the library runs on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+    if device != _DEVICE():
+        raise ValueError(f"{name} is on {t.device}; the library runs on the current device cuda:{_DEVICE()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype:
@@ -600,43 +598,47 @@ def moonep_w4_ffn(d: Dims, topk, gates, x, w13_codes, w13_scales, w2_codes, w2_s
 # routing, and experts without a plan
 # ----------------------------------------------------------------------------
 
-def _logits(d: Dims, logits, mode):
-    """The address of the logits [R, S, E], float32 or bf16, and the mode with their type."""
+def _route_mode(logits, mode):
+    """The mode with the logits' type, float32 or bf16."""
     torch = _torch()
-    at = _ptr(logits, "logits", None, (d.R, d.S, d.E))
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     if mode not in (ROUTE_SOFTMAX, ROUTE_SOFTMAX_ALL, ROUTE_SIGMOID):
         raise ValueError(f"unknown mode {mode!r}")
-    return at, mode | (_ROUTE_BF16 if logits.dtype == torch.bfloat16 else 0)
+    dtype = logits.dtype
+    if dtype is torch.float32:
+        return mode
+    if dtype is torch.bfloat16:
+        return mode | _ROUTE_BF16
+    raise ValueError(f"logits must be float32 or bfloat16, got {dtype}")
 
 
 def moonep_route(d: Dims, logits, bias, topk, gates, mode=ROUTE_SOFTMAX, scale=1.0, stream=None) -> None:
     """topk and gates [R, S, K] of the logits [R, S, E] (float32 or bf16), best first; bias [E] float32 or
     None moves the choice only.  Where fewer than K logits are above -inf: id -1, gate 0."""
     torch = _torch()
-    at, mode = _logits(d, logits, mode)
-    args = (
-        at,
-        _ptr(bias, "bias", torch.float32, (d.E,), optional=True),
-        _ptr(topk, "topk", torch.int32, (d.R, d.S, d.K)),
-        _ptr(gates, "gates", torch.float32, (d.R, d.S, d.K)),
-    )
-    _check(_lib().moonep_route(ctypes.byref(d), mode, float(scale), *args, _stream(stream)), "moonep_route")
+    R, S, E = d.R, d.S, d.E
+    picks = (R, S, d.K)
+    at = _ptr(logits, "logits", None, (R, S, E))
+    _check(_lib().moonep_route(
+        ctypes.byref(d), _route_mode(logits, mode), float(scale), at,
+        None if bias is None else _ptr(bias, "bias", torch.float32, (E,)),
+        _ptr(topk, "topk", torch.int32, picks),
+        _ptr(gates, "gates", torch.float32, picks),
+        _stream(stream)), "moonep_route")
 
 
 def moonep_route_backward(d: Dims, dgates, logits, topk, dlogits, mode=ROUTE_SOFTMAX, scale=1.0, stream=None) -> None:
     """dlogits [R, S, E] (type of the logits) from dgates [R, S, K] float32, for the topk of the forward."""
     torch = _torch()
-    at, mode = _logits(d, logits, mode)
-    args = (
-        _ptr(dgates, "dgates", torch.float32, (d.R, d.S, d.K)),
+    R, S = d.R, d.S
+    picks, row = (R, S, d.K), (R, S, d.E)
+    at = _ptr(logits, "logits", None, row)
+    _check(_lib().moonep_route_backward(
+        ctypes.byref(d), _route_mode(logits, mode), float(scale),
+        _ptr(dgates, "dgates", torch.float32, picks),
         at,
-        _ptr(topk, "topk", torch.int32, (d.R, d.S, d.K)),
-        _ptr(dlogits, "dlogits", logits.dtype, (d.R, d.S, d.E)),
-    )
-    _check(_lib().moonep_route_backward(ctypes.byref(d), mode, float(scale), *args, _stream(stream)),
-           "moonep_route_backward")
+        _ptr(topk, "topk", torch.int32, picks),
+        _ptr(dlogits, "dlogits", logits.dtype, row),
+        _stream(stream)), "moonep_route_backward")
 
 
 def moonep_sort_workspace_bytes(d: Dims) -> int:
@@ -647,15 +649,15 @@ def moonep_sort(d: Dims, topk, ws, offsets, dest, pair=None, stream=None) -> Non
     """Rows grouped by expert without a plan: offsets [E + 1], dest [R, S, K] (-1 for an id outside [0, E)),
     pair [R*S*K] (the pair of each row; None if not needed), all int32."""
     torch = _torch()
-    i32 = torch.int32
-    args = (
-        _ptr(topk, "topk", i32, (d.R, d.S, d.K)),
+    i32, picks = torch.int32, (d.R, d.S, d.K)
+    _check(_lib().moonep_sort(
+        ctypes.byref(d),
+        _ptr(topk, "topk", i32, picks),
         _ptr(ws, "ws", torch.uint8, numel=moonep_sort_workspace_bytes(d)),
         _ptr(offsets, "offsets", i32, (d.E + 1,)),
-        _ptr(dest, "dest", i32, (d.R, d.S, d.K)),
-        _ptr(pair, "pair", i32, (d.R * d.S * d.K,), optional=True),
-    )
-    _check(_lib().moonep_sort(ctypes.byref(d), *args, _stream(stream)), "moonep_sort")
+        _ptr(dest, "dest", i32, picks),
+        None if pair is None else _ptr(pair, "pair", i32, (picks[0] * picks[1] * picks[2],)),
+        _stream(stream)), "moonep_sort")
 
 
 def moonep_combine_backward(d: Dims, dest, y, gates, dout, dy, dgates, stream=None) -> None:
@@ -663,16 +665,17 @@ def moonep_combine_backward(d: Dims, dest, y, gates, dout, dy, dgates, stream=No
     None, y too without dgates."""
     torch = _torch()
     rt, f32 = _rows_dtype(d), torch.float32
-    M = d.R * d.S * d.K
-    args = (
-        _ptr(dest, "dest", torch.int32, (d.R, d.S, d.K)),
-        _ptr(y, "y", rt, (M, d.H), optional=dgates is None),
-        _ptr(gates, "gates", f32, (d.R, d.S, d.K), optional=True),
-        _ptr(dout, "dout", rt, (d.R, d.S, d.H)),
-        _ptr(dy, "dy", rt, (M, d.H), optional=True),
-        _ptr(dgates, "dgates", f32, (d.R, d.S, d.K), optional=True),
-    )
-    _check(_lib().moonep_combine_backward(ctypes.byref(d), *args, _stream(stream)), "moonep_combine_backward")
+    R, S, K, H = d.R, d.S, d.K, d.H
+    picks, rows = (R, S, K), (R * S * K, H)
+    _check(_lib().moonep_combine_backward(
+        ctypes.byref(d),
+        _ptr(dest, "dest", torch.int32, picks),
+        _ptr(y, "y", rt, rows, optional=dgates is None),
+        _ptr(gates, "gates", f32, picks, optional=True),
+        _ptr(dout, "dout", rt, (R, S, H)),
+        _ptr(dy, "dy", rt, rows, optional=True),
+        _ptr(dgates, "dgates", f32, picks, optional=True),
+        _stream(stream)), "moonep_combine_backward")
 
 
 def _fp8_code(Kin: int, N: int) -> int:
@@ -706,21 +709,30 @@ def moonep_fp8_ffn_workspace_bytes(d: Dims) -> int:
     return _dims_bytes("moonep_fp8_ffn_workspace_bytes", bytes(d))
 
 
+@functools.lru_cache(maxsize=1024)
+def _fp8_shapes(dims: bytes):
+    """What moonep_fp8_ffn of these dims takes: the shapes of picks, rows, codes and scales, and the scratch's bytes."""
+    d = Dims.from_buffer_copy(dims)
+    wsb = moonep_fp8_ffn_workspace_bytes(d)
+    weights = [(d.E, f(*size)) for size in ((d.H, 2 * d.I), (d.I, d.H)) for f in (moonep_fp8_code_bytes, moonep_fp8_scale_bytes)]
+    return (d.R, d.S, d.K), (d.R, d.S, d.H), *weights, wsb
+
+
 def moonep_fp8_ffn(d: Dims, topk, gates, x, w13_codes, w13_scales, w2_codes, w2_scales, ws, out, stream=None) -> None:
     """out [R, S, H] = the gated sum of each token's experts' FFN, weights and rows in 8 bits
     (moonep_quantize_fp8 of w13 [E, H, 2I] and w2 [E, I, H]).  Ids outside [0, E) add nothing."""
     torch = _torch()
     u8, bf = torch.uint8, torch.bfloat16
-    wsb = moonep_fp8_ffn_workspace_bytes(d)
-    args = (
-        _ptr(topk, "topk", torch.int32, (d.R, d.S, d.K)),
-        _ptr(gates, "gates", torch.float32, (d.R, d.S, d.K)),
-        _ptr(x, "x", bf, (d.R, d.S, d.H)),
-        _ptr(w13_codes, "w13_codes", u8, (d.E, moonep_fp8_code_bytes(d.H, 2 * d.I))),
-        _ptr(w13_scales, "w13_scales", u8, (d.E, moonep_fp8_scale_bytes(d.H, 2 * d.I))),
-        _ptr(w2_codes, "w2_codes", u8, (d.E, moonep_fp8_code_bytes(d.I, d.H))),
-        _ptr(w2_scales, "w2_scales", u8, (d.E, moonep_fp8_scale_bytes(d.I, d.H))),
+    picks, rows, c13, s13, c2, s2, wsb = _fp8_shapes(bytes(d))
+    _check(_lib().moonep_fp8_ffn(
+        ctypes.byref(d),
+        _ptr(topk, "topk", torch.int32, picks),
+        _ptr(gates, "gates", torch.float32, picks),
+        _ptr(x, "x", bf, rows),
+        _ptr(w13_codes, "w13_codes", u8, c13),
+        _ptr(w13_scales, "w13_scales", u8, s13),
+        _ptr(w2_codes, "w2_codes", u8, c2),
+        _ptr(w2_scales, "w2_scales", u8, s2),
         _ptr(ws, "ws", u8, numel=wsb),
-        _ptr(out, "out", bf, (d.R, d.S, d.H)),
-    )
-    _check(_lib().moonep_fp8_ffn(ctypes.byref(d), *args, _stream(stream)), "moonep_fp8_ffn")
+        _ptr(out, "out", bf, rows),
+        _stream(stream)), "moonep_fp8_ffn")
