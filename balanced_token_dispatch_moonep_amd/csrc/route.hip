@@ -16,7 +16,7 @@
 // Sixteen lanes share a row, so that four rows go through a wave and every step across lanes is a rotation
 // inside 16 lanes, an operand modifier instead of an instruction through LDS.  Where rows are too few to fill the
 // chip, all 64 lanes share one: a quarter of the elements to rank for two more steps (one token over 256 experts,
-// with a bias: 10.5 us, with 64 lanes 7.6, which is what the host needs for a call).  A lane's elements are groups of
+// with a bias: 10.5 us a call, with 64 lanes 7.0, which is what the host needs for it).  A lane's elements are groups of
 // VEC side by side, the lanes' groups next to each other, so that a load of the lanes is one piece of the row.
 #include "common.h"
 
