@@ -9,7 +9,7 @@
 //
 // What bounds it (32 experts of H 7168 and I 2048, 8 a token; a call, inputs changing):
 //   1 token       70 us   reading 352 MB of weights, 5.0 TB/s: the first product has 128 workgroups
-//   64 tokens    266 us   reading 1409 MB, 5.5 TB/s in the products; 18 us to sort, round and join
+//   64 tokens    266 us   reading 1409 MB, 5.5 TB/s in the products; 17 us to sort, round and join
 //   512 tokens   350 us   the same weights, in whole rounds of tiles (3.1 of the first product): 4.2 TB/s
 //   8192 tokens 2770 us   matrix instructions: 2.1 PFLOP/s in all, 2.3 to 2.5 in the first product, where the matrix
 //                         cores are busy 67 to 71 % of the time at the 1.8 GHz that power leaves; the second stores its
@@ -202,7 +202,7 @@ __device__ __forceinline__ void round_row(const uint16_t* x, const F8Ws& w, cons
 }
 
 // All that comes before the products, up to kSortOnce pairs: one workgroup sorts and lists, and the others round x
-// meanwhile (512 pairs 9.7 us; 4096 pairs 20, as three launches take).
+// meanwhile (512 pairs 8.5 us; 4096 pairs 20, three launches 17).
 __global__ __launch_bounds__(64 * kSortWaves) void fp8_begin_kernel(const uint16_t* __restrict__ x, SortArgs a, F8Ws w,
                                                                     F8Dims d) {
     constexpr int NT = 64 * kSortWaves;

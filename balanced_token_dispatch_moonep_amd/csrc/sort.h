@@ -12,9 +12,11 @@
 namespace moonep {
 
 constexpr int kSortWaves = 8;
-constexpr int kSortOnce = 2048;      // pairs that one workgroup sorts in one launch (5.0 us; 4096 8.8, two launches 7.8)
+constexpr int kSortOnce = 2048;      // pairs that one workgroup sorts in one launch (5.1 us; 4096 8.8, two launches 6.9)
 constexpr int kSortParts = 256;      // workgroups of a larger sort, at most
-constexpr int kSortPart = 2048;      // pairs of one of them, at least
+// Pairs of one of them, at least: each reads the counts of all.  Parts of 1024 / 2048 pairs (us, 256 experts): 8192 pairs
+// 7.2 / 8.1, 32768 7.5 / 9.1, 65536 8.2 / 8.9, 262144 12.4 / 11.3, and of 1024 experts 25 / 18.
+constexpr int kSortPart = 1024, kSortLargePart = 2048, kSortLarge = 1 << 16;
 
 // Runs of an expert's rows for the workgroups of a product: run i covers rows first .. first + n of expert e.
 struct Run {
@@ -42,20 +44,21 @@ inline SortArgs sort_args(int P, int E) {
     } else {
         // whole rounds of the workgroup's waves
         constexpr int round = kSortWaves * 64;
-        a.part = std::max(kSortPart, (P + kSortParts - 1) / kSortParts);
+        a.part = std::max(P <= kSortLarge ? kSortPart : kSortLargePart, (P + kSortParts - 1) / kSortParts);
         a.part = (a.part + round - 1) / round * round;
         a.parts = (P + a.part - 1) / a.part;
     }
     return a;
 }
-// The most that a sort of up to P pairs takes.
+// What a sort of up to P pairs takes, at most.
 inline size_t sort_hist_most(int64_t P, int E) {
-    return P > kSortOnce ? (size_t)std::min<int64_t>((P + kSortPart - 1) / kSortPart, kSortParts) * ((E + 1) / 2) * 8 : 0;
+    const int64_t small = (std::min<int64_t>(P, kSortLarge) + kSortPart - 1) / kSortPart;
+    const int64_t parts = std::max(small, std::min<int64_t>((P + kSortLargePart - 1) / kSortLargePart, kSortParts));
+    return P > kSortOnce ? (size_t)parts * ((E + 1) / 2) * 8 : 0;
 }
-inline size_t sort_hist_bytes(const SortArgs& a) { return a.parts > 1 ? (size_t)a.parts * ((a.E + 1) / 2) * 8 : 0; }
 int launch_sort(const SortArgs& a, hipStream_t s);
 
-constexpr int kKept = 4;             // rounds of 64 pairs: a wave's share of kSortPart
+constexpr int kKept = 4;             // rounds of 64 pairs: a wave's share of kSortLargePart
 
 // Lanes of the wave with this lane's id; ids below 2^bits.
 __device__ __forceinline__ unsigned long long same_id(int id, bool valid, int bits) {
@@ -207,9 +210,11 @@ __device__ __forceinline__ void sort_place(const SortArgs& a, int part) {
     };
     unsigned long long same[kKept];
 #pragma unroll
-    for (int r = 0; r < kKept; ++r) same[r] = same_id(kept[r], (unsigned)kept[r] < (unsigned)a.E, bits);
+    for (int r = 0; r < kKept; ++r)
+        if (r < rounds) same[r] = same_id(kept[r], (unsigned)kept[r] < (unsigned)a.E, bits);
 #pragma unroll
-    for (int r = 0; r < kKept; ++r) place(first + r * 64 + lane, kept[r], (unsigned)kept[r] < (unsigned)a.E, same[r]);
+    for (int r = 0; r < kKept; ++r)
+        if (r < rounds) place(first + r * 64 + lane, kept[r], (unsigned)kept[r] < (unsigned)a.E, same[r]);
     for (int p0 = first + kKept * 64; p0 < last; p0 += 64) {
         const int p = p0 + lane;
         const int id = p < last ? a.topk[p] : -1;

@@ -280,9 +280,11 @@ def _check_sort(topk, E, **kw):
         assert (got[n:] == -7).all()                         # behind the last row: left as they were
 
 
-# one workgroup's rounds and waves, its limit of 4096 pairs, several parts of 2048, the last of them short
+# one workgroup's rounds and waves, its limit of 2048 pairs, several parts of 1024 and (over 65536 pairs) 2048, the last of
+# them short
 @pytest.mark.parametrize("T,K,E", [(1, 1, 1), (1, 8, 256), (63, 1, 5), (64, 1, 5), (65, 1, 5), (128, 8, 256), (511, 1, 3),
                                    (513, 1, 3), (512, 8, 1024), (4096, 1, 2), (4097, 1, 500), (1024, 8, 1024), (8193, 1, 7), (4097, 2, 1), (1250, 10, 33), (20011, 15, 1024),
+                                   (2048, 1, 6), (2049, 1, 6), (16384, 4, 300), (16385, 4, 300),
                                    (262144, 4, 256), (70000, 16, 1000)])
 def test_sort(T, K, E):
     say("sort", T, K, E)

@@ -104,8 +104,9 @@ def test_sort_refuses():
 def test_sort_workspace():
     size = lambda **kw: M.moonep_sort_workspace_bytes(_dims(**kw))
     assert size() == size(S=256) == 256                      # one workgroup keeps all of it
-    assert size(S=1025) == 768 and 5 * 32 * 4 == 640         # five parts of 2048 pairs, in whole 256 bytes
-    assert size(S=1025, E=31) == 768                         # an even number of experts
+    assert size(S=1025) == 1280 and 9 * 32 * 4 == 1152       # nine parts of 1024 pairs, in whole 256 bytes
+    assert size(S=1025, E=31) == 1280                        # an even number of experts
+    assert size(S=8192) == size(S=8193) == 64 * 32 * 4       # parts of 2048 pairs: 33, and room for 64 smaller ones
     assert size(S=1 << 26, K=16, E=1024) == 256 * 1024 * 4   # the most parts
 
 
