@@ -87,14 +87,6 @@ static int f8_rows(const F8Dims& d) {
     return pairs < 48ll * d.E ? 64 : pairs < 192ll * d.E ? 128 : 256;
 }
 
-// Whether tiles of 64 rows widen their codes: calls of so few values between the two products that one of them on the wrong
-// side of a border between codes shows in the output's error (the 8-bit instructions put some 4 in 10000 there, which adds
-// a quarter to the error of 2^-9.2 that the output's rounding leaves).  More values take the 8-bit instructions: 64 tokens 258 us
-// instead of 268 (experts as above), of 8 experts of H 4096 and I 1024 38 instead of 49.
-static bool f8_exact(const F8Dims& d) {
-    return f8_rows(d) == 64 && (int64_t)d.T * d.K * d.I < 1 << 14;
-}
-
 static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
     const size_t pairs = (size_t)d.T * d.K, experts = std::min<size_t>(pairs, d.E);
     F8Ws w{};
@@ -614,8 +606,7 @@ struct F8TileIn {
     int nt, row0, rows;
 };
 
-// EXACT: with codes widened to bf16, as multiply_few does.
-template <int BM, bool UP, bool EXACT>
+template <int BM, bool UP>
 __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dims d) {
     using L = F8Tile<BM>;
     constexpr int MT = L::MT, NS = L::NS, PER = L::PER;
@@ -758,9 +749,10 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
         for (int i = 0; i < MT; ++i) read_a(f0, smem, 0, i);
         // The products so far are asked for before what follows: they have no effect that keeps their place, and
         // moved behind a branch they hold the operands' registers.  (No instruction reads them here.)
-        // acc += rows times one column tile, one slice.
+        // acc += rows times one column tile, one slice.  Tiles of 64 rows, which few rows an expert fill, take the time that
+        // reading their weights takes, and widen their operands as multiply_few does.
         auto product = [&](f32x16_t& sum, const i32x8_t& a, const i32x8_t& b, int sa, int sb) {
-            if constexpr (EXACT) {
+            if constexpr (BM == 64) {
 #pragma unroll
                 for (int h = 0; h < 8; h += 2)
                     sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b[h], b[h + 1], scale_of(sb)),
@@ -862,7 +854,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const float g = acc[i][0][r], u = acc[i][1][r];
-                    const float v = !real ? 0.0f : EXACT ? silu_times(g, u) : silu_fast(g, u);
+                    const float v = !real ? 0.0f : BM == 64 ? silu_times(g, u) : silu_fast(g, u);
                     top = max(top, __float_as_uint(v) & 0x7fffffffu);
                     acc[i][0][r] = v;
                 }
@@ -969,9 +961,9 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__
 // host
 // ---------------------------------------------------------------------------
 
-template <int BM, bool UP, bool EXACT>
+template <int BM, bool UP>
 static int launch_tiles(const F8Mat& m, const F8Ws& w, const F8Dims& d, hipStream_t s) {
-    const auto kernel = fp8_tile_kernel<BM, UP, EXACT>;
+    const auto kernel = fp8_tile_kernel<BM, UP>;
     constexpr int smem = F8Tile<BM>::SMEM;
     if (hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         hipSuccess)
@@ -981,10 +973,10 @@ static int launch_tiles(const F8Mat& m, const F8Ws& w, const F8Dims& d, hipStrea
     return MOONEP_OK;
 }
 
-template <int BM, bool EXACT = false>
+template <int BM>
 static int launch_both(const F8Mat& up, const F8Mat& down, const F8Ws& w, const F8Dims& d, hipStream_t s) {
-    const int rc = launch_tiles<BM, true, EXACT>(up, w, d, s);
-    return rc != MOONEP_OK ? rc : launch_tiles<BM, false, EXACT>(down, w, d, s);
+    const int rc = launch_tiles<BM, true>(up, w, d, s);
+    return rc != MOONEP_OK ? rc : launch_tiles<BM, false>(down, w, d, s);
 }
 
 static bool f8_size(int32_t kin, int32_t n) {
@@ -1095,8 +1087,7 @@ extern "C" int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, co
                            s, static_cast<const uint16_t*>(x), w, d);
     }
     MOONEP_LAUNCH_CHECK();
-    const int rc2 = f8_exact(d)          ? launch_both<64, true>(up, down, w, d, s)
-                    : w.run_rows == 64  ? launch_both<64>(up, down, w, d, s)
+    const int rc2 = w.run_rows == 64 ? launch_both<64>(up, down, w, d, s)
                     : w.run_rows == 128 ? launch_both<128>(up, down, w, d, s)
                                         : launch_both<256>(up, down, w, d, s);
     if (rc2 != MOONEP_OK) return rc2;
