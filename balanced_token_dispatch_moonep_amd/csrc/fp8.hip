@@ -79,12 +79,12 @@ static bool f8_few(const F8Dims& d) {
 }
 
 // Rows of a tile otherwise: by the pairs that an expert has on average, with which more rows that are not there meet
-// fewer reads of a weight.  Tiles of 64 / 128 / 256 rows (us, experts as above): 16 pairs an expert 259 / 266 / 315, 64 309
-// / 286 / 335, 128 414 / 360 / 381, 192 530 / 483 / 470, 512 1158 / 913 / 839; 8 experts of H 4096 and I 1024: 128 51
-// / 55 / 74, 512 121 / 115 / 108.
+// fewer reads of a weight.  Tiles of 64 / 128 / 256 rows (us, experts as above): 16 pairs an expert 268 / 262 / 315, 32 275
+// / 267 / -, 40 315 / 272 / -, 64 335 / 282 / 335, 128 - / 360 / 381, 192 - / 483 / 470, 512 - / 913 / 839; 8 experts of
+// H 4096 and I 1024: 128 - / 55 / 74, 512 - / 115 / 108.  (Tiles of 64 rows are the exact ones, below.)
 static int f8_rows(const F8Dims& d) {
     const int64_t pairs = (int64_t)d.T * d.K;
-    return pairs < 48ll * d.E ? 64 : pairs < 192ll * d.E ? 128 : 256;
+    return pairs < 36ll * d.E ? 64 : pairs < 192ll * d.E ? 128 : 256;
 }
 
 static size_t f8_ws_layout(const F8Dims& d, void* base, F8Ws* ws) {
@@ -750,7 +750,10 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
         // The products so far are asked for before what follows: they have no effect that keeps their place, and
         // moved behind a branch they hold the operands' registers.  (No instruction reads them here.)
         // acc += rows times one column tile, one slice.  Tiles of 64 rows, which few rows an expert fill, take the time that
-        // reading their weights takes, and widen their operands as multiply_few does.
+        // reading their weights takes, and widen their operands as multiply_few does (64 tokens 268 us, with the 8-bit
+        // instructions 258, and 128 rows a tile 264; with weights that the caches hold 49, 38 and 44 for 64 tokens of 8 experts
+        // of H 4096 and I 1024: but then the output is off by 0.0019 to 0.0024 instead of 0.0017, unevenly where it
+        // has few values, as some 4 in 10000 of act take another code).
         auto product = [&](f32x16_t& sum, const i32x8_t& a, const i32x8_t& b, int sa, int sb) {
             if constexpr (BM == 64) {
 #pragma unroll
