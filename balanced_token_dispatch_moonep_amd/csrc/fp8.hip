@@ -9,7 +9,7 @@
 //
 // What bounds it (32 experts of H 7168 and I 2048, 8 a token; a call, inputs changing):
 //   1 token       70 us   reading 352 MB of weights, 5.0 TB/s: the first product has 128 workgroups
-//   64 tokens    266 us   reading 1409 MB, 5.5 TB/s in the products; 17 us to sort, round and join
+//   64 tokens    260 us   reading 1409 MB, 5.7 TB/s in the products; 17 us to sort, round and join
 //   512 tokens   350 us   the same weights, in whole rounds of tiles (3.1 of the first product): 4.2 TB/s
 //   8192 tokens 2770 us   matrix instructions: 2.1 PFLOP/s in all, 2.3 to 2.5 in the first product, where the matrix
 //                         cores are busy 67 to 71 % of the time at the 1.8 GHz that power leaves; the second stores its
@@ -79,7 +79,7 @@ static bool f8_few(const F8Dims& d) {
 }
 
 // Rows of a tile otherwise: by the pairs that an expert has on average, with which more rows that are not there meet
-// fewer reads of a weight.  Tiles of 64 / 128 / 256 rows (us, experts as above): 16 pairs an expert 268 / 262 / 315, 32 275
+// fewer reads of a weight.  Tiles of 64 / 128 / 256 rows (us, experts as above): 16 pairs an expert 262 / 262 / 315, 32 272
 // / 267 / -, 40 315 / 272 / -, 64 335 / 282 / 335, 128 - / 360 / 381, 192 - / 483 / 470, 512 - / 913 / 839; 8 experts of
 // H 4096 and I 1024: 128 - / 55 / 74, 512 - / 115 / 108.  (Tiles of 64 rows are the exact ones, below.)
 static int f8_rows(const F8Dims& d) {
@@ -750,12 +750,16 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(F8Mat m, F8Ws w, F8Dim
         // The products so far are asked for before what follows: they have no effect that keeps their place, and
         // moved behind a branch they hold the operands' registers.  (No instruction reads them here.)
         // acc += rows times one column tile, one slice.  Tiles of 64 rows, which few rows an expert fill, take the time that
-        // reading their weights takes, and widen their operands as multiply_few does (64 tokens 268 us, with the 8-bit
-        // instructions 258, and 128 rows a tile 264; with weights that the caches hold 49, 38 and 44 for 64 tokens of 8 experts
+        // reading their weights takes, and widen their operands as multiply_few does (64 tokens 262 us, with the 8-bit
+        // instructions 258, and 128 rows a tile 262; with weights that the caches hold 46, 38 and 44 for 64 tokens of 8 experts
         // of H 4096 and I 1024: but then the output is off by 0.0019 to 0.0024 instead of 0.0017, unevenly where it
         // has few values, as some 4 in 10000 of act take another code).
+        // None of the wave's rows is there: in tiles of 64 rows it multiplies nothing (64 tokens 268 -> 262 us; where tiles
+        // are fuller 1 to 4 % slower).
+        const bool idle = wm * (BM / 2) >= q.rows;
         auto product = [&](f32x16_t& sum, const i32x8_t& a, const i32x8_t& b, int sa, int sb) {
             if constexpr (BM == 64) {
+                if (idle) return;
 #pragma unroll
                 for (int h = 0; h < 8; h += 2)
                     sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b[h], b[h + 1], scale_of(sb)),
