@@ -201,7 +201,7 @@ def _torch():
     global _TORCH, _TENSOR, _DEVICE
     if _TORCH is None:
         import torch
-        _TENSOR, _DEVICE, _TORCH = torch.Tensor, torch._C._cuda_getDevice, torch
+        _TENSOR, _DEVICE, _TORCH = torch.Tensor, getattr(torch._C, "_cuda_getDevice", None), torch
     return _TORCH
 
 
