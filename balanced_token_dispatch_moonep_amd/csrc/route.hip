@@ -274,14 +274,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         next_picks<LANES, KM, 0>(best, pick, a.K, lane);
         mine = ranked_id(pick);
     } else {
-        // finite keys are below 2^130: infinity and NaN are larger ones, so that all are numbers
+        // finite keys are below 2^130: infinity and NaN are larger ones, so that all are numbers.  What either -inf takes
+        // out is none of these, though the sum with a logit that is not finite is NaN.
         double key[NE];
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const int e = index_of<LANES, VEC>(i, lane);
-            const double b = e < a.E ? a.bias[e] : 0.0f;
-            const double v = b + (a.mode == MOONEP_ROUTE_SIGMOID ? 1.0 / (1.0 + exp(-(double)x[i])) : (double)x[i]);
-            key[i] = x[i] == -__builtin_inff() ? kNoKey : v != v ? 0x1p201 : fmin(fmax(v, kNoKey), 0x1p200);
+            const float b = e < a.E ? a.bias[e] : 0.0f;
+            const bool out = x[i] == -__builtin_inff() || b == -__builtin_inff();
+            const double v = (a.mode == MOONEP_ROUTE_SIGMOID ? 1.0 / (1.0 + exp(-(double)x[i])) : (double)x[i]) + b;
+            key[i] = out ? kNoKey : v != v ? 0x1p201 : fmin(fmax(v, kNoKey), 0x1p200);
         }
         for (int k = 0; k < a.K; ++k) {      // first the largest key, then the lowest of the ids that have it
             double best = key[0];

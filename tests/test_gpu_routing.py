@@ -896,3 +896,28 @@ def test_launches_go_to_the_stream_given():
         for v, ref in zip(outs, want):
             assert torch.equal(v, ref)
             v.zero_()
+
+
+# ----------------------------------------------------------------------------
+# masked experts, borders of codes, and workgroups that take several tiles
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("E,K,T", [(4, 4, 6), (70, 16, 30), (256, 8, 4200), (1000, 3, 4200)])
+def test_route_bias_masks_whatever_the_logit(E, K, T, mode):
+    """A bias of -inf takes an expert out, also one whose logit is NaN or infinite."""
+    say("masked by the bias", mode, E, K, T)
+    rng = np.random.default_rng(E)
+    z = (2 * rng.standard_normal((T, E))).astype(np.float32)
+    b = rng.standard_normal(E).astype(np.float32)
+    off = rng.permutation(E)[:E // 2]
+    b[off] = -np.inf
+    bad = np.array([np.nan, np.inf, -np.inf, 3e38, 0.0, -np.nan], np.float32)
+    z[:, off] = bad[rng.integers(0, 6, (T, len(off)))]
+    ids, gates = _route(f32(z), f32(b), K, mode)
+    z[:, off] = -np.inf                                      # picked as if the logits were
+    some = np.unique(np.r_[:min(T, 40), max(T - 40, 0):T])
+    want, ref, tol = G.route(z[some], b, K, mode)
+    np.testing.assert_array_equal(ids.cpu().numpy()[some], want)
+    if mode != "softmax_all":                                # whose gates are made of every logit
+        _near(gates.double().cpu().numpy()[some], ref, tol, "gates")
