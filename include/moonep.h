@@ -357,8 +357,9 @@ int moonep_w4_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* g
  * the lower id.  The key is the logit; with a bias the logit plus the bias, or in SIGMOID the logit's sigmoid
  * plus the bias, in float64 (the bias moves the choice only, no gate).  An expert whose logit or bias is -inf is
  * never picked, whatever the other of them is; where fewer than K are left the id is -1 and the gate 0 (moonep_sort
- * and the decoders take such ids, moonep_plan does not).  A NaN key ranks above all others, and a NaN or +inf among
- * the logits that gates are made of makes the token's gates NaN.  Gates in float32, times scale (finite).
+ * and the decoders take such ids, moonep_plan does not).  A NaN key ranks above all others.  Gates are made of the picked
+ * logits, in SOFTMAX_ALL of all E: a NaN among those makes the token's gates NaN, and so does +inf in SOFTMAX and
+ * SOFTMAX_ALL; in SIGMOID +inf counts as what it is, a sigmoid of 1.  Gates in float32, times scale (finite).
  * Only R, S, K and E of dims matter (E to 1024, K to min(E, 16); MOONEP_ENOTSUP over 2^27 tokens).
  *   logits [R, S, E] float32 or bf16;  bias [E] float32 or NULL
  *   topk   [R, S, K] int32 out;  gates [R, S, K] float32 out
