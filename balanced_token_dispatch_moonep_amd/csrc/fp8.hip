@@ -480,10 +480,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void fp8_few_down_kernel(const int
     }
 }
 
-// The same with the hardware's exponential and reciprocal: off by some 2^-22, far below what the 8-bit products
-// before it are off by.
+// The same with the hardware's exponential and reciprocal, each off by up to 2^-23 of its value.  2^t has the rounding of t
+// in it, |g| 2^-24 of the value; exp(-g) is 2^t (1 + d), where d is what t log(2) leaves of -g, with log(2) in two parts.
+// In all 8 roundings of 2^-24 at most: exponential and its correction 3, sum 1, reciprocal 2, products 2.  (h keeps t finite
+// for large g; t is held below 128, so that for g below -89, whose d is large then, the exponential is infinite.  From -87
+// on the reciprocal may be 0, and the result with it, which is less than 2^-119 |u| there.  Without d, off by up to 66 roundings,
+// 8192 tokens take 2809 instead of 2819 us.)
 __device__ __forceinline__ float silu_fast(float g, float u) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+    const float h = fminf(g, 126.0f), t = fminf(h * -1.44269504089f, 127.99f);
+    const float d = fmaf(t, 0x1.05c61p-29f, fmaf(t, -0x1.62e43p-1f, -h)), e = __builtin_amdgcn_exp2f(t);
+    return g * __builtin_amdgcn_rcpf(1.0f + fmaf(e, d, e)) * u;
 }
 
 // ---------------------------------------------------------------------------

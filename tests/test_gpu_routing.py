@@ -921,3 +921,83 @@ def test_route_bias_masks_whatever_the_logit(E, K, T, mode):
     np.testing.assert_array_equal(ids.cpu().numpy()[some], want)
     if mode != "softmax_all":                                # whose gates are made of every logit
         _near(gates.double().cpu().numpy()[some], ref, tol, "gates")
+
+
+def _next_to_borders(rng, a, k, n=1 << 21):
+    """Gates and ups (g, u) of 128 columns, each a sum of three codes over 1, 16 and 256: the first has the largest
+    silu(g) u, and as many as there are lie so close to the border between two codes that an exponential of -g log2(e)
+    rounded to float32 takes the other one, but 10 roundings of float32 away from it.  Codes [128, 3] of both, and how many
+    those are."""
+    small = np.array([*range(16), *range(16, 32, 2), *range(32, 64, 4)], np.float64)
+    g3 = np.stack([np.full(n, float(a)), rng.choice(small, n), rng.choice(small, n)], 1)
+    u3 = np.stack([rng.choice(np.arange(8.0, 15.0), n), rng.choice(small[:24], n), rng.choice(small[:24], n)], 1) * 2.0 ** k
+    g3[0], u3[0] = (a, 0, 0), (15 * 2.0 ** k, 30 * 2.0 ** k, 30 * 2.0 ** k)
+    parts = np.array([1, 2.0 ** -4, 2.0 ** -8])
+    g, u = -(g3 @ parts), u3 @ parts
+    v = np.abs(g / (1 + np.exp(-g)) * u)
+    m = v / 2.0 ** np.floor(np.log2(v))                      # borders: 1 + odd sixteenths
+    border = 1 + (2 * np.clip(np.floor((m - 1) * 8), 0, 7) + 1) / 16
+    r = m / border - 1
+    t = (-g).astype(np.float32) * np.float32(np.log2(np.e))  # what a float32 product makes of the exponent
+    shift = (t.astype(np.float64) + g * np.log2(np.e)) * np.log(2)
+    clear = np.abs(r) > 10 * U
+    clear &= np.abs(m - 1) > 2.0 ** -8                       # a power of two has borders of two distances
+    other = clear & (np.sign(r - shift) != np.sign(r)) & (np.abs(r - shift) > 8 * U)
+    other[0] = False
+    at = np.flatnonzero(other)[:100]
+    rest = np.flatnonzero(clear & ~other & (np.abs(r) > 2.0 ** -10))
+    at = np.concatenate([[0], at, rest[rest > 0][:127 - len(at)]])
+    assert 448 / 256 * 0.99 > m[0] > 1.01 and (v[at[1:]] < v[0]).all() and (v[at] > v[0] / 2.0 ** 13).all()
+    return -g3[at], u3[at], int(other[at].sum())
+
+
+@pytest.mark.parametrize("T", [6, 24, 60, 240])
+def test_ffn_activation_next_to_borders(T):
+    """silu(g) u within 8 roundings of float32 for gates far below zero, in every way of a call: values closer than
+    2^-18 to the border between two codes, and farther than 10 roundings from it, get the code of their own side.  Every
+    product before and behind the activation is exact."""
+    say("activation", T)
+    rng = np.random.default_rng(77)
+    levels = [(48, 70), (52, 76), (56, 82), (60, 87), (64, 93), (72, 105)]
+    H, I, nb = 128 * len(levels), 128, len(levels)
+    w13, x = np.zeros((1, H, 2 * I)), np.zeros((T, H))
+    want, near = np.zeros((nb, I)), 0
+    for b, (a, k) in enumerate(levels):
+        g3, u3, n = _next_to_borders(rng, a, k)
+        rows = b * 128 + rng.permutation(128)[:3]
+        w13[0, rows, :I], w13[0, rows, I:] = g3.T, u3.T
+        x[b::nb, rows] = 1, 2.0 ** -4, 2.0 ** -8
+        g, u = (c @ np.array([1, 2.0 ** -4, 2.0 ** -8]) for c in (g3, u3))
+        want[b] = G.round_rows((g / (1 + np.exp(-g)) * u)[None])[0]
+        near += n
+    assert near > 50
+    w2 = np.zeros((1, I, H))
+    w2[0, np.arange(I), np.arange(I)] = 1
+    np.testing.assert_array_equal(_values(_bits(w13)), w13)  # held exactly in 8 bits
+    p = _quantized(_bits(w13)), _quantized(_bits(w2))
+    out = f64_of(_run_ffn(np.zeros((T, 1), np.int32), np.ones((T, 1), np.float32), _bits(x), *p, 1, H, I))
+    assert not out[:, I:].any()
+    np.testing.assert_array_equal(out[:, :I], want[np.arange(T) % nb])
+
+
+@pytest.mark.parametrize("T", [6, 24, 60, 240])
+def test_ffn_gates_of_any_size(T):
+    """Gates up to the largest numbers of either sign: silu(g) is g or next to nothing; one that overflows is a block of NaN."""
+    say("large gates", T)
+    H, I = 384, 128
+    sizes = np.array([88, 96, 104, 120, 144, 240]), np.array([1, 1.75, 1.5, 1.125]) * 2.0 ** 127
+    w13, x, want = np.zeros((1, H, 2 * I)), np.zeros((T, H)), np.zeros((2, I))
+    for b in range(2):
+        g = np.resize(np.concatenate([sizes[b], -sizes[b]]), I)
+        w13[0, 128 * b + 5, :I], w13[0, 128 * b + 5, I:] = g, (1, 2.0 ** -100)[b]
+        x[b::3, 128 * b + 5] = 1
+        want[b] = G.round_rows((np.maximum(g, 0) * (1, 2.0 ** -100)[b])[None])[0]
+    w13[0, 300, 7], w13[0, 301, 7], w13[0, 300, I + 7] = 2.0 ** 127, 2.0 ** 127, 1
+    x[2::3, 300:302] = 1                                     # a gate of 2^128 in float32
+    w2 = np.zeros((1, I, H))
+    w2[0, np.arange(I), np.arange(I)] = 1
+    p = _quantized(_bits(w13)), _quantized(_bits(w2))
+    out = f64_of(_run_ffn(np.zeros((T, 1), np.int32), np.ones((T, 1), np.float32), _bits(x), *p, 1, H, I))
+    for b in range(2):
+        assert (out[b::3, :I] == want[b]).all() and not out[b::3, I:].any()
+    assert np.isnan(out[2::3]).all()
