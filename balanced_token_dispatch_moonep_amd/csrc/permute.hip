@@ -319,6 +319,12 @@ static void launch_combine_backward(int K, hipStream_t s, const int32_t* dest, c
     else go(std::integral_constant<int, 14>{});
 }
 
+// Whether a launch has a wave for each of n tokens or rows: its lanes are counted in 32 bits.
+constexpr long long kMostWaves = (1ll << 26) - kWavesPerBlock;
+static bool waves_fit(const moonep_dims_t* d, int rows_a_token) {
+    return (long long)d->R * d->S * rows_a_token <= kMostWaves;
+}
+
 }  // namespace moonep
 
 using namespace moonep;
@@ -327,6 +333,7 @@ extern "C" int moonep_dispatch(const moonep_dims_t* dims, const int32_t* dest, c
                                const float* row_scale, void* recv, void* stream) {
     const int rc = check_row_dims(dims);
     if (rc != MOONEP_OK) return rc;
+    if (!waves_fit(dims, 1)) return MOONEP_ENOTSUP;
     MOONEP_CHECK_PTR(dest);
     MOONEP_CHECK_PTR(src);
     MOONEP_CHECK_PTR(recv);
@@ -354,6 +361,7 @@ extern "C" int moonep_combine(const moonep_dims_t* dims, const int32_t* dest, co
                               const float* gates, void* out, void* stream) {
     const int rc = check_row_dims(dims);
     if (rc != MOONEP_OK) return rc;
+    if (!waves_fit(dims, 1)) return MOONEP_ENOTSUP;
     MOONEP_CHECK_PTR(dest);
     MOONEP_CHECK_PTR(y);
     MOONEP_CHECK_PTR(out);
@@ -381,6 +389,7 @@ extern "C" int moonep_dispatch_staged(const moonep_dims_t* dims, const int32_t* 
                                       const float* row_scale, void* stage, void* recv, void* stream) {
     const int rc = check_dims(dims, false);
     if (rc != MOONEP_OK) return rc;
+    if (!waves_fit(dims, dims->K)) return MOONEP_ENOTSUP;
     MOONEP_CHECK_PTR(dest);
     MOONEP_CHECK_PTR(src);
     MOONEP_CHECK_PTR(stage);
@@ -415,6 +424,7 @@ extern "C" int moonep_combine_staged(const moonep_dims_t* dims, const int32_t* d
                                      const float* gates, void* stage, void* out, void* stream) {
     const int rc = check_dims(dims, false);
     if (rc != MOONEP_OK) return rc;
+    if (!waves_fit(dims, dims->K)) return MOONEP_ENOTSUP;
     MOONEP_CHECK_PTR(dest);
     MOONEP_CHECK_PTR(y);
     MOONEP_CHECK_PTR(stage);

@@ -156,7 +156,8 @@ int moonep_prefetch(const moonep_dims_t* dims, const void* plan_ws,
                     void* w13_slot, void* w2_slot, void* stream);
 
 /* Fused zero-copy permute [TC, "What the technique is"; AL, How it works; TD, architecture]:
- * recv[dest[r,s,k]] = src[r,s] for every (token, k).
+ * recv[dest[r,s,k]] = src[r,s] for every (token, k).  Only R, S, K (1 to 16), H and the row type of dims matter, so
+ * that rows of moonep_sort move too, whatever E is; MOONEP_ENOTSUP over 2^26 - 4 tokens.
  *   src  [R, S, H] bf16 (float32 with MOONEP_F32_ROWS)
  *   row_scale [R, S, K] float32 or NULL.  NULL: bitwise copy.  Otherwise each copy is
  *        multiplied by its scale in float32 and rounded to nearest even (the backward of a
@@ -166,7 +167,7 @@ int moonep_dispatch(const moonep_dims_t* dims, const int32_t* dest, const void* 
                     const float* row_scale, void* recv, void* stream);
 
 /* Fused unpermute [TC, flowchart "combine"]: out[r,s] = sum over k (in k order, float32
- * accumulation) of gates[r,s,k] * y[dest[r,s,k]], rounded to nearest even.
+ * accumulation) of gates[r,s,k] * y[dest[r,s,k]], rounded to nearest even.  The same of dims matters.
  *   y     [R*S*K, H] bf16 (float32 with MOONEP_F32_ROWS)
  *   gates [R, S, K] float32, or NULL for unit weights (the backward of dispatch)
  *   out   [R, S, H] out, same element type as y. */
@@ -179,6 +180,7 @@ int moonep_combine(const moonep_dims_t* dims, const int32_t* dest, const void* y
  * sort-copy then moves them to their expert-grouped rows, recv[dest[p]] = stage[p].  Combine
  * mirrors it: stage[p] = y[dest[p]], then out[r, s] = sum over k of gates * stage[(r, s, k)].
  * Results are bit-identical to moonep_dispatch / moonep_combine; every row crosses HBM twice more.
+ * The planner's limits on dims apply to these two; MOONEP_ENOTSUP over 2^26 - 4 (token, k) pairs.
  *   stage [R*S*K, H] scratch of the row type (contents on return: the arrival-order rows)
  *   other arguments as for moonep_dispatch / moonep_combine. */
 int moonep_dispatch_staged(const moonep_dims_t* dims, const int32_t* dest, const void* src,

@@ -244,3 +244,16 @@ def test_layer_refuses():
         r.backward(torch.zeros(1, 3, 2))
     with pytest.raises(ValueError, match="forward"):
         L.Router(d, training=True, device="cpu").backward(torch.zeros(1, 3, 2))
+
+
+def test_rows_of_more_tokens_than_a_launch_has_waves():
+    """A wave a token, and in the staged calls a wave a (token, k) pair; lanes are counted in 32 bits.  Every call has a
+    misaligned pointer, so that nothing is enqueued where the sizes pass."""
+    most = (1 << 26) - 4
+    for fn, names, rows in (("moonep_dispatch", ("dest", "src", "scale", "recv"), 1),
+                            ("moonep_combine", ("dest", "y", "gates", "out"), 1),
+                            ("moonep_dispatch_staged", ("dest", "src", "scale", "stage", "recv"), 8),
+                            ("moonep_combine_staged", ("dest", "y", "gates", "stage", "out"), 8)):
+        call = _caller(fn, names)
+        for n, code in ((most // rows, EALIGN), (most // rows + 1, ENOTSUP), (1 << 26, ENOTSUP)):
+            assert call(_dims(S=n, K=rows, H=8), dest=FAR * 50 + 4) == code
