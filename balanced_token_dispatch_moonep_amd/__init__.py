@@ -55,7 +55,9 @@ STAT_NAMES = (
 )
 NOALLOC_WS_BYTES = 8 << 20     # static plan workspace of moonep_plan_noalloc, per GPU
 W4_MAX_PAIRS = 8192            # (token, k) pairs of one moonep_w4_ffn call, at most
-FP8_MAX_PAIRS = 1 << 22        # (token, k) pairs of one moonep_fp8_ffn call, at most
+# (token, k) pairs of one moonep_fp8_ffn call, at most.  Its tokens, H padded to a multiple of 128, are also held to
+# 0xffff0000 bytes of a byte a value, and H and I to 2^20.
+FP8_MAX_PAIRS = 1 << 22
 # gates of moonep_route: over the picked logits, over all E, or sigmoids divided by their sum
 ROUTE_SOFTMAX, ROUTE_SOFTMAX_ALL, ROUTE_SIGMOID = 0, 1, 2
 _ROUTE_BF16 = 16
@@ -720,7 +722,8 @@ def _fp8_shapes(dims: bytes):
 
 def moonep_fp8_ffn(d: Dims, topk, gates, x, w13_codes, w13_scales, w2_codes, w2_scales, ws, out, stream=None) -> None:
     """out [R, S, H] = the gated sum of each token's experts' FFN, weights and rows in 8 bits
-    (moonep_quantize_fp8 of w13 [E, H, 2I] and w2 [E, I, H]).  Ids outside [0, E) add nothing."""
+    (moonep_quantize_fp8 of w13 [E, H, 2I] and w2 [E, I, H]).  Ids outside [0, E) add nothing.  A token's bits depend on
+    it and on the kind of call that dims make (few pairs, up to 36 pairs an expert, more), whose sums differ in accuracy."""
     torch = _torch()
     u8, bf = torch.uint8, torch.bfloat16
     picks, rows, c13, s13, c2, s2, wsb = _fp8_shapes(bytes(d))

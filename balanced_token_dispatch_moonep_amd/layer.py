@@ -366,7 +366,11 @@ class W4Experts(_Experts):
 
 
 class Fp8Experts(_Experts):
-    """Experts for decoding and for prompts, weights and rows in 8 bits, a scale for each block of 128."""
+    """Experts for decoding and for prompts, weights and rows in 8 bits, a scale for each block of 128.
+
+    A token's bits do not depend on the others of its call, but on how many those are: up to 8 tokens (and 64 pairs), up
+    to 36 (token, k) pairs an expert, and more are computed in different ways.  The last is the fastest one, with sums
+    in the 8-bit matrix instruction, which are good to some 16 bits instead of 24."""
 
     def _bytes(self, kin, n):
         return moonep_fp8_code_bytes(kin, n), moonep_fp8_scale_bytes(kin, n)

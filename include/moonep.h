@@ -408,10 +408,10 @@ int moonep_sort(const moonep_dims_t* dims, const int32_t* topk, void* ws, int32_
 int moonep_combine_backward(const moonep_dims_t* dims, const int32_t* dest, const void* y, const float* gates,
                             const void* dout, void* dy, float* dgates, void* stream);
 
-/* 8-bit weights.  A matrix [Kin, N] (multiples of 32 both) is held as e4m3 codes (OCP FP8: no infinities) and one
- * scale byte s, worth 2^(s - 127), for each block of 128 x 128.  Powers of two, because the matrix instruction
- * applies those itself.  Layout, chosen so that a wave's 16-byte loads are one KiB in a row and each lane gets 16 input
- * values of one column:
+/* 8-bit weights.  A matrix [Kin, N] (multiples of 32 both, Kin to 2^20, N to 2^21) is held as e4m3 codes (OCP FP8: no
+ * infinities) and one scale byte s, worth 2^(s - 127), for each block of 128 x 128.  Powers of two, because the matrix
+ * instruction applies those itself.  Layout, chosen so that a wave's 16-byte loads are one KiB in a row and each lane
+ * gets 16 input values of one column:
  *   codes  [N/32][ceil(Kin/128)][8 pieces][32 columns][16 bytes along Kin]; codes past Kin are 0
  *   scales [ceil(N/128)][ceil(Kin/128), padded to a multiple of 4]; scales past Kin are 127
  * These give one matrix's bytes; 0 for invalid sizes. */
@@ -427,19 +427,27 @@ int moonep_quantize_fp8(int32_t E, int32_t Kin, int32_t N, const void* w, void* 
 /* The experts' SwiGLU FFN with 8-bit weights, from one decoded token to whole prompts:
  *   out[r,s] = sum over k (in k order) of gates[r,s,k] * (q(silu(q(x) G) * (q(x) U)) D)  of expert topk[r,s,k],
  * G | U the columns of its w13, D its w2.  q rounds a row to e4m3 as the weights are, with a scale for each 128
- * values along it; a block with an infinity or a NaN is NaN.  Products in matrix instructions with float32
- * accumulation; the result is rounded to nearest even once.  In calls of more than a few pairs an expert's output is
- * rounded to float16 too, with a power of two for each 64 columns, before it is weighted.  Needs no plan: dims' R, S,
- * K, E, H and I count, the planner's limits on E/R and B do not apply.  An output depends on its own token only, and
- * on dims.
+ * values along it; a block with an infinity or a NaN is NaN.  Values that q takes to 2^128 may count as infinite,
+ * magnitudes that it leaves below 2^-126 as 0.  The result is rounded to nearest even once; what comes before it is
+ * chosen by dims alone, in three kinds of calls:
+ *   - few pairs (R*S to 8, R*S*K to 64, H to 8192): products with float32 sums;
+ *   - up to 36 pairs an expert (R*S*K < 36 E): products with float32 sums, an expert's output rounded to float16, with a
+ *     power of two for each 64 columns, before it is weighted;
+ *   - more: the same with the 8-bit matrix instruction, whose sums are off by up to about 2^-15 of their terms'
+ *     magnitudes (2^-16 measured), so that more values next to the border of two codes take the other one.  Outputs are
+ *     off by 0.0019 to 0.0024 of their size as a whole, where they are by 0.0017, bf16's own rounding, in the calls
+ *     before (H 7168, I 2048, 8 experts a token).
+ * So a token's output depends on that token and on dims only: the same bits in all calls of a kind, other last bits in
+ * another kind.  Needs no plan: dims' R, S, K, E, H and I count, the planner's limits on E/R and B do not apply.
  *   topk  [R, S, K] int32: an id outside [0, E) adds nothing, whatever its gate (rows of ended
  *         sequences: all ids -1, their output is zero); an id named twice counts twice
  *   gates [R, S, K] float32;  x [R, S, H] bf16;  out [R, S, H] bf16 out
  *   w13_codes, w13_scales: E matrices [H, 2I];  w2_codes, w2_scales: E matrices [I, H]
  *   ws    moonep_fp8_ffn_workspace_bytes() bytes, scratch (same rules as above)
  * out and ws must not overlap inputs or each other (MOONEP_EINVAL).
- * MOONEP_ENOTSUP if H or I is not a multiple of 32, with MOONEP_F32_ROWS, or if R*S*K is more than
- * MOONEP_FP8_MAX_PAIRS. */
+ * MOONEP_ENOTSUP if H or I is not a multiple of 32 or more than 2^20, with MOONEP_F32_ROWS, if R*S*K is more than
+ * MOONEP_FP8_MAX_PAIRS, or if the R*S rows of x, a byte a value and H padded to a multiple of 128, are more than
+ * 0xffff0000 bytes (599,177 tokens of H 7168). */
 #define MOONEP_FP8_MAX_PAIRS (1 << 22)
 size_t moonep_fp8_ffn_workspace_bytes(const moonep_dims_t* dims);
 int moonep_fp8_ffn(const moonep_dims_t* dims, const int32_t* topk, const float* gates, const void* x,
