@@ -1001,3 +1001,74 @@ def test_ffn_gates_of_any_size(T):
     for b in range(2):
         assert (out[b::3, :I] == want[b]).all() and not out[b::3, I:].any()
     assert np.isnan(out[2::3]).all()
+
+
+def _exact_many(topk, E, H, I, seed):
+    """The call's output and the definition's, bit for bit, for many experts: as in test_ffn_exact one value a row, one a
+    column of w2 and large gates, so that every sum of a product has one term; gates that are powers of two, and a token's
+    pairs added in k order in float32."""
+    T, K = topk.shape
+    rng = np.random.default_rng(seed)
+    blocks = lambda n, lo, hi: np.repeat(2.0 ** rng.integers(lo, hi, -(-n // 128)), 128)[:n].astype(np.float32)
+    pick = lambda values, *shape: np.array(values, np.float32)[rng.integers(0, len(values), shape, dtype=np.int8)]
+    at, val = rng.integers(0, H, T), pick([1, 1.5, 2, 3.5], T) * 2.0 ** rng.integers(0, 3, T)
+    x = np.zeros((T, H), np.float32)
+    x[np.arange(T), at] = val
+    w13 = np.empty((E, H, 2 * I), np.float32)
+    gate = 64 * blocks(H, 0, 3)
+    w13[:, :, :I] = gate[:, None]
+    w13[:, :, I:] = pick([-2, -1, 0, 1, 1.5], E, H, I) * (blocks(H, -2, 3)[:, None] * blocks(I, -4, 4))
+    from_i, w2_value = rng.integers(0, I, (E, H)), pick([-1, 1, 1.25], E, H) * blocks(H, -3, 3)
+    w2 = np.zeros((E, I, H), np.float32)
+    w2_value = w2_value * blocks(I, -3, 3)[from_i]
+    np.put_along_axis(w2, from_i[:, None], w2_value[:, None], 1)
+    gates = pick([0.25, 0.5, 1, 2], T, K)
+    want = np.zeros((T, H), np.float32)
+    for k in range(K):
+        on = np.flatnonzero((topk[:, k] >= 0) & (topk[:, k] < E))
+        e = topk[on, k]
+        a = (val[on] * gate[at[on]])[:, None] * (val[on][:, None] * w13[e, at[on], I:])
+        y = np.take_along_axis(G.round_rows(a), from_i[e], 1) * w2_value[e]
+        want[on] += (gates[on, k, None] * y).astype(np.float32)
+    out = _run_ffn(topk, gates, _bits(x), _quantized(_bits(w13)), _quantized(_bits(w2)), E, H, I)
+    return f64_of(out), W.bf16_to_f32(_bits(want))
+
+
+def _tiles(topk, E, H, I):
+    """Tiles of the two products of a call, and the rows of one."""
+    n = np.bincount(topk[(topk >= 0) & (topk < E)], minlength=E)
+    rows = 64 if topk.size < 36 * E else 128 if topk.size < 192 * E else 256
+    runs = int((-(-n // rows)).sum())
+    return runs * -(-I // 128), runs * -(-H // 256), rows, n
+
+
+# More tiles than workgroups in both products, of more stages than the ring holds: each workgroup goes on to further tiles,
+# full ones and those that end early, in rows and in columns, after each other.
+@pytest.mark.parametrize("E,H,I,rows,sizes", [
+    (128, 544, 416, 64, (128, 64, 65, 100, 3, 1, 0, 2, 3, 3, 4, 2)),
+    (64, 800, 544, 128, (128, 256, 1, 140, 129, 40, 0, 127)),
+    (56, 800, 544, 256, (256, 512, 1, 300, 257, 30, 0, 255)),
+])
+def test_ffn_exact_many_tiles(E, H, I, rows, sizes):
+    rng = np.random.default_rng(E)
+    topk = np.concatenate([np.full(sizes[e % len(sizes)], e) for e in range(E)] + [np.full(50, -1)])
+    topk = rng.permutation(topk).astype(np.int32)[:, None]
+    up, down, of, n = _tiles(topk, E, H, I)
+    say("exact, many tiles", len(topk), E, H, I, up, down, of)
+    assert of == rows and up > 300 and down > 256 and (n == rows).any() and (n % rows > 0).any()
+    assert -(-H // 128) > 3 and -(-I // 128) > 3 and H >= 512 and H % 256
+    got, want = _exact_many(topk, E, H, I, E)
+    np.testing.assert_array_equal(got, want)
+
+
+# the join of 4096 tokens and more, seven pieces of 512 columns a wave: several pairs a token, some without an expert, rows
+# of less than a piece, of several, and of more than seven
+@pytest.mark.parametrize("T,K,E,H,I", [(4096, 3, 5, 64, 32), (4099, 8, 40, 1056, 32), (4097, 2, 3, 3616, 32)])
+def test_ffn_exact_joins_of_many_tokens(T, K, E, H, I):
+    say("exact, joins", T, K, E, H, I)
+    rng = np.random.default_rng(H)
+    topk = rng.integers(-1, E + 1, (T, K)).astype(np.int32)  # an id may repeat
+    topk[T // 2] = -1
+    got, want = _exact_many(topk, E, H, I, H)
+    np.testing.assert_array_equal(got, want)
+    assert not got[T // 2].any()
