@@ -245,12 +245,12 @@ __global__ __launch_bounds__(256) void permute_rows_kernel(const int32_t* __rest
 }
 
 // The gradient of the weighted combine, one wave per token: dy[dest[p]] = g * dout[token(p)] as dispatch with a
-// row scale, and dgates[p] = <dout[token(p)], y[dest[p]]> in float32, so dout is read from memory once for both.
+// row scale, and dgates[p] = <dout[token(p)], y[dest[p]]> in float32, from one load of dout.
 // DY, DG: which of the two are wanted.  The K rows are taken one after another, as in combine_kernel, VB vectors a
 // lane of y and of dout at a time; every lane adds its own products first, then the wave joins them: the same
 // order for all rows of a length.
 // What bounds it is memory, a read and a write of each row: 4096 tokens of 8 rows of 7168 bf16 (1.0 GB) take 194 us,
-// 5.1 TB/s, where a large copy reaches 4.9.  With dout kept in registers for all rows 198 us (half as many waves),
+// 5.1 TB/s, where a large copy reaches 4.9 to 5.3 (with what comes of dout from memory more than once, 1.17 GB).  With dout kept in registers for all rows 198 us (half as many waves),
 // with ordinary stores 211, with 7 vectors at a time 200.
 template <bool F32, bool GATES, bool DY, bool DG, int VB>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const int32_t* __restrict__ dest,

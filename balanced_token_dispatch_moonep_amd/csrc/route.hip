@@ -9,9 +9,9 @@
 // A sum of sigmoids that underflows is no division by zero this way: s_k / sum s = softmax(log s)_k.
 //
 // What bounds it is ranking.  Without a bias each lane sorts its best K and the K heads are compared across lanes:
-// 32768 rows of 256 float32 take 11.4 us for K 8 and 15.6 for K 16 in a graph, of which reading them is 6; K times a
-// maximum over all elements took 17.1 and 25.5.  With a bias keys are doubles and are ranked that way, and a sigmoid in
-// float64 comes before it: 37.5 us.
+// 32768 rows of 256 float32 take 11.5 us for K 8 and 16.0 for K 16 in a graph with logits from memory, of which reading
+// them is 5 to 6 (9.7 and 13.3 where the last-level cache holds them); K times a maximum over all elements took 17.1
+// and 25.5.  With a bias keys are doubles and are ranked that way, and a sigmoid in float64 comes before it: 33 to 37 us.
 //
 // Sixteen lanes share a row, so that four rows go through a wave and every step across lanes is a rotation
 // inside 16 lanes, an operand modifier instead of an instruction through LDS.  Where rows are too few to fill the

@@ -409,8 +409,8 @@ int moonep_combine_backward(const moonep_dims_t* dims, const int32_t* dest, cons
                             const void* dout, void* dy, float* dgates, void* stream);
 
 /* 8-bit weights.  A matrix [Kin, N] (multiples of 32 both, Kin to 2^20, N to 2^21) is held as e4m3 codes (OCP FP8: no
- * infinities) and one scale byte s, worth 2^(s - 127), for each block of 128 x 128.  Powers of two, because the matrix
- * instruction applies those itself.  Layout, chosen so that a wave's 16-byte loads are one KiB in a row and each lane
+ * infinities) and one scale byte s, worth 2^(s - 127), for each block of 128 x 128 (0 and 255 are not used).  Powers of
+ * two, because the matrix instruction applies those itself.  Layout, chosen so that a wave's 16-byte loads are one KiB in a row and each lane
  * gets 16 input values of one column:
  *   codes  [N/32][ceil(Kin/128)][8 pieces][32 columns][16 bytes along Kin]; codes past Kin are 0
  *   scales [ceil(N/128)][ceil(Kin/128), padded to a multiple of 4]; scales past Kin are 127
